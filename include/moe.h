@@ -404,6 +404,144 @@ moe_status_t moe_fused_path(const moe_fused_args_t* args, int32_t* path);
 #define MOE_NOALLOC_SCRATCH_BYTES ((size_t)64 << 20)
 moe_status_t moe_fused_forward_noalloc(const moe_fused_args_t* args, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Expert products as operators of their own, on rows grouped by expert, with
+ * their gradients; 4-bit experts for few tokens; and the gated activation
+ * with its inputs kept in 8 bits for the backward pass.  Together they are
+ * the expert half of a layer's training step, and its serving form with
+ * 4-bit weights; moe_route_topk and moe_align produce the grouping they read.
+ *
+ * Conventions, besides those at the top:
+ *  - Grouped rows: row i, 0 <= i < R, belongs to the expert e with
+ *    offsets[e] <= i < offsets[e+1].  offsets is int32 [E+1] on the device,
+ *    non-decreasing (moe_align's expert_offsets, padded or, with block 1,
+ *    not); the kernels clamp its values into [0,R], so a wrong one cannot
+ *    lead outside a buffer.  R is the host's bound (moe_align_capacity);
+ *    rows at or beyond offsets[E] are neither read nor written.
+ *  - A rows operand (moe_rows_t) is a bf16 matrix of `rows` rows with a row
+ *    stride in elements, and optionally ids: grouped row i is then row
+ *    ids[i]/div of the matrix (ids = moe_align's sorted_ids, div = top_k:
+ *    the token of a pair).  An input row whose id is negative or ids[i]/div
+ *    >= rows reads as zeros (sorted_ids' sentinel); an output row with such
+ *    an id is not written.  With ids NULL grouped row i is row i and rows
+ *    must be >= R.  Two output ids that are equal leave either row's result.
+ *  - Every result is a sum in fp32 in an order fixed by the sizes and the
+ *    row's own expert count, rounded once to the output's type: the same
+ *    bits on every call.  There are no atomics and no workspace.
+ *  - MOE_ERR_INVALID_ARG: NULL or misaligned pointers (16 bytes; 4 for int32
+ *    and fp32 vectors), negative sizes, div < 1, a stride below the width or
+ *    not a multiple of 16 bytes, rows < R without ids, an unknown type.
+ *    MOE_ERR_UNSUPPORTED: E > 512, N or K not a multiple of 8 (4-bit weights:
+ *    K not a multiple of the scale group), an expert's matrix of 2^31 bytes
+ *    or more, a row stride of 2^20 elements or more, and, for an input with
+ *    ids, a matrix of 2^32 - 256 bytes or more.
+ *  - Outputs must not overlap inputs or each other.
+ */
+typedef struct {
+  void* data;          /* [rows, width], row i at data + i*stride elements */
+  int64_t stride;      /* elements */
+  int32_t rows;
+  int32_t div;         /* >= 1; ids[i]/div is the matrix row (outputs: must be 1) */
+  const int32_t* ids;  /* [R] or NULL */
+} moe_rows_t;
+
+typedef enum {
+  MOE_OUT_BF16 = 0,
+  MOE_OUT_FP32 = 1,
+  MOE_OUT_RANGE_LO_ = -2147483647 - 1,
+  MOE_OUT_RANGE_HI_ = 2147483647
+} moe_out_t;
+
+typedef enum {
+  MOE_WEIGHT_BF16 = 0,
+  MOE_WEIGHT_MXFP4 = 1, /* e2m1 codes, one E8M0 scale per 32 along K (OCP MXFP4) */
+  MOE_WEIGHT_INT4 = 2,  /* codes q of 0..15 standing for q - 8, one bf16 scale per 128 along K */
+  MOE_WEIGHT_RANGE_LO_ = -2147483647 - 1,
+  MOE_WEIGHT_RANGE_HI_ = 2147483647
+} moe_weight_t;
+
+/*
+ * Grouped product: out[i] = W[e] in[i] for every grouped row i of expert e,
+ * W [E,N,K] row-major, in of width K, out of width N.
+ * 4-bit weights: two codes per byte along K, the low nibble first, rows of
+ * K/2 bytes; w_scale E8M0 [E,N,K/32] (codes 2..252, under which every weight
+ * is zero or a normal bf16) or bf16 [E,N,K/128].  The weights' values are exact
+ * in the product: scales are powers of two in bf16 range (MXFP4), or applied
+ * in fp32 to each group's sum (INT4).  4-bit weights are streamed once per 64
+ * rows of an expert: the form for decoding.  bf16 weights take a streaming or
+ * a tiled kernel by the mean number of rows per expert.
+ */
+typedef struct {
+  int32_t R, E, N, K;
+  const int32_t* offsets; /* [E+1] */
+  moe_rows_t in;
+  moe_weight_t weight;
+  const void* w;
+  const void* w_scale;    /* 4-bit weights; NULL for bf16 */
+  moe_rows_t out;         /* bf16 or fp32 */
+  moe_out_t out_type;
+} moe_grouped_args_t;
+
+moe_status_t moe_grouped_gemm(const moe_grouped_args_t* args, void* stream);
+
+/*
+ * Gradient of the grouped product's input: out[i] = W[e]^T in[i], in of width
+ * N (the output's gradient), out of width K.  bf16 weights only
+ * (MOE_ERR_UNSUPPORTED otherwise).
+ */
+moe_status_t moe_grouped_gemm_dgrad(const moe_grouped_args_t* args, void* stream);
+
+/*
+ * Gradient of the weights: dw[e] = sum over expert e's rows i of
+ * dy[i] in[i]^T, [E,N,K] row-major, dy of width N, in of width K; zero for an
+ * expert without rows.  accumulate 1 (fp32 only, else MOE_ERR_INVALID_ARG):
+ * dw[e] += that sum; experts without rows are then left as they were.
+ */
+typedef struct {
+  int32_t R, E, N, K;
+  const int32_t* offsets; /* [E+1] */
+  moe_rows_t dy;
+  moe_rows_t in;
+  void* dw;
+  moe_out_t out_type;
+  int32_t accumulate;
+} moe_grouped_wgrad_args_t;
+
+moe_status_t moe_grouped_gemm_wgrad(const moe_grouped_wgrad_args_t* args, void* stream);
+
+/*
+ * Gated activation with an 8-bit checkpoint.  gu [R,2I] bf16 (columns [0,I)
+ * gate, [I,2I) up, row stride gu_stride), row_weight fp32 [R] or NULL (ones):
+ *   h[i] = bf16( row_weight[i] * SiLU(g) * u )                  [R,I]
+ *   codes [R,2I] e4m3 and scales [R,2,ceil(I/32)] E8M0: every 32 consecutive
+ *   values of a row's gate half and up half share the smallest power of two
+ *   under which the largest finite magnitude does not pass 448; each value is
+ *   rounded to nearest even under it.  NaN and infinities become the NaN code
+ *   0x7f.
+ * codes and scales are both NULL (h only) or both given; h may be NULL
+ * with them given.  num_rows: device int32 or NULL; rows at or beyond
+ * *num_rows (offsets + E of a padded grouping) are neither read nor written.
+ * row_weight multiplies h before its one rounding, so that the down product's
+ * results need only be added up per token.
+ * I a multiple of 8 below 2^19, R*I below 2^38, gu_stride below 2^20 (else
+ * MOE_ERR_UNSUPPORTED); gu, h and codes 16-byte aligned.
+ */
+moe_status_t moe_swiglu_checkpoint(const void* gu, int64_t gu_stride, const float* row_weight, int32_t R, int32_t I,
+                                   const int32_t* num_rows, void* h, uint8_t* codes, uint8_t* scales, void* stream);
+
+/*
+ * Its gradient, from the checkpoint: with g, u the values that codes and
+ * scales stand for, s = 1/(1+exp(-g)), w = row_weight[i] (or 1), dh [R,I]
+ * bf16 the gradient of h:
+ *   dgu[i] = bf16( w*dh*u*s*(1+g*(1-s)) , w*dh*g*s )              [R,2I]
+ *   h[i]   = bf16( w*g*s*u ), the activation again for the down product's
+ *            weight gradient; NULL = not wanted                   [R,I]
+ *   dweight[i] = sum over the row of dh*g*s*u, fp32; NULL = not wanted [R]
+ */
+moe_status_t moe_swiglu_checkpoint_grad(const uint8_t* codes, const uint8_t* scales, const void* dh,
+                                        const float* row_weight, int32_t R, int32_t I, const int32_t* num_rows,
+                                        void* dgu, void* h, float* dweight, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -17,7 +17,8 @@ import torch
 __all__ = [
     "MoEError", "load", "LIB_PATH", "route_topk", "router_logits", "align_capacity", "align", "quant_e4m3",
     "workspace_size", "fused_align_shape", "fused_forward", "Tuning", "STATUS", "NUM_STAGES", "STAGE_NAMES",
-    "NOALLOC_SCRATCH_BYTES", "fused_path", "PATH_NAMES",
+    "NOALLOC_SCRATCH_BYTES", "fused_path", "PATH_NAMES", "grouped_gemm", "grouped_gemm_dgrad", "grouped_gemm_wgrad",
+    "grouped_gemm_w4", "swiglu_checkpoint", "swiglu_checkpoint_grad", "CHECKPOINT_GROUP", "W4_GROUP",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libmoe_mi355x.so")
@@ -27,6 +28,8 @@ STATUS = {0: "MOE_OK", 1: "MOE_ERR_INVALID_ARG", 2: "MOE_ERR_UNSUPPORTED", 3: "M
 DTYPE_BF16, DTYPE_FP8 = 0, 1
 NUM_STAGES = 5
 NOALLOC_SCRATCH_BYTES = 64 << 20  # MOE_NOALLOC_SCRATCH_BYTES
+CHECKPOINT_GROUP = 32  # values per scale of an 8-bit activation checkpoint
+W4_GROUP = {"mxfp4": 32, "int4": 128}  # weights per scale along K of the 4-bit formats
 STAGE_NAMES = ("route", "align", "gate_up", "down", "finalize")
 # moe_fused_path's MOE_PATH_* values, in order
 PATH_NAMES = ("none", "prefill", "decode", "decode_token_down", "two_launches", "single_launch")
@@ -67,6 +70,23 @@ class _FusedArgs(ctypes.Structure):
     ]
 
 
+class _Rows(ctypes.Structure):  # moe_rows_t
+    _fields_ = [("data", ctypes.c_void_p), ("stride", ctypes.c_int64), ("rows", ctypes.c_int32),
+                ("div", ctypes.c_int32), ("ids", ctypes.c_void_p)]
+
+
+class _GroupedArgs(ctypes.Structure):  # moe_grouped_args_t
+    _fields_ = [("R", ctypes.c_int32), ("E", ctypes.c_int32), ("N", ctypes.c_int32), ("K", ctypes.c_int32),
+                ("offsets", ctypes.c_void_p), ("in_", _Rows), ("weight", ctypes.c_int32), ("w", ctypes.c_void_p),
+                ("w_scale", ctypes.c_void_p), ("out", _Rows), ("out_type", ctypes.c_int32)]
+
+
+class _GroupedWgradArgs(ctypes.Structure):  # moe_grouped_wgrad_args_t
+    _fields_ = [("R", ctypes.c_int32), ("E", ctypes.c_int32), ("N", ctypes.c_int32), ("K", ctypes.c_int32),
+                ("offsets", ctypes.c_void_p), ("dy", _Rows), ("in_", _Rows), ("dw", ctypes.c_void_p),
+                ("out_type", ctypes.c_int32), ("accumulate", ctypes.c_int32)]
+
+
 _lib = None
 _ABI = 15  # moe_abi_version() of the library whose moe_fused_args_t _FusedArgs mirrors
 
@@ -105,6 +125,16 @@ def load():
     lib.moe_fused_path.restype = ctypes.c_int
     lib.moe_fused_path.argtypes = [ctypes.POINTER(_FusedArgs), ctypes.POINTER(i32)]
     lib.moe_fused_forward_noalloc.argtypes = [ctypes.POINTER(_FusedArgs), vp]
+    lib.moe_grouped_gemm.restype = ctypes.c_int
+    lib.moe_grouped_gemm.argtypes = [ctypes.POINTER(_GroupedArgs), vp]
+    lib.moe_grouped_gemm_dgrad.restype = ctypes.c_int
+    lib.moe_grouped_gemm_dgrad.argtypes = [ctypes.POINTER(_GroupedArgs), vp]
+    lib.moe_grouped_gemm_wgrad.restype = ctypes.c_int
+    lib.moe_grouped_gemm_wgrad.argtypes = [ctypes.POINTER(_GroupedWgradArgs), vp]
+    lib.moe_swiglu_checkpoint.restype = ctypes.c_int
+    lib.moe_swiglu_checkpoint.argtypes = [vp, i64, vp, i32, i32, vp, vp, vp, vp, vp]
+    lib.moe_swiglu_checkpoint_grad.restype = ctypes.c_int
+    lib.moe_swiglu_checkpoint_grad.argtypes = [vp, vp, vp, vp, i32, i32, vp, vp, vp, vp, vp]
     if lib.moe_abi_version() != _ABI:
         raise RuntimeError("libmoe_mi355x.so has ABI version %d, this binding expects %d: rebuild it"
                            % (lib.moe_abi_version(), _ABI))
@@ -384,3 +414,215 @@ def fused_forward(x: torch.Tensor, logits: Optional[torch.Tensor], w13: torch.Te
         _check("moe_fused_forward_profiled",
                lib.moe_fused_forward_profiled(ctypes.byref(args), _stream(stream), ctypes.cast(arr, ctypes.c_void_p)))
     return out
+
+
+# ------------------------------------------------------------------ grouped products and the checkpointed activation
+class _Call:
+    """The tensors of one call: all on one GPU, whose current stream (or
+    `stream`) it runs on; outputs made here for a side stream are recorded
+    on it."""
+
+    def __init__(self, like: torch.Tensor, stream):
+        if not isinstance(like, torch.Tensor) or like.device.type != "cuda":
+            raise ValueError("the operands must be GPU tensors")
+        self.device, self.given = like.device, stream
+        self.stream = torch.cuda.current_stream(like.device).cuda_stream if stream is None else _stream(stream)
+
+    def need(self, t, name, dtype, shape):
+        _need(t, name, dtype, shape)
+        self.same_device(t, name)
+        return t.data_ptr()
+
+    def same_device(self, t, name):
+        if t.device != self.device:
+            raise ValueError("%s is on %s, the other operands on %s" % (name, t.device, self.device))
+
+    def empty(self, shape, dtype):
+        t = torch.empty(shape, dtype=dtype, device=self.device)
+        if self.given is not None and self.stream != torch.cuda.current_stream(self.device).cuda_stream:
+            t.record_stream(torch.cuda.ExternalStream(self.stream, device=self.device))
+        return t
+
+    def vector(self, t, name, dtype, n):
+        return None if t is None else self.need(t, name, dtype, (n,))
+
+    def rows(self, t, name, dtypes, width, ids, div, R) -> _Rows:
+        """A [rows, width] operand whose rows may be strided, as moe_rows_t."""
+        if not isinstance(t, torch.Tensor) or t.device.type != "cuda":
+            raise ValueError("%s must be a GPU tensor" % name)
+        self.same_device(t, name)
+        if t.dtype not in dtypes:
+            raise TypeError("%s must be %s, got %s" % (name, " or ".join(map(str, dtypes)), t.dtype))
+        if t.dim() != 2 or t.shape[1] != width:
+            raise ValueError("%s must have shape (rows, %d), got %s" % (name, width, tuple(t.shape)))
+        if t.shape[1] > 1 and t.stride(1) != 1:
+            raise ValueError("%s's rows must be contiguous" % name)
+        ptr = None if ids is None else self.vector(ids, name + "'s row ids", torch.int32, R)
+        # one row has no stride of its own, no row at all no address
+        stride = t.stride(0) if t.shape[0] > 1 else width
+        return _Rows(data=t.data_ptr() or 16, stride=stride, rows=t.shape[0], div=div if ptr else 1,
+                     ids=ptr or None)
+
+    def run(self, fn, *args):
+        with torch.cuda.device(self.device):
+            _check(fn, getattr(load(), fn)(*args, self.stream))
+
+
+_OUT_TYPE = {torch.bfloat16: 0, torch.float32: 1}
+
+
+def _grouped(fn, a, w, N, K, offsets, out, in_rows, in_div, out_rows, out_dtype, stream, weight=0, scales=None):
+    call = _Call(a, stream)
+    E = w.shape[0]
+    src, dst = (N, K) if fn == "moe_grouped_gemm_dgrad" else (K, N)
+    off = call.need(offsets, "offsets", torch.int32, (E + 1,))
+    R = a.shape[0] if in_rows is None else in_rows.numel()
+    if out is None:
+        if out_dtype not in _OUT_TYPE:
+            raise TypeError("out_dtype must be torch.bfloat16 or torch.float32")
+        out = call.empty((R, dst), out_dtype)
+    args = _GroupedArgs(
+        R=R, E=E, N=N, K=K, offsets=off, in_=call.rows(a, "input", (torch.bfloat16,), src, in_rows, in_div, R),
+        weight=weight, w=w.data_ptr(), w_scale=None if scales is None else scales.data_ptr(),
+        out=call.rows(out, "out", tuple(_OUT_TYPE), dst, out_rows, 1, R), out_type=_OUT_TYPE[out.dtype])
+    call.run(fn, ctypes.byref(args))
+    return out
+
+
+def _weights(a, w) -> tuple:
+    if not isinstance(w, torch.Tensor) or w.dim() != 3:
+        raise ValueError("the weights must be a tensor [E, N, K]")
+    call = _Call(a, None)
+    call.need(w, "w", torch.bfloat16, w.shape)
+    return w.shape[1], w.shape[2]
+
+
+def grouped_gemm(a: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, out: Optional[torch.Tensor] = None, *,
+                 a_rows: Optional[torch.Tensor] = None, a_div: int = 1, out_rows: Optional[torch.Tensor] = None,
+                 out_dtype=torch.bfloat16, stream=None) -> torch.Tensor:
+    """out[i] = w[e] a[i] for the rows i of every expert e (moe_grouped_gemm):
+    offsets[e] <= i < offsets[e+1], int32 [E+1] on the GPU.
+
+    a bf16 [R,K] (rows may be strided); w bf16 [E,N,K]; out bf16 or fp32
+    [R,N], made here as out_dtype when not given (rows at or beyond offsets[E]
+    are not written).  a_rows int32 [R]: row i is row a_rows[i] // a_div of a,
+    zeros outside it (a_rows = align's sorted_ids, a_div = top_k: the tokens
+    themselves).  out_rows int32 [R]: row i goes to row out_rows[i] of out, and
+    nowhere outside it (without `out`, a result of R rows is made)."""
+    N, K = _weights(a, w)
+    return _grouped("moe_grouped_gemm", a, w, N, K, offsets, out, a_rows, a_div, out_rows, out_dtype, stream)
+
+
+def grouped_gemm_dgrad(dy: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, out: Optional[torch.Tensor] = None,
+                       *, dy_rows: Optional[torch.Tensor] = None, dy_div: int = 1,
+                       out_rows: Optional[torch.Tensor] = None, out_dtype=torch.bfloat16,
+                       stream=None) -> torch.Tensor:
+    """Gradient of grouped_gemm's input, out[i] = w[e]^T dy[i]
+    (moe_grouped_gemm_dgrad): dy bf16 [R,N] -> out [R,K]; the rest as there."""
+    N, K = _weights(dy, w)
+    return _grouped("moe_grouped_gemm_dgrad", dy, w, N, K, offsets, out, dy_rows, dy_div, out_rows, out_dtype, stream)
+
+
+def grouped_gemm_wgrad(dy: torch.Tensor, a: torch.Tensor, offsets: torch.Tensor, out: Optional[torch.Tensor] = None,
+                       *, dy_rows: Optional[torch.Tensor] = None, dy_div: int = 1,
+                       a_rows: Optional[torch.Tensor] = None, a_div: int = 1, accumulate: bool = False,
+                       out_dtype=torch.float32, stream=None) -> torch.Tensor:
+    """Gradient of grouped_gemm's weights, out[e] = sum of dy[i] a[i]^T over
+    expert e's rows (moe_grouped_gemm_wgrad), zeros for an expert without rows:
+    dy bf16 [R,N], a bf16 [R,K] -> out [E,N,K] fp32 or bf16.  accumulate: add
+    to `out` (fp32) instead.  Rows may be gathered as in grouped_gemm."""
+    call = _Call(dy, stream)
+    if not isinstance(a, torch.Tensor) or dy.dim() != 2 or a.dim() != 2:
+        raise ValueError("dy and a must be [rows, width] tensors")
+    E, N, K = offsets.numel() - 1, dy.shape[1], a.shape[1]
+    off = call.need(offsets, "offsets", torch.int32, (E + 1,))
+    R = (dy_rows.numel() if dy_rows is not None else a_rows.numel() if a_rows is not None
+         else min(dy.shape[0], a.shape[0]))
+    if out is None:
+        if accumulate:
+            raise ValueError("accumulate needs `out`")
+        if out_dtype not in _OUT_TYPE:
+            raise TypeError("out_dtype must be torch.bfloat16 or torch.float32")
+        out = call.empty((E, N, K), out_dtype)
+    if out.dtype not in _OUT_TYPE:
+        raise TypeError("out must be bfloat16 or float32, got %s" % out.dtype)
+    args = _GroupedWgradArgs(
+        R=R, E=E, N=N, K=K, offsets=off, dy=call.rows(dy, "dy", (torch.bfloat16,), N, dy_rows, dy_div, R),
+        in_=call.rows(a, "a", (torch.bfloat16,), K, a_rows, a_div, R), dw=call.need(out, "out", out.dtype, (E, N, K)),
+        out_type=_OUT_TYPE[out.dtype], accumulate=int(bool(accumulate)))
+    call.run("moe_grouped_gemm_wgrad", ctypes.byref(args))
+    return out
+
+
+def grouped_gemm_w4(a: torch.Tensor, w4: torch.Tensor, scales: torch.Tensor, offsets: torch.Tensor,
+                    out: Optional[torch.Tensor] = None, *, a_rows: Optional[torch.Tensor] = None, a_div: int = 1,
+                    out_rows: Optional[torch.Tensor] = None, out_dtype=torch.bfloat16, stream=None) -> torch.Tensor:
+    """grouped_gemm with 4-bit weights, streamed for a few rows per expert:
+    w4 uint8 [E,N,K/2], two codes per byte along K (low nibble first).  scales
+    uint8 [E,N,K/32]: OCP MXFP4 (e2m1 codes, E8M0 scales); scales bf16
+    [E,N,K/128]: integers 0..15 standing for -8..7."""
+    if not isinstance(w4, torch.Tensor) or w4.dim() != 3:
+        raise ValueError("the weights must be a tensor [E, N, K/2]")
+    if not isinstance(scales, torch.Tensor) or scales.dtype not in (torch.uint8, torch.bfloat16):
+        raise TypeError("scales must be uint8 (MXFP4) or bfloat16 (int4)")
+    call = _Call(a, stream)
+    E, N, K = w4.shape[0], w4.shape[1], 2 * w4.shape[2]
+    fmt = 1 if scales.dtype == torch.uint8 else 2
+    call.need(w4, "w4", torch.uint8, (E, N, K // 2))
+    call.need(scales, "scales", scales.dtype, (E, N, K // W4_GROUP["mxfp4" if fmt == 1 else "int4"]))
+    return _grouped("moe_grouped_gemm", a, w4, N, K, offsets, out, a_rows, a_div, out_rows, out_dtype, stream, fmt,
+                    scales)
+
+
+def swiglu_checkpoint(gu: torch.Tensor, row_weight: Optional[torch.Tensor] = None, *, checkpoint: bool = True,
+                      num_rows: Optional[torch.Tensor] = None, h: Optional[torch.Tensor] = None,
+                      codes: Optional[torch.Tensor] = None, scales: Optional[torch.Tensor] = None, stream=None):
+    """h = row_weight * SiLU(gate) * up of gu bf16 [R,2I] (gate columns first;
+    rows may be strided), and gu kept in 8 bits (moe_swiglu_checkpoint).
+
+    Returns (h bf16 [R,I], codes uint8 e4m3 [R,2I], scales uint8 E8M0
+    [R,2,ceil(I/32)]); the last two are None with checkpoint=False.  num_rows
+    int32 [1] on the GPU (offsets[E:]): rows at or beyond it are left alone."""
+    call = _Call(gu, stream)
+    if gu.dim() != 2 or gu.shape[1] % 2:
+        raise ValueError("gu must have shape (rows, 2*I), got %s" % (tuple(gu.shape),))
+    R, I = gu.shape[0], gu.shape[1] // 2
+    src = call.rows(gu, "gu", (torch.bfloat16,), 2 * I, None, 1, R)
+    if h is None:
+        h = call.empty((R, I), torch.bfloat16)
+    G = -(-I // CHECKPOINT_GROUP)
+    if checkpoint:
+        codes = call.empty((R, 2 * I), torch.uint8) if codes is None else codes
+        scales = call.empty((R, 2, G), torch.uint8) if scales is None else scales
+    elif codes is not None or scales is not None:
+        raise ValueError("codes and scales need checkpoint=True")
+    call.run("moe_swiglu_checkpoint", src.data, src.stride, call.vector(row_weight, "row_weight", torch.float32, R), R, I,
+             call.vector(num_rows, "num_rows", torch.int32, 1), call.need(h, "h", torch.bfloat16, (R, I)),
+             call.need(codes, "codes", torch.uint8, (R, 2 * I)) if checkpoint else None,
+             call.need(scales, "scales", torch.uint8, (R, 2, G)) if checkpoint else None)
+    return h, codes, scales
+
+
+def swiglu_checkpoint_grad(codes: torch.Tensor, scales: torch.Tensor, dh: torch.Tensor,
+                           row_weight: Optional[torch.Tensor] = None, *, num_rows: Optional[torch.Tensor] = None,
+                           dgu: Optional[torch.Tensor] = None, h: Optional[torch.Tensor] = None,
+                           dweight: Optional[torch.Tensor] = None, stream=None):
+    """Gradient of swiglu_checkpoint from its codes and scales and dh bf16
+    [R,I] (moe_swiglu_checkpoint_grad): returns (dgu bf16 [R,2I], h bf16 [R,I]
+    recomputed from the checkpoint and weighted, dweight fp32 [R])."""
+    call = _Call(dh, stream)
+    if dh.dim() != 2:
+        raise ValueError("dh must have shape (rows, I), got %s" % (tuple(dh.shape),))
+    R, I = dh.shape
+    if dgu is None:
+        dgu = call.empty((R, 2 * I), torch.bfloat16)
+    if h is None:
+        h = call.empty((R, I), torch.bfloat16)
+    if dweight is None:
+        dweight = call.empty((R,), torch.float32)
+    call.run("moe_swiglu_checkpoint_grad", call.need(codes, "codes", torch.uint8, (R, 2 * I)),
+             call.need(scales, "scales", torch.uint8, (R, 2, -(-I // CHECKPOINT_GROUP))),
+             call.need(dh, "dh", torch.bfloat16, (R, I)), call.vector(row_weight, "row_weight", torch.float32, R), R, I,
+             call.vector(num_rows, "num_rows", torch.int32, 1), call.need(dgu, "dgu", torch.bfloat16, (R, 2 * I)),
+             call.need(h, "h", torch.bfloat16, (R, I)), call.need(dweight, "dweight", torch.float32, (R,)))
+    return dgu, h, dweight

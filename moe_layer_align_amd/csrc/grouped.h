@@ -1,0 +1,57 @@
+// Expert products on rows grouped by expert: what their kernels share.
+#pragma once
+
+#include "moe_device.h"
+
+namespace moe {
+
+// A rows operand as the kernels take it (moe_rows_t): grouped row i is matrix
+// row i, or ids[i]/div; `rows` bounds it.
+struct RowsArg {
+  uint8_t* p;
+  int64_t stride;  // elements
+  int rows, div;
+  const int32_t* ids;
+};
+
+// Matrix row of grouped row i, or -1 when its id is outside the matrix.
+__device__ __forceinline__ int row_of(const RowsArg& r, int i) {
+  if (!r.ids) return i < r.rows ? i : -1;
+  const int f = r.ids[i];
+  const int m = f < 0 ? -1 : (r.div == 1 ? f : (int)((unsigned)f / (unsigned)r.div));
+  return m < r.rows ? m : -1;
+}
+
+struct GroupedArgs {
+  int R, E, N, K;
+  const int32_t* offsets;
+  RowsArg in, out;
+  const uint8_t* w;
+  const uint8_t* w_scale;
+};
+
+struct GroupedWgradArgs {
+  int R, E, N, K;
+  const int32_t* offsets;
+  RowsArg dy, in;
+  uint8_t* dw;
+};
+
+// Row range of expert e, its ends clamped so that no offset leads outside
+// [0, R].
+__device__ __forceinline__ void group_range(const int32_t* offsets, int e, int R, int* lo, int* hi) {
+  const int a = offsets[e], b = offsets[e + 1];
+  *lo = min(max(a, 0), R);
+  *hi = min(max(b, *lo), R);
+}
+
+// Host launchers; false when the launch could not be set up.
+bool launch_grouped_tile(bool dgrad, bool f32, hipStream_t st, const GroupedArgs& a);
+bool launch_grouped_wgrad(bool f32, bool accumulate, hipStream_t st, const GroupedWgradArgs& a);
+bool launch_grouped_stream(int format, bool f32, hipStream_t st, const GroupedArgs& a);
+void launch_swiglu_checkpoint(const uint8_t* gu, int64_t stride, const float* w, int R, int I, const int32_t* num_rows,
+                              uint8_t* h, uint8_t* codes, uint8_t* scales, hipStream_t st);
+void launch_swiglu_grad(const uint8_t* codes, const uint8_t* scales, const uint8_t* dh, const float* w, int R, int I,
+                        const int32_t* num_rows, uint8_t* dgu, uint8_t* h, float* dweight, hipStream_t st);
+
+}  // namespace moe
