@@ -431,10 +431,10 @@ moe_status_t moe_fused_forward_noalloc(const moe_fused_args_t* args, void* strea
  *  - MOE_ERR_INVALID_ARG: NULL or misaligned pointers (16 bytes; 4 for int32
  *    and fp32 vectors), negative sizes, div < 1, a stride below the width or
  *    not a multiple of 16 bytes, rows < R without ids, an unknown type.
- *    MOE_ERR_UNSUPPORTED: E > 512, N or K not a multiple of 8 (4-bit weights:
- *    K not a multiple of the scale group), an expert's matrix of 2^31 bytes
- *    or more, a row stride of 2^20 elements or more, and, for an input with
- *    ids, a matrix of 2^32 - 256 bytes or more.
+ *    MOE_ERR_UNSUPPORTED: R >= 2^26, E > 512, N or K not a multiple of 8
+ *    (4-bit weights: K not a multiple of the scale group), an expert's matrix
+ *    of 2^31 bytes or more, a row stride of 2^20 elements or more, and, for an
+ *    input with ids, a matrix (rows * stride) of more than 2^32 - 2^22 bytes.
  *  - Outputs must not overlap inputs or each other.
  */
 typedef struct {

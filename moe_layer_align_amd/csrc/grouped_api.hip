@@ -17,7 +17,9 @@ moe_status_t launch_status() { return hipGetLastError() == hipSuccess ? MOE_OK :
 
 constexpr int64_t kMaxStride = (int64_t)1 << 20;         // elements of a row stride: tile offsets stay below 2^31 bytes
 constexpr int64_t kMaxExpertBytes = (int64_t)1 << 31;    // one expert's matrix, addressed by 32-bit offsets
-constexpr int64_t kMaxGatherBytes = ((int64_t)1 << 32) - 256;  // a gathered matrix, by unsigned 32-bit offsets
+constexpr int64_t kMaxGatherBytes = ((int64_t)1 << 32) - ((int64_t)1 << 22);  // a gathered matrix, by unsigned 32-bit
+                                                                              // offsets (the tiled kernels' kOob)
+constexpr int kMaxRows = 1 << 26;                        // keeps the tiled products' grids below 2^31 workgroups
 constexpr int64_t kMaxElements = (int64_t)1 << 38;  // keeps the activation's grid below 2^31 workgroups
 
 bool known_out(moe_out_t t) { return t == MOE_OUT_BF16 || t == MOE_OUT_FP32; }
@@ -35,7 +37,7 @@ moe_status_t check_rows(const moe_rows_t& r, int R, int width, int esz, bool inp
 
 moe_status_t check_sizes(int R, int E, int N, int K) {
   if (R < 0 || E < 1 || N < 1 || K < 1) return MOE_ERR_INVALID_ARG;
-  if (E > kMaxExperts || N % 8 || K % 8 || (int64_t)N * K * 2 >= kMaxExpertBytes) return MOE_ERR_UNSUPPORTED;
+  if (R >= kMaxRows || E > kMaxExperts || N % 8 || K % 8 || (int64_t)N * K * 2 >= kMaxExpertBytes) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
 

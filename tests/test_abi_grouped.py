@@ -38,7 +38,7 @@ BAD = [
     (dict(R=-1), INVALID), (dict(E=0), INVALID), (dict(N=0), INVALID), (dict(K=-8), INVALID),
     (dict(offsets=None), INVALID), (dict(offsets=P + 2), INVALID), (dict(w=None), INVALID), (dict(w=P + 8), INVALID),
     (dict(w_scale=P), INVALID), (dict(weight=3), INVALID), (dict(weight=-1), INVALID), (dict(out_type=2), INVALID),
-    (dict(E=513), UNSUPPORTED), (dict(N=12), UNSUPPORTED), (dict(K=132), UNSUPPORTED),
+    (dict(E=513), UNSUPPORTED), (dict(R=1 << 26, in_=dict(n=1 << 26), out=dict(n=1 << 26)), UNSUPPORTED), (dict(N=12), UNSUPPORTED), (dict(K=132), UNSUPPORTED),
     (dict(N=1 << 16, K=1 << 14), UNSUPPORTED),
     (dict(in_=dict(data=None)), INVALID), (dict(in_=dict(data=P + 8)), INVALID), (dict(in_=dict(stride=64 - 8)), INVALID),
     (dict(in_=dict(stride=132)), INVALID), (dict(in_=dict(stride=1 << 20)), UNSUPPORTED),
