@@ -19,7 +19,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 UNITS = ["moe_api.hip", "launch_decode_bf16.hip", "launch_decode_fp8.hip", "launch_decode_fp8_static.hip",
          "launch_prefill.hip", "launch_layer1.hip", "launch_down_token.hip",
-         "grouped_api.hip", "grouped_tile.hip", "grouped_stream.hip", "swiglu.hip"]
+         "grouped_api.hip", "grouped_tile.hip", "grouped_stream.hip"]
 LIB = os.path.join(PKG, "libmoe_mi355x.so")
 PROBE_UNITS = ["probes.hip"]
 PROBE_LIB = os.path.join(PKG, "libmoe_probes.so")

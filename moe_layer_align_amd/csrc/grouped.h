@@ -49,9 +49,5 @@ __device__ __forceinline__ void group_range(const int32_t* offsets, int e, int R
 bool launch_grouped_tile(bool dgrad, bool f32, hipStream_t st, const GroupedArgs& a);
 bool launch_grouped_wgrad(bool f32, bool accumulate, hipStream_t st, const GroupedWgradArgs& a);
 bool launch_grouped_stream(int format, bool f32, hipStream_t st, const GroupedArgs& a);
-void launch_swiglu_checkpoint(const uint8_t* gu, int64_t stride, const float* w, int R, int I, const int32_t* num_rows,
-                              uint8_t* h, uint8_t* codes, uint8_t* scales, hipStream_t st);
-void launch_swiglu_grad(const uint8_t* codes, const uint8_t* scales, const uint8_t* dh, const float* w, int R, int I,
-                        const int32_t* num_rows, uint8_t* dgu, uint8_t* h, float* dweight, hipStream_t st);
 
 }  // namespace moe

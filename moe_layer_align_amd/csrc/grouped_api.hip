@@ -1,11 +1,13 @@
 // Host side of the grouped expert products and the checkpointed activation
-// (include/moe.h): argument validation and launches.
+// (include/moe.h): argument validation and launches.  The activation's
+// kernels are compiled here.
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
 
 #include "moe.h"
 #include "grouped.h"
+#include "swiglu.h"
 
 using namespace moe;
 

@@ -12,14 +12,15 @@
 // which clips mantissas above 1.75), no value is ever clipped, so each is
 // within half a step, 2^-4 of its own size, of the value it stands for (down
 // to the format's subnormals, 2^-15 of the group's largest).
+#pragma once
+
 #include "grouped.h"
 
 namespace moe {
-namespace {
 
-constexpr int kGroup = 32;     // values per scale
-constexpr int kPer = 8;        // values per thread and half
-constexpr int kQuad = kGroup / kPer;
+constexpr int kCkptGroup = 32;  // values per scale
+constexpr int kCkptPer = 8;     // values per thread and half
+constexpr int kCkptQuad = kCkptGroup / kCkptPer;
 
 // Biased exponent of the scale for a largest finite magnitude with bits
 // `amax`: exponent - 8, one more where the mantissa is above 1.75 (448 = 1.75
@@ -97,21 +98,21 @@ __device__ __forceinline__ float sigmoid_fast(float x) {
 
 // Threads run over (row, chunk of 8 columns), the chunks of a row padded to
 // whole quads.
-__global__ __launch_bounds__(256) void swiglu_checkpoint_kernel(const uint8_t* __restrict__ gu, int64_t stride,
+static __global__ __launch_bounds__(256) void swiglu_checkpoint_kernel(const uint8_t* __restrict__ gu, int64_t stride,
                                                                 const float* __restrict__ weight, int R, int I,
                                                                 const int32_t* __restrict__ num_rows,
                                                                 uint8_t* __restrict__ h, uint8_t* __restrict__ codes,
                                                                 uint8_t* __restrict__ scales) {
-  const int groups = (I + kGroup - 1) / kGroup, per_row = groups * kQuad;
+  const int groups = (I + kCkptGroup - 1) / kCkptGroup, per_row = groups * kCkptQuad;
   const int64_t base = (int64_t)blockIdx.x * 256;
   const int row0 = (int)(base / per_row);
   const unsigned local = (unsigned)(base - (int64_t)row0 * per_row) + threadIdx.x;
   const int row = row0 + (int)(local / (unsigned)per_row), chunk = (int)(local % (unsigned)per_row);
   const int limit = num_rows ? min(R, *num_rows) : R;
-  const bool in_row = row < limit, ok = in_row && chunk * kPer < I;
+  const bool in_row = row < limit, ok = in_row && chunk * kCkptPer < I;
   float g[8] = {}, u[8] = {};
   if (ok) {
-    const uint8_t* p = gu + ((int64_t)row * stride + chunk * kPer) * 2;
+    const uint8_t* p = gu + ((int64_t)row * stride + chunk * kCkptPer) * 2;
     unpack8(*(const u32x4*)p, g);
     unpack8(*(const u32x4*)(p + 2 * (int64_t)I), u);
   }
@@ -120,18 +121,18 @@ __global__ __launch_bounds__(256) void swiglu_checkpoint_kernel(const uint8_t* _
     float o[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) o[i] = g[i] * sigmoid_fast(g[i]) * u[i] * w;
-    *(u32x4*)(h + ((int64_t)row * I + chunk * kPer) * 2) = pack8(o);
+    *(u32x4*)(h + ((int64_t)row * I + chunk * kCkptPer) * 2) = pack8(o);
   }
   if (!codes) return;
   int cg, cu;
   const u32x2 qg = encode8(g, &cg), qu = encode8(u, &cu);
   if (ok) {
-    uint8_t* c = codes + (int64_t)row * 2 * I + chunk * kPer;
+    uint8_t* c = codes + (int64_t)row * 2 * I + chunk * kCkptPer;
     *(u32x2*)c = qg;
     *(u32x2*)(c + I) = qu;
   }
-  if (in_row && chunk % kQuad == 0) {
-    uint8_t* s = scales + (int64_t)row * 2 * groups + chunk / kQuad;
+  if (in_row && chunk % kCkptQuad == 0) {
+    uint8_t* s = scales + (int64_t)row * 2 * groups + chunk / kCkptQuad;
     s[0] = (uint8_t)cg;
     s[groups] = (uint8_t)cu;
   }
@@ -148,7 +149,7 @@ __global__ __launch_bounds__(WPR < 4 ? 256 : 64 * WPR) void swiglu_grad_kernel(
   __shared__ float part[WPR * kRows];
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   const int row = blockIdx.x * kRows + wave / WPR, wr = wave % WPR;
-  const int groups = (I + kGroup - 1) / kGroup;
+  const int groups = (I + kCkptGroup - 1) / kCkptGroup;
   const int limit = num_rows ? min(R, *num_rows) : R;
   float sum = 0.0f;
   if (row < limit) {
@@ -157,10 +158,10 @@ __global__ __launch_bounds__(WPR < 4 ? 256 : 64 * WPR) void swiglu_grad_kernel(
     const uint8_t* s = scales + (int64_t)row * 2 * groups;
     const uint8_t* d = dh + (int64_t)row * I * 2;
     uint8_t* o = dgu + (int64_t)row * I * 4;
-    for (int col = (wr * 64 + lane) * kPer; col < I; col += WPR * 64 * kPer) {
+    for (int col = (wr * 64 + lane) * kCkptPer; col < I; col += WPR * 64 * kCkptPer) {
       float g[8], u[8], dv[8], og[8], ou[8], oh[8];
-      decode8(*(const u32x2*)(c + col), pow2_of(s[col / kGroup]), g);
-      decode8(*(const u32x2*)(c + I + col), pow2_of(s[groups + col / kGroup]), u);
+      decode8(*(const u32x2*)(c + col), pow2_of(s[col / kCkptGroup]), g);
+      decode8(*(const u32x2*)(c + I + col), pow2_of(s[groups + col / kCkptGroup]), u);
       unpack8(*(const u32x4*)(d + 2 * (int64_t)col), dv);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
@@ -187,16 +188,14 @@ __global__ __launch_bounds__(WPR < 4 ? 256 : 64 * WPR) void swiglu_grad_kernel(
   }
 }
 
-}  // namespace
-
-void launch_swiglu_checkpoint(const uint8_t* gu, int64_t stride, const float* w, int R, int I, const int32_t* num_rows,
+inline void launch_swiglu_checkpoint(const uint8_t* gu, int64_t stride, const float* w, int R, int I, const int32_t* num_rows,
                               uint8_t* h, uint8_t* codes, uint8_t* scales, hipStream_t st) {
-  const int64_t threads = (int64_t)R * ((I + kGroup - 1) / kGroup) * kQuad;
+  const int64_t threads = (int64_t)R * ((I + kCkptGroup - 1) / kCkptGroup) * kCkptQuad;
   swiglu_checkpoint_kernel<<<(unsigned)((threads + 255) / 256), 256, 0, st>>>(gu, stride, w, R, I, num_rows, h, codes,
                                                                               scales);
 }
 
-void launch_swiglu_grad(const uint8_t* codes, const uint8_t* scales, const uint8_t* dh, const float* w, int R, int I,
+inline void launch_swiglu_grad(const uint8_t* codes, const uint8_t* scales, const uint8_t* dh, const float* w, int R, int I,
                         const int32_t* num_rows, uint8_t* dgu, uint8_t* h, float* dweight, hipStream_t st) {
   if (I <= 2048)
     swiglu_grad_kernel<1><<<(unsigned)((R + 3) / 4), 256, 0, st>>>(codes, scales, dh, w, R, I, num_rows, dgu, h, dweight);
