@@ -467,8 +467,9 @@ typedef enum {
  * K/2 bytes; w_scale E8M0 [E,N,K/32] (codes 2..252, under which every weight
  * is zero or a normal bf16) or bf16 [E,N,K/128].  The weights' values are exact
  * in the product: scales are powers of two in bf16 range (MXFP4), or applied
- * in fp32 to each group's sum (INT4).  4-bit weights are streamed once per 64
- * rows of an expert: the form for decoding.  bf16 weights take a streaming or
+ * in fp32 to each group's sum (INT4, where an infinite element of a row makes
+ * the row's results NaN).  4-bit weights are streamed once per 32 rows of an
+ * expert: the form for decoding.  bf16 weights take a streaming or
  * a tiled kernel by the mean number of rows per expert.
  */
 typedef struct {

@@ -204,9 +204,10 @@ def test_mxfp4_short_groups(K, name):
 
 
 @pytest.mark.parametrize("fmt", ["mxfp4", "int4"])
-def test_w4_larger(fmt):
-    # several workgroups per expert in both directions
-    w4_case(fmt, "many_small", 1544, 1408, True, True, torch.bfloat16)
+@pytest.mark.parametrize("N,K", [(1544, 1408), (2056, 1408), (3400, 640)])
+def test_w4_larger(fmt, N, K):
+    # many workgroups per expert: the launch's wider bands, with K long and short
+    w4_case(fmt, "many_small", N, K, True, True, torch.bfloat16)
 
 
 def w4_case(fmt, name, N, K, gather, scatter, dtype):
