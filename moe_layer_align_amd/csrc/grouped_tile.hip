@@ -27,6 +27,7 @@
 // use: about 100 KB are in flight per CU.  One barrier per phase (512 MFMA
 // cycles per SIMD).
 #include <atomic>
+#include <type_traits>
 
 #include "grouped.h"
 #include "mfma_tile.h"
@@ -75,9 +76,34 @@ __device__ __forceinline__ unsigned extent(int64_t rows, int64_t ld, int64_t wid
   return rows > 0 && width > 0 ? (unsigned)((rows - 1) * ld + width) : 0u;
 }
 
+// 16 bytes per lane from base + off (zeros past `bytes`) to dst + 16 * lane.
+// The compiler makes a transpose read from LDS wait for every tracked load into
+// LDS, which would empty the queue of loads in each phase: kernels with
+// transposed operands issue theirs as untracked instructions (they write no
+// register) and wait for them by count themselves.
+template <bool TRACKED>
 __device__ __forceinline__ void load_lds(const uint8_t* base, unsigned bytes, lds_u8* dst, unsigned off) {
-  const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc((void*)base, (short)0, (int)bytes, kBufferWord3);
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (void __attribute__((address_space(3)))*)dst, 16, (int)off, 0, 0, 0);
+  if constexpr (TRACKED) {
+    const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc((void*)base, (short)0, (int)bytes, kBufferWord3);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (void __attribute__((address_space(3)))*)dst, 16, (int)off, 0, 0, 0);
+  } else {
+    // the no-op is the wait that a vector load needs after its descriptor or m0
+    // was written, which the compiler does not see here
+    const uint64_t p = (uint64_t)base;
+    const u32x4 r = {(unsigned)uniform((int)(unsigned)p), (unsigned)uniform((int)((unsigned)(p >> 32) & 0xffffu)),
+                     (unsigned)uniform((int)bytes), (unsigned)kBufferWord3};
+    const unsigned at = (unsigned)uniform((int)(unsigned)(uintptr_t)dst);
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(at), "v"(off), "s"(r)
+                 : "memory");  // m0: nothing else in these kernels uses it
+  }
+}
+
+// Start of a phase: this wave's loads but the last N have landed and its LDS
+// reads are done; then the barrier.
+template <int N>
+__device__ __forceinline__ void phase_begin() {
+  __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0), for the compiler's own count of LDS reads
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
 }
 
 // A transposed operand's loads: the base moves with the steps, or, with row
@@ -89,23 +115,29 @@ struct TransLoads {
   int64_t ld;         // row bytes
   int64_t width;      // bytes from the tile's first index to a row's end
   unsigned bytes;     // buffer size of the current step
-  unsigned off0, off1;
+  u32x2 off;
   // row ids
   const int32_t* ids;
   int rows, div, first, end;  // matrix rows; grouped rows [first, end)
-  int id0, id1;
 
   __device__ __forceinline__ static int row(int wave, int lane) { return 8 * wave + (lane >> 4); }
   __device__ __forceinline__ static unsigned chunk(int lane) {
     return (unsigned)((lane & 15) ^ (4 * (lane >> 4))) << 4;
   }
   __device__ __forceinline__ void lane_offsets(int wave, int lane) {
-    off0 = (unsigned)(row(wave, lane) * ld) + chunk(lane);
-    off1 = off0 + (unsigned)(4 * ld);
+    const unsigned o = (unsigned)(row(wave, lane) * ld) + chunk(lane);
+    off = u32x2{o, o + (unsigned)(4 * ld)};
   }
-  __device__ __forceinline__ void fetch_ids(int s, int wave, int lane) {
-    id0 = ids[min(first + kC * s + row(wave, lane), end - 1)];
-    id1 = ids[min(first + kC * s + row(wave, lane) + 4, end - 1)];
+  // The wave's eight ids of step s by scalar loads (vector loads would be
+  // waited for together with the loads into LDS), then the lane's two.
+  __device__ __forceinline__ void fetch_ids(const int32_t* from, int s, int wave, int lane, int* id0, int* id1) const {
+    const __attribute__((address_space(4))) int32_t* p = (const __attribute__((address_space(4))) int32_t*)from;
+    const int r = first + kC * s + 8 * wave, g = lane >> 4;
+    const int last = end - 1;
+    const int a0 = p[min(r, last)], a1 = p[min(r + 1, last)], a2 = p[min(r + 2, last)], a3 = p[min(r + 3, last)];
+    const int b0 = p[min(r + 4, last)], b1 = p[min(r + 5, last)], b2 = p[min(r + 6, last)], b3 = p[min(r + 7, last)];
+    *id0 = g < 2 ? (g == 0 ? a0 : a1) : (g == 2 ? a2 : a3);
+    *id1 = g < 2 ? (g == 0 ? b0 : b1) : (g == 2 ? b2 : b3);
   }
   __device__ __forceinline__ unsigned id_offset(int f, bool in, int lane) const {
     const unsigned m = div == 1 ? (unsigned)f : (unsigned)f / (unsigned)div;
@@ -113,21 +145,49 @@ struct TransLoads {
   }
   // Step s (steps are taken in order, from 0): `count` rows in all.
   __device__ __forceinline__ void step(int s, int count, int wave, int lane) {
-    if (ids) {
+    const bool by_id = ids != nullptr;
+    u32x2 o = off;
+    unsigned n = bytes;
+    const uint8_t* at = base;
+    if (by_id) {
+      int f0, f1;
+      fetch_ids(ids, s, wave, lane, &f0, &f1);
       const int r = kC * s + row(wave, lane);
-      off0 = id_offset(id0, r < count, lane);
-      off1 = id_offset(id1, r + 4 < count, lane);
-      fetch_ids(s + 1, wave, lane);
+      o = u32x2{id_offset(f0, r < count, lane), id_offset(f1, r + 4 < count, lane)};
     } else {
-      if (s) base += kC * ld;
-      bytes = extent(min(kC, count - kC * s), ld, width);
+      if (s) at += kC * ld;
+      n = extent(min(kC, count - kC * s), ld, width);
     }
+    off = o;
+    base = at;
+    bytes = n;
   }
   __device__ __forceinline__ void issue(lds_u8* dst, int h) const {
-    load_lds(base, bytes, dst, off0 + h * (kHalf * 2));
-    load_lds(base, bytes, dst + 1024, off1 + h * (kHalf * 2));
+    load_lds<false>(base, bytes, dst, off[0] + h * (kHalf * 2));
+    load_lds<false>(base, bytes, dst + 1024, off[1] + h * (kHalf * 2));
   }
 };
+
+// Issue order of a phase: its MFMAs with the NDS fragment reads of the next
+// phase spread between the first six of them and the NVM loads after the third
+// and the last ones.  Reads or loads issued ahead of the MFMAs leave the matrix
+// pipe idle while the LDS takes them from eight waves at once.
+template <int NMF, int NDS, int NVM, int ID, int I = 0>
+__device__ __forceinline__ void interleave() {
+  if constexpr (I < NMF) {
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, ID);  // one MFMA
+    constexpr int kOver = NMF * 3 / 4;
+    if constexpr (I < kOver) {
+      constexpr int n = NDS * (I + 1) / kOver - NDS * I / kOver;
+      if constexpr (n > 0) __builtin_amdgcn_sched_group_barrier(0x100, n, ID);  // LDS reads
+    }
+    if constexpr (I >= kOver) {
+      constexpr int v = NVM * (I + 1 - kOver) / (NMF - kOver) - NVM * (I - kOver) / (NMF - kOver);
+      if constexpr (v > 0) __builtin_amdgcn_sched_group_barrier(0x020, v, ID);  // direct-to-LDS loads
+    }
+    interleave<NMF, NDS, NVM, ID, I + 1>();
+  }
+}
 
 template <int OP, bool F32, bool ACC, bool HALF>
 __device__ __forceinline__ void tile_product(const TileArgs& a, const Tile t, lds_u8* smem) {
@@ -168,7 +228,6 @@ __device__ __forceinline__ void tile_product(const TileArgs& a, const Tile t, ld
     if (r.ids) {
       l.base = r.p + (int64_t)x0 * 2;
       l.bytes = extent(r.rows, l.ld, l.width);
-      l.fetch_ids(0, wave, lane);
     } else {
       l.base = r.p + t.lo * l.ld + (int64_t)x0 * 2;
       l.lane_offsets(wave, lane);
@@ -208,7 +267,7 @@ __device__ __forceinline__ void tile_product(const TileArgs& a, const Tile t, ld
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
         const unsigned off = poff[q] + (unsigned)(h * kHalf * a.K * 2 + s * (kC * 2));
-        load_lds(pbase, pbytes, dst + q * 1024, ((nchunk ^ q) << 3) < len - kC * s ? off : kOob);
+        load_lds<true>(pbase, pbytes, dst + q * 1024, ((nchunk ^ q) << 3) < len - kC * s ? off : kOob);
       }
     }
   };
@@ -219,7 +278,7 @@ __device__ __forceinline__ void tile_product(const TileArgs& a, const Tile t, ld
     } else {
 #pragma unroll
       for (int q = 0; q < 2; ++q)
-        load_lds(qbase, kOob, dst + q * 1024,
+        load_lds<!kTransP>(qbase, kOob, dst + q * 1024,
                  ((nchunk ^ q) << 3) < len - kC * s ? qoff[h][q] + (unsigned)(s * (kC * 2)) : kOob);
     }
   };
@@ -269,6 +328,7 @@ __device__ __forceinline__ void tile_product(const TileArgs& a, const Tile t, ld
       for (int k = 0; k < 2; ++k)
 #pragma unroll
         for (int v = 0; v < 16; ++v) acc[i][j][k][v] = 0.0f;
+  constexpr int kReadsP = kTransP ? 16 : 8, kReadsQ = kTransQ ? 8 : 4;  // LDS reads of a half
   u32x4 A0[2][4], A1[2][4], F0[4], F1[4];
   auto mma = [&](f32x16 (&c)[2], const u32x4 (&p)[2][4], const u32x4 (&q)[4]) {
 #pragma unroll
@@ -281,10 +341,7 @@ __device__ __forceinline__ void tile_product(const TileArgs& a, const Tile t, ld
     if constexpr (!HALF) {
       // A phase at time t waits until at most the loads of the last six phases
       // are outstanding: those it is about to read were issued seven phases ago.
-      auto begin = [&] {
-        wait_vm<12>();
-        ring_barrier();
-      };
+      auto begin = [] { phase_begin<12>(); };
       auto fence = [] { __builtin_amdgcn_sched_barrier(0); };
       step_p(0);
       issue_p(0, 0, 0);
@@ -305,46 +362,48 @@ __device__ __forceinline__ void tile_product(const TileArgs& a, const Tile t, ld
       step_p(2);
       issue_p(0, 2, 0);
       // X holds Q half 0 of the step on entry; Y takes half 1, then half 0 of the next step
-      auto step = [&](int s, int b, u32x4 (&X)[4], u32x4 (&Y)[4]) {
+      auto step = [&](int s, auto bt, u32x4 (&X)[4], u32x4 (&Y)[4]) {
+        constexpr int b = decltype(bt)::value;
         begin();
+        fence();
         read_q(Y, 1, b);
         step_q(s + 2);
         issue_q(0, s + 2, b);
-        fence();
         mma(acc[0][0], A0, X);
+        interleave<8, kReadsQ, 2, 4 * b>();
         fence();
         begin();
+        fence();
         read_p(A1, 1, b);
         issue_q(1, s + 2, b);
-        fence();
         mma(acc[0][HALF ? 0 : 1], A0, Y);
+        interleave<8, kReadsP, 2, 4 * b + 1>();
         fence();
         begin();
+        fence();
         read_p(A0, 0, b ^ 1);
         issue_p(1, s + 2, b);
-        fence();
         mma(acc[1][HALF ? 0 : 1], A1, Y);
+        interleave<8, kReadsP, 2, 4 * b + 2>();
         fence();
         begin();
+        fence();
         read_q(Y, 0, b ^ 1);
         step_p(s + 3);
         issue_p(0, s + 3, b ^ 1);
-        fence();
         mma(acc[1][0], A1, X);
+        interleave<8, kReadsQ, 2, 4 * b + 3>();
         fence();
       };
       for (int s = 0; s < nk; s += 2) {
-        step(s, 0, F0, F1);
+        step(s, std::integral_constant<int, 0>{}, F0, F1);
         if (s + 1 >= nk) break;
-        step(s + 1, 1, F1, F0);
+        step(s + 1, std::integral_constant<int, 1>{}, F1, F0);
       }
     } else {
       // At most 128 q: two phases per step, P half 1 is read in the first, P
       // half 0 and Q of the next step in the second.
-      auto begin = [&] {
-        wait_vm<6>();
-        ring_barrier();
-      };
+      auto begin = [] { phase_begin<6>(); };
       auto fence = [] { __builtin_amdgcn_sched_barrier(0); };
       step_p(0);
       issue_p(0, 0, 0);
@@ -361,32 +420,34 @@ __device__ __forceinline__ void tile_product(const TileArgs& a, const Tile t, ld
       ring_barrier();
       // the order of all later issues: P1(1), then P0(2) Q0(2), P1(2), ...
       issue_p(1, 1, 1);
-      auto step = [&](int s, int b, u32x4 (&X)[4], u32x4 (&Y)[4]) {
+      auto step = [&](int s, auto bt, u32x4 (&X)[4], u32x4 (&Y)[4]) {
+        constexpr int b = decltype(bt)::value;
         begin();
+        fence();
         read_p(A1, 1, b);
         step_p(s + 2);
         issue_p(0, s + 2, b);
         step_q(s + 2);
         issue_q(0, s + 2, b);
-        fence();
         mma(acc[0][0], A0, X);
+        interleave<8, kReadsP, 4, 8 + 2 * b>();
         fence();
         begin();
+        fence();
         read_p(A0, 0, b ^ 1);
         read_q(Y, 0, b ^ 1);
         issue_p(1, s + 2, b);
-        fence();
         mma(acc[1][0], A1, X);
+        interleave<8, kReadsP + kReadsQ, 2, 9 + 2 * b>();
         fence();
       };
       for (int s = 0; s < nk; s += 2) {
-        step(s, 0, F0, F1);
+        step(s, std::integral_constant<int, 0>{}, F0, F1);
         if (s + 1 >= nk) break;
-        step(s + 1, 1, F1, F0);
+        step(s + 1, std::integral_constant<int, 1>{}, F1, F0);
       }
     }
-    wait_vm<0>();  // the loads past the last step (zeros) still write LDS
-    ring_barrier();
+    phase_begin<0>();  // the loads past the last step (zeros) still write LDS
   }
 
   // ---- epilogue: each wave transposes its 64 p x 32 q of a quadrant through
