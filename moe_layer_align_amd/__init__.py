@@ -420,81 +420,99 @@ def fused_forward(x: torch.Tensor, logits: Optional[torch.Tensor], w13: torch.Te
 class _Call:
     """The tensors of one call: all on one GPU, whose current stream (or
     `stream`) it runs on; outputs made here for a side stream are recorded
-    on it."""
+    on it.  A decode-sized call takes about ten microseconds on the GPU, so the
+    checks are written for few Python steps."""
+
+    __slots__ = ("index", "given", "stream")
 
     def __init__(self, like: torch.Tensor, stream):
-        if not isinstance(like, torch.Tensor) or like.device.type != "cuda":
+        if not isinstance(like, torch.Tensor) or not like.is_cuda:
             raise ValueError("the operands must be GPU tensors")
-        self.device, self.given = like.device, stream
-        self.stream = torch.cuda.current_stream(like.device).cuda_stream if stream is None else _stream(stream)
+        self.index, self.given = like.get_device(), stream
+        self.stream = torch._C._cuda_getCurrentRawStream(self.index) if stream is None else _stream(stream)
 
     def need(self, t, name, dtype, shape):
-        _need(t, name, dtype, shape)
-        self.same_device(t, name)
+        """Pointer of a contiguous tensor of this type and shape."""
+        if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+            _need(t, name, dtype, shape)  # says what is wrong
+        if t.get_device() != self.index:
+            self.elsewhere(t, name)
         return t.data_ptr()
 
-    def same_device(self, t, name):
-        if t.device != self.device:
-            raise ValueError("%s is on %s, the other operands on %s" % (name, t.device, self.device))
+    def elsewhere(self, t, name):
+        raise ValueError("%s is on %s, the other operands on cuda:%d" % (name, t.device, self.index))
 
     def empty(self, shape, dtype):
-        t = torch.empty(shape, dtype=dtype, device=self.device)
-        if self.given is not None and self.stream != torch.cuda.current_stream(self.device).cuda_stream:
-            t.record_stream(torch.cuda.ExternalStream(self.stream, device=self.device))
+        t = torch.empty(shape, dtype=dtype, device=torch.device("cuda", self.index))
+        if self.given is not None and self.stream != torch._C._cuda_getCurrentRawStream(self.index):
+            t.record_stream(torch.cuda.ExternalStream(self.stream, device=t.device))
         return t
 
     def vector(self, t, name, dtype, n):
         return None if t is None else self.need(t, name, dtype, (n,))
 
-    def rows(self, t, name, dtypes, width, ids, div, R) -> _Rows:
+    def rows(self, t, name, dtype, width, ids, div, R) -> _Rows:
         """A [rows, width] operand whose rows may be strided, as moe_rows_t."""
-        if not isinstance(t, torch.Tensor) or t.device.type != "cuda":
-            raise ValueError("%s must be a GPU tensor" % name)
-        self.same_device(t, name)
-        if t.dtype not in dtypes:
-            raise TypeError("%s must be %s, got %s" % (name, " or ".join(map(str, dtypes)), t.dtype))
-        if t.dim() != 2 or t.shape[1] != width:
-            raise ValueError("%s must have shape (rows, %d), got %s" % (name, width, tuple(t.shape)))
-        if t.shape[1] > 1 and t.stride(1) != 1:
+        if not isinstance(t, torch.Tensor) or t.get_device() != self.index:
+            raise ValueError("%s must be a tensor on cuda:%d" % (name, self.index))
+        if t.dtype is not dtype:
+            raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+        shape = t.shape
+        if len(shape) != 2 or shape[1] != width:
+            raise ValueError("%s must have shape (rows, %d), got %s" % (name, width, tuple(shape)))
+        step = t.stride()
+        if step[1] != 1 and width > 1:
             raise ValueError("%s's rows must be contiguous" % name)
-        ptr = None if ids is None else self.vector(ids, name + "'s row ids", torch.int32, R)
+        ptr = None
+        if ids is not None:
+            ptr = self.need(ids, name + "'s row ids", torch.int32, (R,)) or None
         # one row has no stride of its own, no row at all no address
-        stride = t.stride(0) if t.shape[0] > 1 else width
-        return _Rows(data=t.data_ptr() or 16, stride=stride, rows=t.shape[0], div=div if ptr else 1,
-                     ids=ptr or None)
+        return _Rows(t.data_ptr() or 16, step[0] if shape[0] > 1 else width, shape[0], div if ptr else 1, ptr)
 
     def run(self, fn, *args):
-        with torch.cuda.device(self.device):
-            _check(fn, getattr(load(), fn)(*args, self.stream))
+        call = getattr(_lib or load(), fn)
+        if torch._C._cuda_getDevice() == self.index:
+            code = call(*args, self.stream)
+        else:
+            with torch.cuda.device(self.index):
+                code = call(*args, self.stream)
+        if code:
+            raise MoEError(fn, code)
 
 
 _OUT_TYPE = {torch.bfloat16: 0, torch.float32: 1}
 
 
-def _grouped(fn, a, w, N, K, offsets, out, in_rows, in_div, out_rows, out_dtype, stream, weight=0, scales=None):
-    call = _Call(a, stream)
-    E = w.shape[0]
+def _out_type(dtype, name) -> int:
+    if dtype not in _OUT_TYPE:
+        raise TypeError("%s must be torch.bfloat16 or torch.float32, got %s" % (name, dtype))
+    return _OUT_TYPE[dtype]
+
+
+def _grouped(fn, call, a, w, E, N, K, offsets, out, in_rows, in_div, out_rows, out_dtype, weight=0, scales=None):
     src, dst = (N, K) if fn == "moe_grouped_gemm_dgrad" else (K, N)
     off = call.need(offsets, "offsets", torch.int32, (E + 1,))
     R = a.shape[0] if in_rows is None else in_rows.numel()
     if out is None:
-        if out_dtype not in _OUT_TYPE:
-            raise TypeError("out_dtype must be torch.bfloat16 or torch.float32")
+        out_type = _out_type(out_dtype, "out_dtype")
         out = call.empty((R, dst), out_dtype)
-    args = _GroupedArgs(
-        R=R, E=E, N=N, K=K, offsets=off, in_=call.rows(a, "input", (torch.bfloat16,), src, in_rows, in_div, R),
-        weight=weight, w=w.data_ptr(), w_scale=None if scales is None else scales.data_ptr(),
-        out=call.rows(out, "out", tuple(_OUT_TYPE), dst, out_rows, 1, R), out_type=_OUT_TYPE[out.dtype])
+    elif isinstance(out, torch.Tensor):
+        out_type = _out_type(out.dtype, "out")
+    else:
+        raise ValueError("out must be a GPU tensor")
+    args = _GroupedArgs(R, E, N, K, off, call.rows(a, "input", torch.bfloat16, src, in_rows, in_div, R), weight, w,
+                        scales, call.rows(out, "out", out.dtype, dst, out_rows, 1, R), out_type)
     call.run(fn, ctypes.byref(args))
     return out
 
 
-def _weights(a, w) -> tuple:
+def _bf16_product(fn, a, w, offsets, out, in_rows, in_div, out_rows, out_dtype, stream):
+    call = _Call(a, stream)
     if not isinstance(w, torch.Tensor) or w.dim() != 3:
         raise ValueError("the weights must be a tensor [E, N, K]")
-    call = _Call(a, None)
-    call.need(w, "w", torch.bfloat16, w.shape)
-    return w.shape[1], w.shape[2]
+    E, N, K = w.shape
+    return _grouped(fn, call, a, call.need(w, "w", torch.bfloat16, (E, N, K)), E, N, K, offsets, out, in_rows, in_div,
+                    out_rows, out_dtype)
 
 
 def grouped_gemm(a: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, out: Optional[torch.Tensor] = None, *,
@@ -509,8 +527,7 @@ def grouped_gemm(a: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, out: O
     zeros outside it (a_rows = align's sorted_ids, a_div = top_k: the tokens
     themselves).  out_rows int32 [R]: row i goes to row out_rows[i] of out, and
     nowhere outside it (without `out`, a result of R rows is made)."""
-    N, K = _weights(a, w)
-    return _grouped("moe_grouped_gemm", a, w, N, K, offsets, out, a_rows, a_div, out_rows, out_dtype, stream)
+    return _bf16_product("moe_grouped_gemm", a, w, offsets, out, a_rows, a_div, out_rows, out_dtype, stream)
 
 
 def grouped_gemm_dgrad(dy: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, out: Optional[torch.Tensor] = None,
@@ -519,8 +536,7 @@ def grouped_gemm_dgrad(dy: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor,
                        stream=None) -> torch.Tensor:
     """Gradient of grouped_gemm's input, out[i] = w[e]^T dy[i]
     (moe_grouped_gemm_dgrad): dy bf16 [R,N] -> out [R,K]; the rest as there."""
-    N, K = _weights(dy, w)
-    return _grouped("moe_grouped_gemm_dgrad", dy, w, N, K, offsets, out, dy_rows, dy_div, out_rows, out_dtype, stream)
+    return _bf16_product("moe_grouped_gemm_dgrad", dy, w, offsets, out, dy_rows, dy_div, out_rows, out_dtype, stream)
 
 
 def grouped_gemm_wgrad(dy: torch.Tensor, a: torch.Tensor, offsets: torch.Tensor, out: Optional[torch.Tensor] = None,
@@ -541,15 +557,14 @@ def grouped_gemm_wgrad(dy: torch.Tensor, a: torch.Tensor, offsets: torch.Tensor,
     if out is None:
         if accumulate:
             raise ValueError("accumulate needs `out`")
-        if out_dtype not in _OUT_TYPE:
-            raise TypeError("out_dtype must be torch.bfloat16 or torch.float32")
+        _out_type(out_dtype, "out_dtype")
         out = call.empty((E, N, K), out_dtype)
-    if out.dtype not in _OUT_TYPE:
-        raise TypeError("out must be bfloat16 or float32, got %s" % out.dtype)
-    args = _GroupedWgradArgs(
-        R=R, E=E, N=N, K=K, offsets=off, dy=call.rows(dy, "dy", (torch.bfloat16,), N, dy_rows, dy_div, R),
-        in_=call.rows(a, "a", (torch.bfloat16,), K, a_rows, a_div, R), dw=call.need(out, "out", out.dtype, (E, N, K)),
-        out_type=_OUT_TYPE[out.dtype], accumulate=int(bool(accumulate)))
+    elif not isinstance(out, torch.Tensor):
+        raise ValueError("out must be a GPU tensor")
+    args = _GroupedWgradArgs(R, E, N, K, off, call.rows(dy, "dy", torch.bfloat16, N, dy_rows, dy_div, R),
+                             call.rows(a, "a", torch.bfloat16, K, a_rows, a_div, R),
+                             call.need(out, "out", out.dtype, (E, N, K)), _out_type(out.dtype, "out"),
+                             int(bool(accumulate)))
     call.run("moe_grouped_gemm_wgrad", ctypes.byref(args))
     return out
 
@@ -567,11 +582,10 @@ def grouped_gemm_w4(a: torch.Tensor, w4: torch.Tensor, scales: torch.Tensor, off
         raise TypeError("scales must be uint8 (MXFP4) or bfloat16 (int4)")
     call = _Call(a, stream)
     E, N, K = w4.shape[0], w4.shape[1], 2 * w4.shape[2]
-    fmt = 1 if scales.dtype == torch.uint8 else 2
-    call.need(w4, "w4", torch.uint8, (E, N, K // 2))
-    call.need(scales, "scales", scales.dtype, (E, N, K // W4_GROUP["mxfp4" if fmt == 1 else "int4"]))
-    return _grouped("moe_grouped_gemm", a, w4, N, K, offsets, out, a_rows, a_div, out_rows, out_dtype, stream, fmt,
-                    scales)
+    fmt, group = (1, W4_GROUP["mxfp4"]) if scales.dtype is torch.uint8 else (2, W4_GROUP["int4"])
+    return _grouped("moe_grouped_gemm", call, a, call.need(w4, "w4", torch.uint8, (E, N, K // 2)), E, N, K, offsets, out,
+                    a_rows, a_div, out_rows, out_dtype, fmt,
+                    call.need(scales, "scales", scales.dtype, (E, N, K // group)))
 
 
 def swiglu_checkpoint(gu: torch.Tensor, row_weight: Optional[torch.Tensor] = None, *, checkpoint: bool = True,
@@ -587,7 +601,7 @@ def swiglu_checkpoint(gu: torch.Tensor, row_weight: Optional[torch.Tensor] = Non
     if gu.dim() != 2 or gu.shape[1] % 2:
         raise ValueError("gu must have shape (rows, 2*I), got %s" % (tuple(gu.shape),))
     R, I = gu.shape[0], gu.shape[1] // 2
-    src = call.rows(gu, "gu", (torch.bfloat16,), 2 * I, None, 1, R)
+    src = call.rows(gu, "gu", torch.bfloat16, 2 * I, None, 1, R)
     if h is None:
         h = call.empty((R, I), torch.bfloat16)
     G = -(-I // CHECKPOINT_GROUP)

@@ -26,6 +26,16 @@
 // loads of the half whose slot the phase before freed, six phases ahead of its
 // use: about 100 KB are in flight per CU.  One barrier per phase (512 MFMA
 // cycles per SIMD).
+//
+// One persistent workgroup per CU walks the tiles, and its loads run on into
+// the next tile: the queue stays full over a tile's epilogue, which transposes
+// the results through LDS beside the ring.  Filling the ring anew for every
+// tile, all CUs at once, cost 9 to 14 us a tile of 24 to 100.
+//
+// Rows of an expert past its last whole tile make a tile of 256 x 256 (more
+// than 128 rows), 256 x 128 (more than 64) or several of 128 x 64, and each
+// kind is run after the larger ones: the small ones are bound by the stream of
+// the weights and fill the CUs that the large ones leave idle at the end.
 #include <atomic>
 #include <type_traits>
 
@@ -46,7 +56,12 @@ constexpr int kC = 64;            // contraction per step
 constexpr int kHalf = 128;        // indices of an operand half
 constexpr int kTile = 256;
 constexpr int kPiece = kHalf * kC * 2;  // 16 KB: one half of one step
-constexpr int kLds = 8 * kPiece;  // 2 stages x 2 operands x 2 halves
+constexpr int kRing = 8 * kPiece;       // 2 stages x 2 operands x 2 halves
+constexpr int kEpi = 2048;              // epilogue area of a wave
+constexpr int kTable = kRing + 8 * kEpi;  // tile counts of the experts
+constexpr int kLds = kTable + 2 * kMaxExperts * 4 + 64;
+constexpr int kSlots = 32;              // most workgroups per XCD: one per CU
+static_assert(kLds <= 160 * 1024, "LDS of one gfx950 CU");
 // offset of a lane that loads nothing: past every buffer (their sizes are at
 // most this), and far enough below 2^32 that an in-row offset added to it does
 // not wrap
@@ -68,6 +83,8 @@ struct Tile {
   int e, lo, hi, q0, p0;
 };
 
+// Workgroups per XCD, the stride of a workgroup's items.
+__device__ __forceinline__ int slots() { return (int)gridDim.x >> 3; }
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
 // Bytes from the first of `rows` rows `ld` bytes apart to the end of the last
@@ -96,6 +113,13 @@ __device__ __forceinline__ void load_lds(const uint8_t* base, unsigned bytes, ld
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(at), "v"(off), "s"(r)
                  : "memory");  // m0: nothing else in these kernels uses it
   }
+}
+
+// Between a wave's LDS writes and its other lanes' reads of them: the hardware
+// keeps a wave's LDS accesses in order, the compiler has to be told.
+__device__ __forceinline__ void wave_exchange() {
+  __builtin_amdgcn_wave_barrier();
+  asm volatile("" ::: "memory");
 }
 
 // Start of a phase: this wave's loads but the last N have landed and its LDS
@@ -143,7 +167,24 @@ struct TransLoads {
     const unsigned m = div == 1 ? (unsigned)f : (unsigned)f / (unsigned)div;
     return in && f >= 0 && m < (unsigned)rows ? m * (unsigned)ld + chunk(lane) : kOob;
   }
-  // Step s (steps are taken in order, from 0): `count` rows in all.
+  // Columns from x0 on of a rows operand, over the rows of tile t.
+  __device__ __forceinline__ void rows_of(const RowsArg& r, int w, int x0, const Tile& t, int wave, int lane) {
+    ids = r.ids;
+    ld = r.stride * 2;
+    width = (int64_t)(w - x0) * 2;
+    rows = r.rows;
+    div = r.div;
+    first = t.lo;
+    end = t.hi;
+    base = r.p + (int64_t)x0 * 2 + (ids ? 0 : t.lo * ld);
+    bytes = ids ? extent(rows, ld, width) : 0u;
+    lane_offsets(wave, lane);
+  }
+  __device__ __forceinline__ void none() {
+    ids = nullptr;
+    bytes = 0;
+  }
+  // Step s (steps are taken in order, from 0): `count` rows in all, at least one.
   __device__ __forceinline__ void step(int s, int count, int wave, int lane) {
     const bool by_id = ids != nullptr;
     u32x2 o = off;
@@ -189,130 +230,192 @@ __device__ __forceinline__ void interleave() {
   }
 }
 
-template <int OP, bool F32, bool ACC, bool HALF>
-__device__ __forceinline__ void tile_product(const TileArgs& a, const Tile t, lds_u8* smem) {
-  constexpr bool kTransP = OP != 0, kTransQ = OP == 2;
-  const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
-  const int wr = wave >> 2, wc = wave & 3;
-  const int len = OP == 0 ? a.K : (OP == 1 ? a.N : t.hi - t.lo);  // contraction
-  const int nk = (len + kC - 1) / kC;
-  const int width = OP == 0 ? a.N : a.K;                           // of p
+// Number of 64-deep steps of a tile, even (the loop takes two at a time; a step
+// past the end multiplies zeros).
+template <int OP>
+__device__ __forceinline__ int contraction(const TileArgs& a, const Tile& t) {
+  return OP == 0 ? a.K : (OP == 1 ? a.N : t.hi - t.lo);
+}
+__device__ __forceinline__ int steps_of(int len) { return 2 * ((len + 2 * kC - 1) / (2 * kC)); }
 
-  // ---- loads.  Natural: wave w loads rows 16w + 8q + lane/8 (q = 0, 1), lane l
-  // the logical chunk (l%8) ^ pf_mix(row) = (l%8) ^ (l/8) ^ q.
-  const int nrow = 16 * wave + (lane >> 3);
-  const int nchunk = (lane & 7) ^ (lane >> 3);
-  const uint8_t* pbase = nullptr;
-  unsigned pbytes = 0, poff[2];
+// The loads of one workgroup's sequence of tiles, step by step.
+template <int OP, bool HALF>
+struct Loads {
+  static constexpr bool kTransP = OP != 0, kTransQ = OP == 2;
+  int s, nk, len;  // step of the current tile, its steps and its contraction
+  const uint8_t* pbase;
+  const uint8_t* qbase;
+  unsigned pbytes;
+  u32x2 poff;           // natural P: rows 16w + lane/8 and 8 more
+  u32x2 qoff0, qoff1;   // natural Q: the same of half 0 and half 1
   TransLoads tp, tq;
-  if constexpr (!kTransP) {
-    pbase = a.w + ((int64_t)t.e * a.N + t.p0) * a.K * 2;
-    pbytes = extent(min(kTile, a.N - t.p0), (int64_t)a.K * 2, (int64_t)a.K * 2);
-#pragma unroll
-    for (int q = 0; q < 2; ++q) poff[q] = (unsigned)((nrow + 8 * q) * a.K * 2 + ((nchunk ^ q) << 4));
-  } else if constexpr (OP == 1) {
-    tp.ids = nullptr;
-    tp.ld = (int64_t)a.K * 2;
-    tp.width = (int64_t)(a.K - t.p0) * 2;
-    tp.base = a.w + ((int64_t)t.e * a.N * a.K + t.p0) * 2;
-    tp.lane_offsets(wave, lane);
-  }
-  auto rows_loads = [&](TransLoads& l, const RowsArg& r, int w, int x0) {  // OP 2
-    l.ids = r.ids;
-    l.ld = r.stride * 2;
-    l.width = (int64_t)(w - x0) * 2;
-    l.rows = r.rows;
-    l.div = r.div;
-    l.first = t.lo;
-    l.end = t.hi;
-    if (r.ids) {
-      l.base = r.p + (int64_t)x0 * 2;
-      l.bytes = extent(r.rows, l.ld, l.width);
-    } else {
-      l.base = r.p + t.lo * l.ld + (int64_t)x0 * 2;
-      l.lane_offsets(wave, lane);
+
+  // Natural operands: wave w loads rows 16w + 8i + lane/8 (i = 0, 1) of a half,
+  // lane l the logical chunk (l%8) ^ pf_mix(row) = (l%8) ^ (l/8) ^ i.
+  __device__ __forceinline__ static int nrow(int wave, int lane) { return 16 * wave + (lane >> 3); }
+  __device__ __forceinline__ static int nchunk(int lane) { return (lane & 7) ^ (lane >> 3); }
+
+  __device__ __forceinline__ void init(const TileArgs& a, int wave, int lane) {
+    if constexpr (!kTransP)
+      poff = u32x2{(unsigned)(nrow(wave, lane) * a.K * 2 + (nchunk(lane) << 4)),
+                   (unsigned)((nrow(wave, lane) + 8) * a.K * 2 + ((nchunk(lane) ^ 1) << 4))};
+    if constexpr (OP == 1) {
+      tp.ids = nullptr;
+      tp.ld = (int64_t)a.K * 2;
+      tp.lane_offsets(wave, lane);
     }
-  };
-  const uint8_t* qbase = nullptr;
-  unsigned qoff[2][2];
-  if constexpr (kTransQ) {
-    rows_loads(tp, a.p, a.K, t.p0);
-    rows_loads(tq, a.q, a.N, t.q0);
-  } else {
-    qbase = a.q.ids ? a.q.p : a.q.p + t.q0 * a.q.stride * 2;
-#pragma unroll
-    for (int h = 0; h < (HALF ? 1 : 2); ++h)
-#pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        const int i = kHalf * h + nrow + 8 * q;
-        const int m = t.q0 + i < t.hi ? (a.q.ids ? row_of(a.q, t.q0 + i) : i) : -1;
-        qoff[h][q] = m >= 0 ? (unsigned)m * (unsigned)(a.q.stride * 2) + ((nchunk ^ q) << 4) : kOob;
-      }
   }
-  auto p_slot = [&](int h, int b) { return smem + (2 * h + b) * kPiece; };
-  auto q_slot = [&](int h, int b) { return smem + (4 + 2 * h + b) * kPiece; };
-  auto step_p = [&](int s) {
+  __device__ __forceinline__ unsigned row_offset(const TileArgs& a, const Tile& t, int i, int chunk) const {
+    const int m = t.q0 + i < t.hi ? (a.q.ids ? row_of(a.q, t.q0 + i) : i) : -1;
+    return m >= 0 ? (unsigned)m * (unsigned)(a.q.stride * 2) + (chunk << 4) : kOob;
+  }
+  // To the first step of a tile.
+  __device__ __forceinline__ void tile(const TileArgs& a, const Tile& t, int wave, int lane) {
+    len = contraction<OP>(a, t);
+    nk = steps_of(len);
+    s = 0;
+    if constexpr (OP == 0) {
+      pbase = a.w + ((int64_t)t.e * a.N + t.p0) * a.K * 2;
+      pbytes = extent(min(kTile, a.N - t.p0), (int64_t)a.K * 2, (int64_t)a.K * 2);
+    }
+    if constexpr (OP == 1) {
+      tp.width = (int64_t)(a.K - t.p0) * 2;
+      tp.base = a.w + ((int64_t)t.e * a.N * a.K + t.p0) * 2;
+    }
+    if constexpr (!kTransQ) {
+      qbase = a.q.ids ? a.q.p : a.q.p + t.q0 * a.q.stride * 2;
+      const int r = nrow(wave, lane), c = nchunk(lane);
+      qoff0 = u32x2{row_offset(a, t, r, c), row_offset(a, t, r + 8, c ^ 1)};
+      if constexpr (!HALF) qoff1 = u32x2{row_offset(a, t, kHalf + r, c), row_offset(a, t, kHalf + r + 8, c ^ 1)};
+    } else {
+      tp.rows_of(a.p, a.K, t.p0, t, wave, lane);
+      tq.rows_of(a.q, a.N, t.q0, t, wave, lane);
+    }
+    if constexpr (kTransP) tp.step(0, len, wave, lane);
+    if constexpr (kTransQ) tq.step(0, len, wave, lane);
+  }
+  __device__ __forceinline__ void step(int wave, int lane) {  // to the next step of the tile
+    ++s;
     if constexpr (kTransP) tp.step(s, len, wave, lane);
-  };
-  auto step_q = [&](int s) {
     if constexpr (kTransQ) tq.step(s, len, wave, lane);
-  };
-  // half h of step s (b = s & 1); a natural chunk at or past the contraction's
-  // end loads nothing (zeros)
-  auto issue_p = [&](int h, int s, int b) {
-    lds_u8* dst = p_slot(h, b) + wave * 2048;
+  }
+  __device__ __forceinline__ void end() {  // no more tiles: load nothing
+    nk = 0x7fffffff;
+    s = 0;
+    len = 0;
+    if constexpr (!kTransQ) qoff0 = qoff1 = u32x2{kOob, kOob};
+    pbytes = 0;
+    tp.none();
+    tq.none();
+  }
+  // Half h into its slot; a natural chunk at or past the contraction's end
+  // loads nothing (zeros).
+  __device__ __forceinline__ void issue_p(const TileArgs& a, lds_u8* dst, int h, int lane) const {
     if constexpr (kTransP) {
       tp.issue(dst, h);
     } else {
-#pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        const unsigned off = poff[q] + (unsigned)(h * kHalf * a.K * 2 + s * (kC * 2));
-        load_lds<true>(pbase, pbytes, dst + q * 1024, ((nchunk ^ q) << 3) < len - kC * s ? off : kOob);
-      }
+      const unsigned at = (unsigned)(h * kHalf * a.K * 2 + s * (kC * 2));
+      load_lds<true>(pbase, pbytes, dst, nchunk(lane) << 3 < len - kC * s ? poff[0] + at : kOob);
+      load_lds<true>(pbase, pbytes, dst + 1024, (nchunk(lane) ^ 1) << 3 < len - kC * s ? poff[1] + at : kOob);
     }
-  };
-  auto issue_q = [&](int h, int s, int b) {
-    lds_u8* dst = q_slot(h, b) + wave * 2048;
+  }
+  __device__ __forceinline__ void issue_q(lds_u8* dst, int h, int lane) const {
     if constexpr (kTransQ) {
       tq.issue(dst, h);
     } else {
-#pragma unroll
-      for (int q = 0; q < 2; ++q)
-        load_lds<!kTransP>(qbase, kOob, dst + q * 1024,
-                 ((nchunk ^ q) << 3) < len - kC * s ? qoff[h][q] + (unsigned)(s * (kC * 2)) : kOob);
+      const u32x2 o = HALF || h == 0 ? qoff0 : qoff1;
+      const unsigned at = (unsigned)(s * (kC * 2));
+      load_lds<!kTransP>(qbase, kOob, dst, nchunk(lane) << 3 < len - kC * s ? o[0] + at : kOob);
+      load_lds<!kTransP>(qbase, kOob, dst + 1024, (nchunk(lane) ^ 1) << 3 < len - kC * s ? o[1] + at : kOob);
+    }
+  }
+};
+
+// LDS address of a lane's transpose read of 32 indices from idx0 on, at kk = 0.
+__device__ __forceinline__ int trans_at(int idx0, int lane) {
+  const int r = 8 * (lane >> 5) + ((lane & 15) >> 2);  // its row of the step's 64
+  const int chunk = idx0 / 8 + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
+  return r * 256 + ((chunk ^ (4 * (r & 3))) << 4) + 8 * (lane & 1);
+}
+__device__ __forceinline__ int natural_at(int idx0, int lane) {
+  return (idx0 + (lane & 31)) * 128 + (((lane >> 5) ^ pf_mix(lane & 31)) << 4);
+}
+// Eight c of one index per lane: rows r..r+3 and r+4..r+7 of the transposed half.
+__device__ __forceinline__ u32x4 tr_frag(const lds_u8* p) {
+  const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)p);
+  const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + 4 * 256));
+  const u32x2 l = __builtin_bit_cast(u32x2, lo), g = __builtin_bit_cast(u32x2, hi);
+  return u32x4{l[0], l[1], g[0], g[1]};
+}
+
+// Where a tile's result row q goes: nullptr for a row that is not written.
+template <int OP, bool F32>
+__device__ __forceinline__ uint8_t* out_row(const TileArgs& a, const Tile& t, int q) {
+  constexpr int kEsz = F32 ? 4 : 2;
+  if constexpr (OP == 2) {
+    if (t.q0 + q >= a.N) return nullptr;
+    return a.dw + ((int64_t)t.e * a.N + t.q0 + q) * a.K * kEsz;
+  } else {
+    const int m = t.q0 + q < t.hi ? row_of(a.out, t.q0 + q) : -1;
+    return m < 0 ? nullptr : a.out.p + (int64_t)m * a.out.stride * kEsz;
+  }
+}
+
+// All tiles of one kind (HALF: at most 128 q) of a workgroup: items(u, &tile)
+// moves u to the next item from u on, or returns false.
+template <int OP, bool F32, bool ACC, bool HALF, typename Items>
+__device__ __forceinline__ void run_tiles(const TileArgs& a, lds_u8* smem, int& u, const Items& items) {
+  constexpr bool kTransP = OP != 0, kTransQ = OP == 2;
+  constexpr int kReadsP = kTransP ? 16 : 8, kReadsQ = kTransQ ? 8 : 4;  // LDS reads of a half
+  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+  const int wr = wave >> 2, wc = wave & 3;
+  const int width = OP == 0 ? a.N : a.K;  // of p
+  Tile t;
+  if (!items(u, &t)) return;
+  Loads<OP, HALF> L;
+  Tile lt = t;  // the loads' tile
+  int lu = u;
+  L.init(a, wave, lane);
+  // A tile without steps (a weight gradient of an expert without rows) has no loads.
+  auto load_tile = [&](bool have) {
+    while (have && contraction<OP>(a, lt) == 0) {
+      lu += slots();
+      have = items(lu, &lt);
+    }
+    if (have)
+      L.tile(a, lt, wave, lane);
+    else
+      L.end();
+  };
+  auto load_next = [&] {
+    if (L.s + 1 < L.nk) {
+      L.step(wave, lane);
+    } else {
+      lu += slots();
+      load_tile(items(lu, &lt));
     }
   };
+  auto issue_p = [&](int h, int b) { L.issue_p(a, smem + (2 * h + b) * kPiece + wave * 2048, h, lane); };
+  auto issue_q = [&](int h, int b) { L.issue_q(smem + (4 + 2 * h + b) * kPiece + wave * 2048, h, lane); };
 
-  // ---- fragments: index base + 32*tile + lane%32, c = 16*kk + 8*(lane/32)..+7
-  const int fr = lane & 31, hl = lane >> 5;
-  auto trans_at = [&](int idx0) {
-    const int r = 8 * hl + ((lane & 15) >> 2);  // its row of the step's 64, at kk = 0
-    const int chunk = idx0 / 8 + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
-    return r * 256 + ((chunk ^ (4 * (r & 3))) << 4) + 8 * (lane & 1);
-  };
-  // address at kk = 0 (natural: kk k flips bits 5 and 6 of it; transposed: kk
-  // is a constant offset, tile 1 flips bit 6)
-  int pa = kTransP ? trans_at(64 * wr) : (64 * wr + fr) * 128 + ((hl ^ pf_mix(fr)) << 4);
-  int qa = kTransQ ? trans_at(32 * wc) : (32 * wc + fr) * 128 + ((hl ^ pf_mix(fr)) << 4);
-  auto tr_frag = [&](const lds_u8* p) {  // rows r..r+3 and r+4..r+7 of one index each
-    const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)p);
-    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + 4 * 256));
-    const u32x2 l = __builtin_bit_cast(u32x2, lo), g = __builtin_bit_cast(u32x2, hi);
-    return u32x4{l[0], l[1], g[0], g[1]};
-  };
-  // the empty asm keeps the compiler from holding every flipped address in a
-  // register of its own across the loop
+  // Fragments: index base + 32*tile + lane%32, c = 16*kk + 8*(lane/32)..+7.
+  // Natural: kk flips bits 5 and 6 of the address; transposed: kk is a constant
+  // offset, tile 1 flips bit 6.  The empty asm keeps the compiler from holding
+  // every flipped address in a register of its own across the loop.
+  int pa = kTransP ? trans_at(64 * wr, lane) : natural_at(64 * wr, lane);
+  int qa = kTransQ ? trans_at(32 * wc, lane) : natural_at(32 * wc, lane);
   auto read_p = [&](u32x4 (&f)[2][4], int h, int b) {
-    const lds_u8* s = p_slot(h, b);
+    const lds_u8* s = smem + (2 * h + b) * kPiece;
     asm volatile("" : "+v"(pa));
 #pragma unroll
     for (int kk = 0; kk < 4; ++kk)
 #pragma unroll
       for (int i = 0; i < 2; ++i)
-        f[i][kk] = kTransP ? tr_frag(s + (pa ^ (64 * i)) + kk * 4096) : *(const lds_u32x4*)(s + (pa ^ (32 * kk)) + i * 4096);
+        f[i][kk] = kTransP ? tr_frag(s + (pa ^ (64 * i)) + kk * 4096)
+                           : *(const lds_u32x4*)(s + (pa ^ (32 * kk)) + i * 4096);
   };
   auto read_q = [&](u32x4 (&f)[4], int h, int b) {
-    const lds_u8* s = q_slot(h, b);
+    const lds_u8* s = smem + (4 + 2 * h + b) * kPiece;
     asm volatile("" : "+v"(qa));
 #pragma unroll
     for (int kk = 0; kk < 4; ++kk)
@@ -320,15 +423,16 @@ __device__ __forceinline__ void tile_product(const TileArgs& a, const Tile t, ld
   };
 
   f32x16 acc[2][HALF ? 1 : 2][2];  // [P half][Q half][tile]
+  auto clear = [&] {
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < 2; ++i)
 #pragma unroll
-    for (int j = 0; j < (HALF ? 1 : 2); ++j)
+      for (int j = 0; j < (HALF ? 1 : 2); ++j)
 #pragma unroll
-      for (int k = 0; k < 2; ++k)
+        for (int k = 0; k < 2; ++k)
 #pragma unroll
-        for (int v = 0; v < 16; ++v) acc[i][j][k][v] = 0.0f;
-  constexpr int kReadsP = kTransP ? 16 : 8, kReadsQ = kTransQ ? 8 : 4;  // LDS reads of a half
+          for (int v = 0; v < 16; ++v) acc[i][j][k][v] = 0.0f;
+  };
   u32x4 A0[2][4], A1[2][4], F0[4], F1[4];
   auto mma = [&](f32x16 (&c)[2], const u32x4 (&p)[2][4], const u32x4 (&q)[4]) {
 #pragma unroll
@@ -336,221 +440,321 @@ __device__ __forceinline__ void tile_product(const TileArgs& a, const Tile t, ld
 #pragma unroll
       for (int i = 0; i < 2; ++i) c[i] = mfma32_bf16(p[i][kk], q[kk], c[i]);
   };
+  auto fence = [] { __builtin_amdgcn_sched_barrier(0); };
+  // A phase waits until at most the loads of the last six phases (HALF: the
+  // last three halves) are outstanding: those it is about to read were issued
+  // before.
+  constexpr int kAhead = HALF ? 6 : 12;
+  auto begin = [] { phase_begin<kAhead>(); };
 
-  if (nk > 0) {
+  // The order of all issues, by step: P0, Q0, Q1, P1 (HALF: P0, Q0, P1).
+  load_tile(true);
+  issue_p(0, 0);
+  issue_q(0, 0);
+  if constexpr (!HALF) issue_q(1, 0);
+  issue_p(1, 0);
+  load_next();
+  issue_p(0, 1);
+  issue_q(0, 1);
+  if constexpr (!HALF) issue_q(1, 1);
+  if constexpr (!HALF) {
+    issue_p(1, 1);
+    load_next();
+  }
+  begin();
+  read_p(A0, 0, 0);
+  read_q(F0, 0, 0);
+  ring_barrier();
+  if constexpr (HALF)
+    issue_p(1, 1);
+  else
+    issue_p(0, 0);
+  // X holds Q half 0 of the step on entry; Y takes half 1, then half 0 of the next step
+  auto step = [&](auto bt, u32x4 (&X)[4], u32x4 (&Y)[4]) {
+    constexpr int b = decltype(bt)::value;
     if constexpr (!HALF) {
-      // A phase at time t waits until at most the loads of the last six phases
-      // are outstanding: those it is about to read were issued seven phases ago.
-      auto begin = [] { phase_begin<12>(); };
-      auto fence = [] { __builtin_amdgcn_sched_barrier(0); };
-      step_p(0);
-      issue_p(0, 0, 0);
-      step_q(0);
-      issue_q(0, 0, 0);
-      issue_q(1, 0, 0);
-      issue_p(1, 0, 0);
-      step_p(1);
-      issue_p(0, 1, 1);
-      step_q(1);
-      issue_q(0, 1, 1);
-      issue_q(1, 1, 1);
-      issue_p(1, 1, 1);
       begin();
-      read_p(A0, 0, 0);
-      read_q(F0, 0, 0);
-      ring_barrier();
-      step_p(2);
-      issue_p(0, 2, 0);
-      // X holds Q half 0 of the step on entry; Y takes half 1, then half 0 of the next step
-      auto step = [&](int s, auto bt, u32x4 (&X)[4], u32x4 (&Y)[4]) {
-        constexpr int b = decltype(bt)::value;
-        begin();
-        fence();
-        read_q(Y, 1, b);
-        step_q(s + 2);
-        issue_q(0, s + 2, b);
-        mma(acc[0][0], A0, X);
-        interleave<8, kReadsQ, 2, 4 * b>();
-        fence();
-        begin();
-        fence();
-        read_p(A1, 1, b);
-        issue_q(1, s + 2, b);
-        mma(acc[0][HALF ? 0 : 1], A0, Y);
-        interleave<8, kReadsP, 2, 4 * b + 1>();
-        fence();
-        begin();
-        fence();
-        read_p(A0, 0, b ^ 1);
-        issue_p(1, s + 2, b);
-        mma(acc[1][HALF ? 0 : 1], A1, Y);
-        interleave<8, kReadsP, 2, 4 * b + 2>();
-        fence();
-        begin();
-        fence();
-        read_q(Y, 0, b ^ 1);
-        step_p(s + 3);
-        issue_p(0, s + 3, b ^ 1);
-        mma(acc[1][0], A1, X);
-        interleave<8, kReadsQ, 2, 4 * b + 3>();
-        fence();
-      };
-      for (int s = 0; s < nk; s += 2) {
-        step(s, std::integral_constant<int, 0>{}, F0, F1);
-        if (s + 1 >= nk) break;
-        step(s + 1, std::integral_constant<int, 1>{}, F1, F0);
-      }
+      fence();
+      read_q(Y, 1, b);
+      issue_q(0, b);
+      mma(acc[0][0], A0, X);
+      interleave<8, kReadsQ, 2, 4 * b>();
+      fence();
+      begin();
+      fence();
+      read_p(A1, 1, b);
+      issue_q(1, b);
+      mma(acc[0][HALF ? 0 : 1], A0, Y);
+      interleave<8, kReadsP, 2, 4 * b + 1>();
+      fence();
+      begin();
+      fence();
+      read_p(A0, 0, b ^ 1);
+      issue_p(1, b);
+      mma(acc[1][HALF ? 0 : 1], A1, Y);
+      interleave<8, kReadsP, 2, 4 * b + 2>();
+      fence();
+      load_next();
+      begin();
+      fence();
+      read_q(Y, 0, b ^ 1);
+      issue_p(0, b ^ 1);
+      mma(acc[1][0], A1, X);
+      interleave<8, kReadsQ, 2, 4 * b + 3>();
+      fence();
     } else {
-      // At most 128 q: two phases per step, P half 1 is read in the first, P
-      // half 0 and Q of the next step in the second.
-      auto begin = [] { phase_begin<6>(); };
-      auto fence = [] { __builtin_amdgcn_sched_barrier(0); };
-      step_p(0);
-      issue_p(0, 0, 0);
-      step_q(0);
-      issue_q(0, 0, 0);
-      issue_p(1, 0, 0);
-      step_p(1);
-      issue_p(0, 1, 1);
-      step_q(1);
-      issue_q(0, 1, 1);
+      load_next();
       begin();
-      read_p(A0, 0, 0);
-      read_q(F0, 0, 0);
-      ring_barrier();
-      // the order of all later issues: P1(1), then P0(2) Q0(2), P1(2), ...
-      issue_p(1, 1, 1);
-      auto step = [&](int s, auto bt, u32x4 (&X)[4], u32x4 (&Y)[4]) {
-        constexpr int b = decltype(bt)::value;
-        begin();
-        fence();
-        read_p(A1, 1, b);
-        step_p(s + 2);
-        issue_p(0, s + 2, b);
-        step_q(s + 2);
-        issue_q(0, s + 2, b);
-        mma(acc[0][0], A0, X);
-        interleave<8, kReadsP, 4, 8 + 2 * b>();
-        fence();
-        begin();
-        fence();
-        read_p(A0, 0, b ^ 1);
-        read_q(Y, 0, b ^ 1);
-        issue_p(1, s + 2, b);
-        mma(acc[1][0], A1, X);
-        interleave<8, kReadsP + kReadsQ, 2, 9 + 2 * b>();
-        fence();
-      };
-      for (int s = 0; s < nk; s += 2) {
-        step(s, std::integral_constant<int, 0>{}, F0, F1);
-        if (s + 1 >= nk) break;
-        step(s + 1, std::integral_constant<int, 1>{}, F1, F0);
-      }
+      fence();
+      read_p(A1, 1, b);
+      issue_p(0, b);
+      issue_q(0, b);
+      mma(acc[0][0], A0, X);
+      interleave<8, kReadsP, 4, 8 + 2 * b>();
+      fence();
+      begin();
+      fence();
+      read_p(A0, 0, b ^ 1);
+      read_q(Y, 0, b ^ 1);
+      issue_p(1, b);
+      mma(acc[1][0], A1, X);
+      interleave<8, kReadsP + kReadsQ, 2, 9 + 2 * b>();
+      fence();
     }
-    phase_begin<0>();  // the loads past the last step (zeros) still write LDS
-  }
+  };
 
-  // ---- epilogue: each wave transposes its 64 p x 32 q of a quadrant through
-  // its own LDS, so that a store writes whole 128-byte lines of a result row.
-  const int rows = OP == 2 ? a.N - t.q0 : t.hi - t.q0;  // valid q
-  lds_u8* ep = smem + wave * 8192;
-  int el = (int)__builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, 0u));  // the lane, again: nothing lives
-  asm volatile("" : "+v"(el));                                                         // across the loop for this part
-  const int ef = el & 31, eh = el >> 5;
-#pragma unroll
-  for (int j = 0; j < (HALF ? 1 : 2); ++j) {
-    const int qb = kHalf * j + 32 * wc;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int pb = t.p0 + kHalf * i + 64 * wr;
-#pragma unroll
-      for (int k = 0; k < 2; ++k)
-#pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          const f32x16& c = acc[i][j][k];
-          const f32x4 v = {c[4 * g], c[4 * g + 1], c[4 * g + 2], c[4 * g + 3]};
-          if constexpr (F32)
-            *(lds_f32x4*)(ep + ef * 256 + (((8 * k + 2 * g + eh) ^ (ef & 15)) << 4)) = v;
-          else
-            *(lds_u32x2*)(ep + ef * 128 + (((4 * k + g) ^ pf_mix(ef)) << 4) + 8 * eh) =
-                u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
-        }
-      constexpr int kLanes = F32 ? 16 : 8;   // lanes of a result row
-      constexpr int kRows = 64 / kLanes;     // rows per store
+  while (true) {
+    const int nk = steps_of(contraction<OP>(a, t));
+    clear();
+    for (int s = 0; s < nk; s += 2) {
+      step(std::integral_constant<int, 0>{}, F0, F1);
+      step(std::integral_constant<int, 1>{}, F1, F0);
+    }
+    // Epilogue: each wave transposes its 64 p x 32 q of a quadrant through its
+    // own 2 KB beside the ring, so that a store writes whole 128-byte lines of a
+    // result row: 16 (bf16) or 8 (fp32) q at a time.
+    if (!(ACC && nk == 0)) {
+      int el = (int)__builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, 0u));  // the lane, again: nothing
+      asm volatile("" : "+v"(el));                                                         // lives across the loop
+      const int ef = el & 31, eh = el >> 5;
+      lds_u8* ep = smem + kRing + wave * kEpi;
+      constexpr int kQ = F32 ? 8 : 16;      // q rows at a time
+      constexpr int kRowB = kEpi / kQ;      // their bytes
+      constexpr int kLanes = kRowB / 16;    // lanes of a result row
       const int rl = el / kLanes, cl = el % kLanes;
-      const int p = pb + cl * (F32 ? 4 : 8);
 #pragma unroll
-      for (int rr = 0; rr < 32 / kRows; ++rr) {
-        const int x = kRows * rr + rl, q = qb + x;
-        const u32x4 v = *(const lds_u32x4*)(ep + x * (F32 ? 256 : 128) + ((cl ^ (F32 ? x & 15 : pf_mix(x))) << 4));
-        if (q >= rows || p >= width) continue;
-        if constexpr (OP == 2) {
-          u32x4* o = (u32x4*)(a.dw + (((int64_t)t.e * a.N + t.q0 + q) * a.K + p) * (F32 ? 4 : 2));
-          if constexpr (ACC) {
-            const f32x4 s = *(const f32x4*)o + __builtin_bit_cast(f32x4, v);
-            *(f32x4*)o = s;
-          } else {
-            *o = v;
+      for (int j = 0; j < (HALF ? 1 : 2); ++j)
+#pragma unroll
+        for (int z = 0; z < 32 / kQ; ++z)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            if (ef / kQ == z) {
+              const int x = ef % kQ;
+#pragma unroll
+              for (int k = 0; k < 2; ++k)
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                  const f32x16& c = acc[i][j][k];
+                  const f32x4 v = {c[4 * g], c[4 * g + 1], c[4 * g + 2], c[4 * g + 3]};
+                  if constexpr (F32)
+                    *(lds_f32x4*)(ep + x * kRowB + (((8 * k + 2 * g + eh) ^ x) << 4)) = v;
+                  else
+                    *(lds_u32x2*)(ep + x * kRowB + (((4 * k + g) ^ (x & 7)) << 4) + 8 * eh) =
+                        u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+                }
+            }
+            wave_exchange();
+            const int p = t.p0 + kHalf * i + 64 * wr + cl * (F32 ? 4 : 8);
+#pragma unroll
+            for (int rr = 0; rr < kQ * kLanes / 64; ++rr) {
+              const int x = (64 / kLanes) * rr + rl;
+              const u32x4 v = *(const lds_u32x4*)(ep + x * kRowB + ((cl ^ (F32 ? x : x & 7)) << 4));
+              uint8_t* o = out_row<OP, F32>(a, t, kHalf * j + 32 * wc + kQ * z + x);
+              if (o && p < width) {
+                u32x4* at = (u32x4*)(o + (int64_t)p * (F32 ? 4 : 2));
+                if constexpr (ACC)
+                  *(f32x4*)at = *(const f32x4*)at + __builtin_bit_cast(f32x4, v);
+                else
+                  *at = v;
+              }
+            }
+            wave_exchange();
           }
-        } else {
-          const int m = row_of(a.out, t.q0 + q);
-          if (m >= 0) *(u32x4*)(a.out.p + ((int64_t)m * a.out.stride + p) * (F32 ? 4 : 2)) = v;
-        }
-      }
     }
+    u += slots();
+    if (!items(u, &t)) break;
+  }
+  phase_begin<0>();  // the loads past the last tile (zeros) still write LDS
+}
+
+// Tiles of at most 64 q: 128 p x 64 q, five steps of 24 KB in a ring, four of
+// them in flight.  Wave w owns 32 p (w%4) x 32 q (w/4).
+constexpr int kSmallQ = 64;
+constexpr int kSmallStages = 5;
+constexpr int kSmallStage = kPiece + kSmallQ * kC * 2;
+static_assert(kSmallStages * kSmallStage <= kRing, "the small tiles' ring");
+
+template <int OP, bool F32, typename Items>
+__device__ __forceinline__ void run_small(const TileArgs& a, lds_u8* smem, int& u, const Items& items) {
+  constexpr bool kTransP = OP != 0;
+  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+  const int wp = wave & 3, wq = wave >> 2;
+  const int width = OP == 0 ? a.N : a.K, len = OP == 0 ? a.K : a.N;
+  const int nk = (len + kC - 1) / kC;
+  Loads<OP, true> L;
+  L.init(a, wave, lane);
+  const int pa = kTransP ? trans_at(32 * wp, lane) : natural_at(32 * wp, lane);
+  const int qa = natural_at(32 * wq, lane);
+  const int qc = (lane & 7) ^ (lane >> 3) ^ (wave & 1);  // chunk of Q row 8w + lane/8
+  for (Tile t; items(u, &t); u += slots()) {
+    L.tile(a, t, wave, lane);
+    if constexpr (OP == 0) L.pbytes = extent(min(kHalf, a.N - t.p0), (int64_t)a.K * 2, (int64_t)a.K * 2);
+    const unsigned qoff = L.row_offset(a, t, 8 * wave + (lane >> 3), qc);
+    auto issue = [&](int stage) {  // step L.s, then on to the next
+      lds_u8* dst = smem + stage * kSmallStage;
+      L.issue_p(a, dst + wave * 2048, 0, lane);
+      load_lds<!kTransP>(L.qbase, kOob, dst + kPiece + wave * 1024,
+                         qc << 3 < len - kC * L.s ? qoff + (unsigned)(L.s * (kC * 2)) : kOob);
+      L.step(wave, lane);
+    };
+    f32x16 acc;
+#pragma unroll
+    for (int v = 0; v < 16; ++v) acc[v] = 0.0f;
+    for (int i = 0; i < kSmallStages - 1; ++i) issue(i);
+    int stage = 0;
+    for (int s = 0; s < nk; ++s) {
+      phase_begin<3 * (kSmallStages - 2)>();
+      const lds_u8* at = smem + stage * kSmallStage;
+      u32x4 p[4], q[4];
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk) {
+        p[kk] = kTransP ? tr_frag(at + pa + kk * 4096) : *(const lds_u32x4*)(at + (pa ^ (32 * kk)));
+        q[kk] = *(const lds_u32x4*)(at + kPiece + (qa ^ (32 * kk)));
+      }
+      issue(stage == 0 ? kSmallStages - 1 : stage - 1);  // the slot whose reads the barrier ended
+      stage = stage == kSmallStages - 1 ? 0 : stage + 1;
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk) acc = mfma32_bf16(p[kk], q[kk], acc);
+    }
+    phase_begin<0>();  // the loads past the last step (zeros)
+    uint8_t* o = out_row<OP, F32>(a, t, 32 * wq + (lane & 31));
+    if (o)
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const int p = t.p0 + 32 * wp + 8 * g + 4 * (lane >> 5);
+        if (p >= width) continue;
+        const f32x4 v = {acc[4 * g], acc[4 * g + 1], acc[4 * g + 2], acc[4 * g + 3]};
+        if constexpr (F32)
+          *(f32x4*)(o + (int64_t)p * 4) = v;
+        else
+          *(u32x2*)(o + (int64_t)p * 2) = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+      }
   }
 }
 
-// Row tile and p tile of grid position (XCD, index in XCD): row tiles are
-// numbered expert by expert; an XCD takes an eighth of all tiles, in groups of
-// four row tiles, p tiles outer, so that the ~32 workgroups that run together
-// on an XCD share operands in its L2.
-__device__ __forceinline__ bool map_tile(int NT, int PT, int* rt, int* pt) {
-  const int T = NT * PT, per = (T + 7) >> 3, x = blockIdx.x & 7, j = blockIdx.x >> 3;
-  const int L = x * per + j;
-  if (j >= per || L >= T) return false;
-  const int g = L / (4 * PT), r = L - g * 4 * PT, n = min(4, NT - 4 * g);
-  *rt = 4 * g + r % n;
-  *pt = r / n;
-  return true;
+// Tiles of an expert with n rows: whole ones, and the kind of the rest.
+__device__ __forceinline__ int full_tiles(int n) { return n / kTile + (n % kTile > kHalf); }
+__device__ __forceinline__ bool half_tile(int n) { return n % kTile > kSmallQ && n % kTile <= kHalf; }
+__device__ __forceinline__ bool small_tile(int n) { return n % kTile > 0 && n % kTile <= kSmallQ; }
+
+typedef __attribute__((address_space(3))) int lds_int;
+
+// Number of the E inclusive prefix sums tab[0..E) (shifted and masked) that are
+// at most v: the expert of item v.
+__device__ __forceinline__ int expert_of(const lds_int* tab, int E, int shift, int mask, int v, int lane) {
+  int e = 0;
+  for (int i = 0; i < E; i += 64) {
+    const bool le = i + lane < E && ((tab[i + lane] >> shift) & mask) <= v;
+    e += __popcll(__ballot(le));
+  }
+  return uniform(e);
 }
 
+// Product and input gradient.  Row tiles are numbered expert by expert, each
+// kind on its own; an XCD takes an eighth of a kind's tiles, whole ones and
+// halves in groups of four row tiles with p tiles outer, so that the ~32
+// workgroups that run together on an XCD share operands in its L2.
 template <int OP, bool F32>
 __global__ __launch_bounds__(kThreads) void grouped_rows_kernel(TileArgs a) {
   extern __shared__ __align__(16) uint8_t smem_raw[];
   lds_u8* smem = (lds_u8*)smem_raw;
-  // thread e: the row tiles of expert e, and their prefix sum
-  __attribute__((address_space(3))) int* sc = (__attribute__((address_space(3))) int*)smem;
-  const int tid = threadIdx.x, wave = tid >> 6;
-  int lo = 0, hi = 0;
-  if (tid < a.E) group_range(a.offsets, tid, a.R, &lo, &hi);
-  const int nt = (hi - lo + kTile - 1) / kTile;
-  const int incl = wave_incl_scan(nt);
-  if ((tid & 63) == 63) sc[wave] = incl;
-  __syncthreads();
-  int before = incl - nt, NT = 0;
+  lds_int* full = (lds_int*)(smem + kTable);  // [E] inclusive sums of whole tiles
+  lds_int* rest = full + kMaxExperts;         // [E] of half tiles, and << 16 of small ones
+  lds_int* part = rest + kMaxExperts;
+  {
+    const int tid = threadIdx.x, wave = tid >> 6;
+    int lo = 0, hi = 0;
+    if (tid < a.E) group_range(a.offsets, tid, a.R, &lo, &hi);
+    const int f = full_tiles(hi - lo), r = (half_tile(hi - lo) ? 1 : 0) + (small_tile(hi - lo) ? 1 << 16 : 0);
+    int fi = wave_incl_scan(f), ri = wave_incl_scan(r);
+    if ((tid & 63) == 63) {
+      part[wave] = fi;
+      part[8 + wave] = ri;
+    }
+    __syncthreads();
 #pragma unroll
-  for (int w = 0; w < 8; ++w) {
-    const int v = sc[w];
-    before += w < wave ? v : 0;
-    NT += v;
+    for (int w = 0; w < 8; ++w) {
+      fi += w < wave ? part[w] : 0;
+      ri += w < wave ? part[8 + w] : 0;
+    }
+    full[tid] = fi;
+    rest[tid] = ri;
+    __syncthreads();
   }
-  const int PT = ((OP == 0 ? a.N : a.K) + kTile - 1) / kTile;
-  int rt, pt;
-  if (!map_tile(uniform(NT), PT, &rt, &pt)) return;
-  if (rt >= before && rt < before + nt) {
-    sc[8] = tid;
-    sc[9] = lo;
-    sc[10] = hi;
-    sc[11] = lo + (rt - before) * kTile;
-  }
-  __syncthreads();
-  const Tile t = {uniform(sc[8]), uniform(sc[9]), uniform(sc[10]), uniform(sc[11]), pt * kTile};
-  __syncthreads();
-  if (t.hi - t.q0 <= kHalf)
-    tile_product<OP, F32, false, true>(a, t, smem);
-  else
-    tile_product<OP, F32, false, false>(a, t, smem);
+  const int NF = uniform(full[a.E - 1]), NR = uniform(rest[a.E - 1]), NH = NR & 0xffff, NS = NR >> 16;
+  const int width = OP == 0 ? a.N : a.K;
+  const int PT = (width + kTile - 1) / kTile, PS = (width + kHalf - 1) / kHalf;
+  const int x = blockIdx.x & 7;
+  const int lane = threadIdx.x & 63;
+  // items of this XCD: [0, nf) whole tiles, [nf, nf + nh) halves, then small ones
+  const int nf = (NF * PT + 7) >> 3, nh = (NH * PT + 7) >> 3, ns = (NS * PS + 7) >> 3;
+  const __attribute__((address_space(4))) int32_t* offsets = (const __attribute__((address_space(4))) int32_t*)a.offsets;
+  auto range = [&](Tile* t) {  // of expert t->e, by scalar loads
+    const int lo = min(max(offsets[t->e], 0), a.R);
+    t->lo = lo;
+    t->hi = min(max(offsets[t->e + 1], lo), a.R);
+  };
+  auto raster = [&](int n, int rows, int j, int* rt, int* pt) {  // item j of this XCD's n
+    const int i = x * n + j;
+    if (j >= n || i >= rows * PT) return false;
+    const int g = i / (4 * PT), r = i - g * 4 * PT, m = min(4, rows - 4 * g);
+    *rt = 4 * g + r % m;
+    *pt = r / m;
+    return true;
+  };
+  auto whole = [&](int& u, Tile* t) {
+    int rt, pt;
+    if (u >= nf || !raster(nf, NF, u, &rt, &pt)) return false;
+    t->e = expert_of(full, a.E, 0, -1, rt, lane);
+    range(t);
+    t->q0 = t->lo + (rt - (uniform(full[t->e]) - full_tiles(t->hi - t->lo))) * kTile;
+    t->p0 = pt * kTile;
+    return true;
+  };
+  auto half = [&](int& u, Tile* t) {
+    int rt, pt;
+    if (u >= nf + nh || !raster(nh, NH, u - nf, &rt, &pt)) return false;
+    t->e = expert_of(rest, a.E, 0, 0xffff, rt, lane);
+    range(t);
+    t->q0 = t->lo + full_tiles(t->hi - t->lo) * kTile;
+    t->p0 = pt * kTile;
+    return true;
+  };
+  auto small = [&](int& u, Tile* t) {
+    const int j = u - nf - nh, i = x * ns + j;
+    if (j >= ns || i >= NS * PS) return false;
+    t->e = expert_of(rest, a.E, 16, 0xffff, i / PS, lane);
+    range(t);
+    t->q0 = t->lo + full_tiles(t->hi - t->lo) * kTile;
+    t->p0 = i % PS * kHalf;
+    return true;
+  };
+  int u = blockIdx.x >> 3;
+  run_tiles<OP, F32, false, false>(a, smem, u, whole);
+  while (u < nf) u += slots();  // an XCD's last items can be missing
+  run_tiles<OP, F32, false, true>(a, smem, u, half);
+  while (u < nf + nh) u += slots();
+  run_small<OP, F32>(a, smem, u, small);
 }
 
 // Weight gradient: the tiles of an expert are split over the XCDs (experts
@@ -559,28 +763,45 @@ __global__ __launch_bounds__(kThreads) void grouped_rows_kernel(TileArgs a) {
 template <bool F32, bool ACC>
 __global__ __launch_bounds__(kThreads) void grouped_wgrad_kernel(TileArgs a) {
   extern __shared__ __align__(16) uint8_t smem_raw[];
-  const int QT = (a.N + kTile - 1) / kTile, PT = (a.K + kTile - 1) / kTile, T = QT * PT;
-  const int x = blockIdx.x & 7, j = blockIdx.x >> 3;
-  int e, i;
-  if (T >= 16) {
-    const int per = (T + 7) >> 3;
-    e = j / per;
-    i = x * per + j % per;
-  } else {
-    e = (int)blockIdx.x / T;
-    i = (int)blockIdx.x % T;
-  }
-  if (e >= a.E || i >= T) return;
-  const int g = i / (4 * PT), r = i - g * 4 * PT, n = min(4, QT - 4 * g);
-  Tile t = {e, 0, 0, (4 * g + r % n) * kTile, (r / n) * kTile};
-  group_range(a.offsets, e, a.R, &t.lo, &t.hi);
-  t.lo = uniform(t.lo);
-  t.hi = uniform(t.hi);
-  if (ACC && t.lo == t.hi) return;
-  if (a.N - t.q0 <= kHalf)
-    tile_product<2, F32, ACC, true>(a, t, (lds_u8*)smem_raw);
-  else
-    tile_product<2, F32, ACC, false>(a, t, (lds_u8*)smem_raw);
+  lds_u8* smem = (lds_u8*)smem_raw;
+  const bool last_half = a.N % kTile > 0 && a.N % kTile <= kHalf;  // the last q tile is a half
+  const int QT = (a.N + kTile - 1) / kTile - last_half, PT = (a.K + kTile - 1) / kTile;
+  const int x = blockIdx.x & 7;
+  const __attribute__((address_space(4))) int32_t* offsets = (const __attribute__((address_space(4))) int32_t*)a.offsets;
+  auto range = [&](Tile* t) {
+    const int lo = min(max(offsets[t->e], 0), a.R);
+    t->lo = lo;
+    t->hi = min(max(offsets[t->e + 1], lo), a.R);
+  };
+  const int T = QT * PT, per = (T + 7) >> 3;
+  const int nf = T >= 16 ? per * a.E : (T * a.E + 7) >> 3, nh = last_half ? (PT * a.E + 7) >> 3 : 0;
+  auto whole = [&](int& u, Tile* t) {
+    for (; u < nf; u += slots()) {
+      const int e = T >= 16 ? u / per : (u * 8 + x) / max(T, 1);
+      const int i = T >= 16 ? x * per + u % per : (u * 8 + x) % max(T, 1);
+      if (i >= T || e >= a.E) continue;
+      const int g = i / (4 * PT), r = i - g * 4 * PT, n = min(4, QT - 4 * g);
+      t->e = e;
+      t->q0 = (4 * g + r % n) * kTile;
+      t->p0 = (r / n) * kTile;
+      range(t);
+      return true;
+    }
+    return false;
+  };
+  auto half = [&](int& u, Tile* t) {
+    const int i = (u - nf) * 8 + x;
+    if (u >= nf + nh || i >= PT * a.E) return false;
+    t->e = i / PT;
+    t->q0 = QT * kTile;
+    t->p0 = i % PT * kTile;
+    range(t);
+    return true;
+  };
+  int u = blockIdx.x >> 3;
+  run_tiles<2, F32, ACC, false>(a, smem, u, whole);
+  while (u < nf) u += slots();
+  run_tiles<2, F32, ACC, true>(a, smem, u, half);
 }
 
 // Launch with kLds bytes of dynamic LDS; the kernel's ceiling is raised once
@@ -614,6 +835,14 @@ int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 }  // namespace
 
+namespace {
+
+// One workgroup per CU: kSlots on each of the eight XCDs, fewer where there are
+// fewer tiles than that.
+int64_t persistent_grid(int64_t tiles) { return 8 * (cdiv(tiles, 8) < kSlots ? cdiv(tiles, 8) : kSlots); }
+
+}  // namespace
+
 bool launch_grouped_tile(bool dgrad, bool f32, hipStream_t st, const GroupedArgs& a) {
   TileArgs t = {};
   t.R = a.R;
@@ -624,9 +853,9 @@ bool launch_grouped_tile(bool dgrad, bool f32, hipStream_t st, const GroupedArgs
   t.q = a.in;
   t.w = a.w;
   t.out = a.out;
-  // row tiles: at most R/256 whole ones and one more per expert that holds rows
+  // at most R/256 whole row tiles and one rest per expert that holds rows
   const int64_t rows = a.R / kTile + (a.R < a.E ? a.R : a.E);
-  const int64_t grid = 8 * cdiv(rows * cdiv(dgrad ? a.K : a.N, kTile), 8);
+  const int64_t grid = persistent_grid(rows * cdiv(dgrad ? a.K : a.N, kHalf));
   if (dgrad) return f32 ? launch_rows<1, true>(grid, st, t) : launch_rows<1, false>(grid, st, t);
   return f32 ? launch_rows<0, true>(grid, st, t) : launch_rows<0, false>(grid, st, t);
 }
@@ -641,8 +870,7 @@ bool launch_grouped_wgrad(bool f32, bool accumulate, hipStream_t st, const Group
   t.q = a.dy;
   t.p = a.in;
   t.dw = a.dw;
-  const int64_t tiles = cdiv(a.N, kTile) * cdiv(a.K, kTile);
-  const int64_t grid = tiles >= 16 ? 8 * cdiv(tiles, 8) * a.E : 8 * cdiv(tiles * a.E, 8);
+  const int64_t grid = persistent_grid(cdiv(a.N, kTile) * cdiv(a.K, kTile) * a.E);
   if (f32) return accumulate ? launch_weights<true, true>(grid, st, t) : launch_weights<true, false>(grid, st, t);
   return launch_weights<false, false>(grid, st, t);
 }
