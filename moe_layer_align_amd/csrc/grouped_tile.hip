@@ -57,11 +57,14 @@ constexpr int kHalf = 128;        // indices of an operand half
 constexpr int kTile = 256;
 constexpr int kPiece = kHalf * kC * 2;  // 16 KB: one half of one step
 constexpr int kRing = 8 * kPiece;       // 2 stages x 2 operands x 2 halves
-constexpr int kEpi = 2048;              // epilogue area of a wave
-constexpr int kTable = kRing + 8 * kEpi;  // tile counts of the experts
-constexpr int kLds = kTable + 2 * kMaxExperts * 4 + 64;
+// epilogue area of a wave: the weight gradient needs no table of tile counts
+__host__ __device__ constexpr int epilogue_bytes(int op) { return op == 2 ? 4096 : 2048; }
+constexpr int kTable = kRing + 8 * epilogue_bytes(0);  // tile counts of the experts
+constexpr int lds_bytes(int op) {
+  return op == 2 ? kRing + 8 * epilogue_bytes(2) : kTable + 2 * kMaxExperts * 4 + 64;
+}
 constexpr int kSlots = 32;              // most workgroups per XCD: one per CU
-static_assert(kLds <= 160 * 1024, "LDS of one gfx950 CU");
+static_assert(lds_bytes(0) <= 160 * 1024 && lds_bytes(2) <= 160 * 1024, "LDS of one gfx950 CU");
 // offset of a lane that loads nothing: past every buffer (their sizes are at
 // most this), and far enough below 2^32 that an in-row offset added to it does
 // not wrap
@@ -86,6 +89,14 @@ struct Tile {
 // Workgroups per XCD, the stride of a workgroup's items.
 __device__ __forceinline__ int slots() { return (int)gridDim.x >> 3; }
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
+// The lane, made anew: what is derived from it is not held in registers across
+// the loops around.
+__device__ __forceinline__ int lane_now() {
+  int l = (int)__builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, 0u));
+  asm volatile("" : "+v"(l));
+  return l;
+}
 
 // Bytes from the first of `rows` rows `ld` bytes apart to the end of the last
 // one's `width` bytes.
@@ -134,6 +145,7 @@ __device__ __forceinline__ void phase_begin() {
 // ids, the lane offsets do.  Wave w loads rows 8w + 4q + lane/16 (q = 0, 1) of
 // a step's 64, lane l the 16-byte chunk (l%16) ^ 4*(l/16) of the half's 256
 // bytes (so that the four rows of a transpose read lie in different banks).
+template <bool IDS>
 struct TransLoads {
   const uint8_t* base;
   int64_t ld;         // row bytes
@@ -169,7 +181,7 @@ struct TransLoads {
   }
   // Columns from x0 on of a rows operand, over the rows of tile t.
   __device__ __forceinline__ void rows_of(const RowsArg& r, int w, int x0, const Tile& t, int wave, int lane) {
-    ids = r.ids;
+    ids = IDS ? r.ids : nullptr;
     ld = r.stride * 2;
     width = (int64_t)(w - x0) * 2;
     rows = r.rows;
@@ -186,22 +198,16 @@ struct TransLoads {
   }
   // Step s (steps are taken in order, from 0): `count` rows in all, at least one.
   __device__ __forceinline__ void step(int s, int count, int wave, int lane) {
-    const bool by_id = ids != nullptr;
-    u32x2 o = off;
-    unsigned n = bytes;
-    const uint8_t* at = base;
-    if (by_id) {
+    if (IDS && ids) {
       int f0, f1;
       fetch_ids(ids, s, wave, lane, &f0, &f1);
       const int r = kC * s + row(wave, lane);
-      o = u32x2{id_offset(f0, r < count, lane), id_offset(f1, r + 4 < count, lane)};
+      off = u32x2{id_offset(f0, r < count, lane), id_offset(f1, r + 4 < count, lane)};
     } else {
-      if (s) at += kC * ld;
-      n = extent(min(kC, count - kC * s), ld, width);
+      base += s ? kC * ld : 0;
+      const int left = min(kC, count - kC * s);
+      bytes = left > 0 ? (unsigned)((left - 1) * ld + width) : 0u;
     }
-    off = o;
-    base = at;
-    bytes = n;
   }
   __device__ __forceinline__ void issue(lds_u8* dst, int h) const {
     load_lds<false>(base, bytes, dst, off[0] + h * (kHalf * 2));
@@ -239,7 +245,7 @@ __device__ __forceinline__ int contraction(const TileArgs& a, const Tile& t) {
 __device__ __forceinline__ int steps_of(int len) { return 2 * ((len + 2 * kC - 1) / (2 * kC)); }
 
 // The loads of one workgroup's sequence of tiles, step by step.
-template <int OP, bool HALF>
+template <int OP, bool HALF, bool IDS>
 struct Loads {
   static constexpr bool kTransP = OP != 0, kTransQ = OP == 2;
   int s, nk, len;  // step of the current tile, its steps and its contraction
@@ -248,7 +254,7 @@ struct Loads {
   unsigned pbytes;
   u32x2 poff;           // natural P: rows 16w + lane/8 and 8 more
   u32x2 qoff0, qoff1;   // natural Q: the same of half 0 and half 1
-  TransLoads tp, tq;
+  TransLoads<OP == 2 && IDS> tp, tq;
 
   // Natural operands: wave w loads rows 16w + 8i + lane/8 (i = 0, 1) of a half,
   // lane l the logical chunk (l%8) ^ pf_mix(row) = (l%8) ^ (l/8) ^ i.
@@ -270,7 +276,8 @@ struct Loads {
     return m >= 0 ? (unsigned)m * (unsigned)(a.q.stride * 2) + (chunk << 4) : kOob;
   }
   // To the first step of a tile.
-  __device__ __forceinline__ void tile(const TileArgs& a, const Tile& t, int wave, int lane) {
+  __device__ __forceinline__ void tile(const TileArgs& a, const Tile& t, int wave) {
+    const int lane = lane_now();
     len = contraction<OP>(a, t);
     nk = steps_of(len);
     s = 0;
@@ -294,7 +301,8 @@ struct Loads {
     if constexpr (kTransP) tp.step(0, len, wave, lane);
     if constexpr (kTransQ) tq.step(0, len, wave, lane);
   }
-  __device__ __forceinline__ void step(int wave, int lane) {  // to the next step of the tile
+  __device__ __forceinline__ void step(int wave) {  // to the next step of the tile
+    const int lane = OP == 2 && IDS ? lane_now() : 0;
     ++s;
     if constexpr (kTransP) tp.step(s, len, wave, lane);
     if constexpr (kTransQ) tq.step(s, len, wave, lane);
@@ -304,9 +312,9 @@ struct Loads {
     s = 0;
     len = 0;
     if constexpr (!kTransQ) qoff0 = qoff1 = u32x2{kOob, kOob};
-    pbytes = 0;
-    tp.none();
-    tq.none();
+    if constexpr (!kTransP) pbytes = 0;
+    if constexpr (kTransP) tp.none();
+    if constexpr (kTransQ) tq.none();
   }
   // Half h into its slot; a natural chunk at or past the contraction's end
   // loads nothing (zeros).
@@ -363,7 +371,7 @@ __device__ __forceinline__ uint8_t* out_row(const TileArgs& a, const Tile& t, in
 
 // All tiles of one kind (HALF: at most 128 q) of a workgroup: items(u, &tile)
 // moves u to the next item from u on, or returns false.
-template <int OP, bool F32, bool ACC, bool HALF, typename Items>
+template <int OP, bool F32, bool ACC, bool HALF, bool IDS, typename Items>
 __device__ __forceinline__ void run_tiles(const TileArgs& a, lds_u8* smem, int& u, const Items& items) {
   constexpr bool kTransP = OP != 0, kTransQ = OP == 2;
   constexpr int kReadsP = kTransP ? 16 : 8, kReadsQ = kTransQ ? 8 : 4;  // LDS reads of a half
@@ -372,25 +380,21 @@ __device__ __forceinline__ void run_tiles(const TileArgs& a, lds_u8* smem, int& 
   const int width = OP == 0 ? a.N : a.K;  // of p
   Tile t;
   if (!items(u, &t)) return;
-  Loads<OP, HALF> L;
+  Loads<OP, HALF, IDS> L;
   Tile lt = t;  // the loads' tile
   int lu = u;
   L.init(a, wave, lane);
-  // A tile without steps (a weight gradient of an expert without rows) has no loads.
   auto load_tile = [&](bool have) {
-    while (have && contraction<OP>(a, lt) == 0) {
-      lu += slots();
-      have = items(lu, &lt);
-    }
     if (have)
-      L.tile(a, lt, wave, lane);
+      L.tile(a, lt, wave);
     else
       L.end();
   };
+  // After a step: to the next tile where it was the last.  L.step itself is
+  // scheduled among the MFMAs; past the last step it changes nothing that the
+  // next tile keeps.
   auto load_next = [&] {
-    if (L.s + 1 < L.nk) {
-      L.step(wave, lane);
-    } else {
+    if (L.s >= L.nk) {
       lu += slots();
       load_tile(items(lu, &lt));
     }
@@ -453,22 +457,26 @@ __device__ __forceinline__ void run_tiles(const TileArgs& a, lds_u8* smem, int& 
   issue_q(0, 0);
   if constexpr (!HALF) issue_q(1, 0);
   issue_p(1, 0);
+  L.step(wave);
   load_next();
   issue_p(0, 1);
   issue_q(0, 1);
   if constexpr (!HALF) issue_q(1, 1);
   if constexpr (!HALF) {
     issue_p(1, 1);
+    L.step(wave);
     load_next();
   }
   begin();
   read_p(A0, 0, 0);
   read_q(F0, 0, 0);
   ring_barrier();
-  if constexpr (HALF)
+  if constexpr (HALF) {
     issue_p(1, 1);
-  else
+    L.step(wave);
+  } else {
     issue_p(0, 0);
+  }
   // X holds Q half 0 of the step on entry; Y takes half 1, then half 0 of the next step
   auto step = [&](auto bt, u32x4 (&X)[4], u32x4 (&Y)[4]) {
     constexpr int b = decltype(bt)::value;
@@ -491,6 +499,7 @@ __device__ __forceinline__ void run_tiles(const TileArgs& a, lds_u8* smem, int& 
       fence();
       read_p(A0, 0, b ^ 1);
       issue_p(1, b);
+      L.step(wave);
       mma(acc[1][HALF ? 0 : 1], A1, Y);
       interleave<8, kReadsP, 2, 4 * b + 2>();
       fence();
@@ -517,6 +526,7 @@ __device__ __forceinline__ void run_tiles(const TileArgs& a, lds_u8* smem, int& 
       read_p(A0, 0, b ^ 1);
       read_q(Y, 0, b ^ 1);
       issue_p(1, b);
+      L.step(wave);
       mma(acc[1][0], A1, X);
       interleave<8, kReadsP + kReadsQ, 2, 9 + 2 * b>();
       fence();
@@ -531,56 +541,54 @@ __device__ __forceinline__ void run_tiles(const TileArgs& a, lds_u8* smem, int& 
       step(std::integral_constant<int, 1>{}, F1, F0);
     }
     // Epilogue: each wave transposes its 64 p x 32 q of a quadrant through its
-    // own 2 KB beside the ring, so that a store writes whole 128-byte lines of a
-    // result row: 16 (bf16) or 8 (fp32) q at a time.
-    if (!(ACC && nk == 0)) {
-      int el = (int)__builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, 0u));  // the lane, again: nothing
-      asm volatile("" : "+v"(el));                                                         // lives across the loop
-      const int ef = el & 31, eh = el >> 5;
-      lds_u8* ep = smem + kRing + wave * kEpi;
-      constexpr int kQ = F32 ? 8 : 16;      // q rows at a time
-      constexpr int kRowB = kEpi / kQ;      // their bytes
-      constexpr int kLanes = kRowB / 16;    // lanes of a result row
-      const int rl = el / kLanes, cl = el % kLanes;
+    // own LDS beside the ring, kQ result rows at a time, so that a store writes
+    // whole 128-byte lines of a row.
+    const int el = lane_now(), ef = el & 31, eh = el >> 5;
+    constexpr int kArea = epilogue_bytes(OP);
+    constexpr int kRowB = F32 ? 256 : 128;  // bytes of a quadrant's result row
+    constexpr int kQ = kArea / kRowB;
+    constexpr int kLanes = kRowB / 16;      // lanes of a result row
+    constexpr int kX = kLanes - 1;          // chunk swizzle
+    lds_u8* ep = smem + kRing + wave * kArea;
+    const int rl = el / kLanes, cl = el % kLanes;
 #pragma unroll
-      for (int j = 0; j < (HALF ? 1 : 2); ++j)
+    for (int j = 0; j < (HALF ? 1 : 2); ++j)
 #pragma unroll
-        for (int z = 0; z < 32 / kQ; ++z)
+      for (int z = 0; z < 32 / kQ; ++z)
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            if (ef / kQ == z) {
-              const int x = ef % kQ;
+        for (int i = 0; i < 2; ++i) {
+          if (kQ == 32 || ef / kQ == z) {
+            const int x = ef % kQ;
 #pragma unroll
-              for (int k = 0; k < 2; ++k)
+            for (int k = 0; k < 2; ++k)
 #pragma unroll
-                for (int g = 0; g < 4; ++g) {
-                  const f32x16& c = acc[i][j][k];
-                  const f32x4 v = {c[4 * g], c[4 * g + 1], c[4 * g + 2], c[4 * g + 3]};
-                  if constexpr (F32)
-                    *(lds_f32x4*)(ep + x * kRowB + (((8 * k + 2 * g + eh) ^ x) << 4)) = v;
-                  else
-                    *(lds_u32x2*)(ep + x * kRowB + (((4 * k + g) ^ (x & 7)) << 4) + 8 * eh) =
-                        u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
-                }
-            }
-            wave_exchange();
-            const int p = t.p0 + kHalf * i + 64 * wr + cl * (F32 ? 4 : 8);
-#pragma unroll
-            for (int rr = 0; rr < kQ * kLanes / 64; ++rr) {
-              const int x = (64 / kLanes) * rr + rl;
-              const u32x4 v = *(const lds_u32x4*)(ep + x * kRowB + ((cl ^ (F32 ? x : x & 7)) << 4));
-              uint8_t* o = out_row<OP, F32>(a, t, kHalf * j + 32 * wc + kQ * z + x);
-              if (o && p < width) {
-                u32x4* at = (u32x4*)(o + (int64_t)p * (F32 ? 4 : 2));
-                if constexpr (ACC)
-                  *(f32x4*)at = *(const f32x4*)at + __builtin_bit_cast(f32x4, v);
+              for (int g = 0; g < 4; ++g) {
+                const f32x16& c = acc[i][j][k];
+                const f32x4 v = {c[4 * g], c[4 * g + 1], c[4 * g + 2], c[4 * g + 3]};
+                if constexpr (F32)
+                  *(lds_f32x4*)(ep + x * kRowB + (((8 * k + 2 * g + eh) ^ (x & kX)) << 4)) = v;
                 else
-                  *at = v;
+                  *(lds_u32x2*)(ep + x * kRowB + (((4 * k + g) ^ (x & kX)) << 4) + 8 * eh) =
+                      u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
               }
-            }
-            wave_exchange();
           }
-    }
+          wave_exchange();
+          const int p = t.p0 + kHalf * i + 64 * wr + cl * (F32 ? 4 : 8);
+#pragma unroll
+          for (int rr = 0; rr < kQ * kLanes / 64; ++rr) {
+            const int x = (64 / kLanes) * rr + rl;
+            const u32x4 v = *(const lds_u32x4*)(ep + x * kRowB + ((cl ^ (x & kX)) << 4));
+            uint8_t* o = out_row<OP, F32>(a, t, kHalf * j + 32 * wc + kQ * z + x);
+            if (o && p < width) {
+              u32x4* at = (u32x4*)(o + (int64_t)p * (F32 ? 4 : 2));
+              if constexpr (ACC)
+                *(f32x4*)at = *(const f32x4*)at + __builtin_bit_cast(f32x4, v);
+              else
+                *at = v;
+            }
+          }
+          wave_exchange();
+        }
     u += slots();
     if (!items(u, &t)) break;
   }
@@ -601,13 +609,13 @@ __device__ __forceinline__ void run_small(const TileArgs& a, lds_u8* smem, int& 
   const int wp = wave & 3, wq = wave >> 2;
   const int width = OP == 0 ? a.N : a.K, len = OP == 0 ? a.K : a.N;
   const int nk = (len + kC - 1) / kC;
-  Loads<OP, true> L;
+  Loads<OP, true, false> L;
   L.init(a, wave, lane);
   const int pa = kTransP ? trans_at(32 * wp, lane) : natural_at(32 * wp, lane);
   const int qa = natural_at(32 * wq, lane);
   const int qc = (lane & 7) ^ (lane >> 3) ^ (wave & 1);  // chunk of Q row 8w + lane/8
   for (Tile t; items(u, &t); u += slots()) {
-    L.tile(a, t, wave, lane);
+    L.tile(a, t, wave);
     if constexpr (OP == 0) L.pbytes = extent(min(kHalf, a.N - t.p0), (int64_t)a.K * 2, (int64_t)a.K * 2);
     const unsigned qoff = L.row_offset(a, t, 8 * wave + (lane >> 3), qc);
     auto issue = [&](int stage) {  // step L.s, then on to the next
@@ -615,7 +623,7 @@ __device__ __forceinline__ void run_small(const TileArgs& a, lds_u8* smem, int& 
       L.issue_p(a, dst + wave * 2048, 0, lane);
       load_lds<!kTransP>(L.qbase, kOob, dst + kPiece + wave * 1024,
                          qc << 3 < len - kC * L.s ? qoff + (unsigned)(L.s * (kC * 2)) : kOob);
-      L.step(wave, lane);
+      L.step(wave);
     };
     f32x16 acc;
 #pragma unroll
@@ -750,17 +758,18 @@ __global__ __launch_bounds__(kThreads) void grouped_rows_kernel(TileArgs a) {
     return true;
   };
   int u = blockIdx.x >> 3;
-  run_tiles<OP, F32, false, false>(a, smem, u, whole);
+  run_tiles<OP, F32, false, false, true>(a, smem, u, whole);
   while (u < nf) u += slots();  // an XCD's last items can be missing
-  run_tiles<OP, F32, false, true>(a, smem, u, half);
+  run_tiles<OP, F32, false, true, true>(a, smem, u, half);
   while (u < nf + nh) u += slots();
   run_small<OP, F32>(a, smem, u, small);
 }
 
 // Weight gradient: the tiles of an expert are split over the XCDs (experts
 // differ in their contraction, so whole experts would not balance), each XCD
-// taking a contiguous band; few tiles are dealt round robin.
-template <bool F32, bool ACC>
+// taking a contiguous band; few tiles are dealt round robin.  Experts without
+// rows have no tiles.
+template <bool F32, bool ACC, bool IDS>
 __global__ __launch_bounds__(kThreads) void grouped_wgrad_kernel(TileArgs a) {
   extern __shared__ __align__(16) uint8_t smem_raw[];
   lds_u8* smem = (lds_u8*)smem_raw;
@@ -785,50 +794,72 @@ __global__ __launch_bounds__(kThreads) void grouped_wgrad_kernel(TileArgs a) {
       t->q0 = (4 * g + r % n) * kTile;
       t->p0 = (r / n) * kTile;
       range(t);
-      return true;
+      if (t->lo < t->hi) return true;
     }
     return false;
   };
   auto half = [&](int& u, Tile* t) {
-    const int i = (u - nf) * 8 + x;
-    if (u >= nf + nh || i >= PT * a.E) return false;
-    t->e = i / PT;
-    t->q0 = QT * kTile;
-    t->p0 = i % PT * kTile;
-    range(t);
-    return true;
+    for (; u < nf + nh; u += slots()) {
+      const int i = (u - nf) * 8 + x;
+      if (i >= PT * a.E) return false;
+      t->e = i / PT;
+      t->q0 = QT * kTile;
+      t->p0 = i % PT * kTile;
+      range(t);
+      if (t->lo < t->hi) return true;
+    }
+    return false;
   };
+  // experts without rows: zeros, or nothing to add
+  if constexpr (!ACC) {
+    const int64_t bytes = (int64_t)a.N * a.K * (F32 ? 4 : 2);
+    const int lane = threadIdx.x & 63;
+    for (int e0 = 0; e0 < a.E; e0 += 64) {
+      int lo = 0, hi = 1;
+      if (e0 + lane < a.E) group_range(a.offsets, e0 + lane, a.R, &lo, &hi);
+      for (unsigned long long m = __ballot(lo == hi); m; m &= m - 1) {
+        uint8_t* o = a.dw + (e0 + __ffsll(m) - 1) * bytes;
+        for (int64_t i = ((int64_t)blockIdx.x * kThreads + threadIdx.x) * 16; i < bytes; i += (int64_t)gridDim.x * kThreads * 16)
+          *(u32x4*)(o + i) = u32x4{0, 0, 0, 0};
+      }
+    }
+  }
   int u = blockIdx.x >> 3;
-  run_tiles<2, F32, ACC, false>(a, smem, u, whole);
+  run_tiles<2, F32, ACC, false, IDS>(a, smem, u, whole);
   while (u < nf) u += slots();
-  run_tiles<2, F32, ACC, true>(a, smem, u, half);
+  run_tiles<2, F32, ACC, true, IDS>(a, smem, u, half);
 }
 
-// Launch with kLds bytes of dynamic LDS; the kernel's ceiling is raised once
+// Launch with `lds` bytes of dynamic LDS; the kernel's ceiling is raised once
 // per device.
 template <typename Kernel>
-bool launch(Kernel kernel, std::atomic<bool> (&lds_set)[64], int64_t grid, hipStream_t st, const TileArgs& a) {
+bool launch(Kernel kernel, int lds, std::atomic<bool> (&lds_set)[64], int64_t grid, hipStream_t st, const TileArgs& a) {
   int dev = 0;
   if (hipGetDevice(&dev) != hipSuccess || dev < 0) return false;
   if (dev >= 64 || !lds_set[dev].load(std::memory_order_acquire)) {
-    if (hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, kLds) != hipSuccess)
+    if (hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, lds) != hipSuccess)
       return false;
     if (dev < 64) lds_set[dev].store(true, std::memory_order_release);
   }
-  kernel<<<(unsigned)grid, kThreads, kLds, st>>>(a);
+  kernel<<<(unsigned)grid, kThreads, lds, st>>>(a);
   return true;
 }
 
 template <int OP, bool F32>
 bool launch_rows(int64_t grid, hipStream_t st, const TileArgs& a) {
   static std::atomic<bool> lds_set[64];
-  return launch(grouped_rows_kernel<OP, F32>, lds_set, grid, st, a);
+  return launch(grouped_rows_kernel<OP, F32>, lds_bytes(OP), lds_set, grid, st, a);
 }
 
-template <bool F32, bool ACC>
+template <bool F32, bool ACC, bool IDS>
 bool launch_weights(int64_t grid, hipStream_t st, const TileArgs& a) {
   static std::atomic<bool> lds_set[64];
-  return launch(grouped_wgrad_kernel<F32, ACC>, lds_set, grid, st, a);
+  return launch(grouped_wgrad_kernel<F32, ACC, IDS>, lds_bytes(2), lds_set, grid, st, a);
+}
+template <bool F32, bool ACC>
+bool launch_weights(int64_t grid, hipStream_t st, const TileArgs& a) {
+  return a.p.ids || a.q.ids ? launch_weights<F32, ACC, true>(grid, st, a)
+                            : launch_weights<F32, ACC, false>(grid, st, a);
 }
 
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
