@@ -204,10 +204,12 @@ def test_mxfp4_short_groups(K, name):
 
 
 @pytest.mark.parametrize("fmt", ["mxfp4", "int4"])
-@pytest.mark.parametrize("N,K", [(1544, 1408), (2056, 1408), (3400, 640)])
-def test_w4_larger(fmt, N, K):
-    # many workgroups per expert: the launch's wider bands, with K long and short
-    w4_case(fmt, "many_small", N, K, True, True, torch.bfloat16)
+@pytest.mark.parametrize("name,N,K", [("many_small", 1544, 1408), ("many_small", 2056, 1280), ("many_small", 3400, 640),
+                                      ("edges_64", 3400, 1408), ("edges_64", 3400, 640), ("one_row", 16648, 1152),
+                                      ("two_of_three", 8328, 384)])
+def test_w4_larger(fmt, name, N, K):
+    # the launch's wider bands, with K long and short, few and many rows per expert
+    w4_case(fmt, name, N, K, True, True, torch.bfloat16)
 
 
 def w4_case(fmt, name, N, K, gather, scatter, dtype):
