@@ -810,6 +810,10 @@ __global__ __launch_bounds__(kThreads) void grouped_wgrad_kernel(TileArgs a) {
     }
     return false;
   };
+  int u = blockIdx.x >> 3;
+  run_tiles<2, F32, ACC, false, IDS>(a, smem, u, whole);
+  while (u < nf) u += slots();
+  run_tiles<2, F32, ACC, true, IDS>(a, smem, u, half);
   // experts without rows: zeros, or nothing to add
   if constexpr (!ACC) {
     const int64_t bytes = (int64_t)a.N * a.K * (F32 ? 4 : 2);
@@ -824,10 +828,6 @@ __global__ __launch_bounds__(kThreads) void grouped_wgrad_kernel(TileArgs a) {
       }
     }
   }
-  int u = blockIdx.x >> 3;
-  run_tiles<2, F32, ACC, false, IDS>(a, smem, u, whole);
-  while (u < nf) u += slots();
-  run_tiles<2, F32, ACC, true, IDS>(a, smem, u, half);
 }
 
 // Launch with `lds` bytes of dynamic LDS; the kernel's ceiling is raised once
@@ -869,8 +869,12 @@ int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 namespace {
 
 // One workgroup per CU: kSlots on each of the eight XCDs, fewer where there are
-// fewer tiles than that.
-int64_t persistent_grid(int64_t tiles) { return 8 * (cdiv(tiles, 8) < kSlots ? cdiv(tiles, 8) : kSlots); }
+// fewer tiles than that.  An XCD's share of each of the up to three kinds of
+// tiles is rounded up.
+int64_t persistent_grid(int64_t tiles) {
+  const int64_t slots = cdiv(tiles, 8) + 2;
+  return 8 * (slots < kSlots ? slots : kSlots);
+}
 
 }  // namespace
 
