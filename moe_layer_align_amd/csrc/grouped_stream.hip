@@ -105,10 +105,10 @@ __device__ __forceinline__ void pass(const GroupedArgs& a, int e, int n0, int i0
   const unsigned wrow = (unsigned)a.K / 2, srow = FMT == kMxfp4 ? (unsigned)a.K / 32 : (unsigned)a.K / 128 * 2;
   const __amdgpu_buffer_rsrc_t rw = buffer(a.w + (int64_t)e * a.N * wrow, (unsigned)a.N * wrow);
   const __amdgpu_buffer_rsrc_t rx = buffer(a.in.ids ? a.in.p : a.in.p + (int64_t)i0 * a.in.stride * 2, kOob);
-  // the expert's scales, from the aligned dword on that holds the first
+  // the expert's scales, in the aligned dwords that hold them
   const uint8_t* const sp = a.w_scale + (int64_t)e * a.N * srow;
   const unsigned slead = (unsigned)(uintptr_t)sp & 3;
-  const __amdgpu_buffer_rsrc_t rs = buffer(sp - slead, (unsigned)a.N * srow + slead);
+  const __amdgpu_buffer_rsrc_t rs = buffer(sp - slead, ((unsigned)a.N * srow + slead + 3) & ~3u);
   lds_u8* const stage = smem + wave * (2 * kStage);
   const int nb = n0 + 16 * FT * wb;  // the wave's first weight row
 

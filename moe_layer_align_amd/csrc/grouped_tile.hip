@@ -709,7 +709,9 @@ __global__ __launch_bounds__(kThreads) void grouped_rows_kernel(TileArgs a) {
     rest[tid] = ri;
     __syncthreads();
   }
-  const int NF = uniform(full[a.E - 1]), NR = uniform(rest[a.E - 1]), NH = NR & 0xffff, NS = NR >> 16;
+  // offsets that decrease could make experts overlap: no more tiles than R rows have
+  const int NF = min(uniform(full[a.E - 1]), a.R / kTile + a.E);
+  const int NR = uniform(rest[a.E - 1]), NH = NR & 0xffff, NS = NR >> 16;
   const int width = OP == 0 ? a.N : a.K;
   const int PT = (width + kTile - 1) / kTile, PS = (width + kHalf - 1) / kHalf;
   const int x = blockIdx.x & 7;

@@ -115,6 +115,31 @@ def test_product_rows(kind, gather, scatter, dtype, name):
     run_product(kind, name, 264, 328, gather, scatter, dtype)
 
 
+MANY = {  # several tiles of each kind for every workgroup
+    "whole": [2100, 700, 0, 2900, 1500],
+    "halves": [70 + i % 59 for i in range(40)],
+    "small": [1 + i % 64 for i in range(48)],
+    "mixed": [256 * (i % 3) + (37 * i) % 256 for i in range(30)],
+}
+
+
+@pytest.mark.parametrize("kind", ["fwd", "dgrad"])
+@pytest.mark.parametrize("name", list(MANY))
+@pytest.mark.parametrize("inner", [72, 200, 328])
+def test_many_tiles_per_workgroup(kind, name, inner, monkeypatch):
+    monkeypatch.setitem(COUNTS, name, MANY[name])
+    N, K = (4360, inner) if kind == "fwd" else (inner, 4360)
+    run_product(kind, name, N, K, inner == 200, inner == 328, torch.bfloat16)
+
+
+@pytest.mark.parametrize("gather", [False, True])
+@pytest.mark.parametrize("dtype,accumulate", [(torch.bfloat16, False), (torch.float32, False), (torch.float32, True)])
+@pytest.mark.parametrize("counts", [[130, 1, 0, 64, 300, 65, 129, 128], [5] * 12])
+def test_wgrad_many_tiles_per_workgroup(gather, dtype, accumulate, counts, monkeypatch):
+    monkeypatch.setitem(COUNTS, "many", counts)
+    wgrad_case("many", 4360, 1544, False, gather, dtype, accumulate)
+
+
 @pytest.mark.parametrize("kind", ["fwd", "dgrad"])
 def test_long_contraction(kind):
     # the contraction runs over 4104 terms, one 64-step and 8 more past 64 whole ones
