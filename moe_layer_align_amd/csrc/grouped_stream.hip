@@ -54,9 +54,14 @@ __device__ __forceinline__ u32x4 load16(__amdgpu_buffer_rsrc_t r, unsigned off) 
   return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, (int)off, 0, 0));
 }
 
+// int4: 16 + q is the exponent of 16 with q in mantissa bits 3..6.
+constexpr unsigned kInt4One = 0x41804180u;
+
 // 8 codes -> 8 bf16 in the order k, or (int4) the pairs (0,4) (1,5) (2,6) (3,7).
+// `one` is kInt4One in a vector register: with both constants as literals the
+// and-or would be two instructions.
 template <int FMT>
-__device__ __forceinline__ u32x4 dequant(unsigned w, unsigned scale) {
+__device__ __forceinline__ u32x4 dequant(unsigned w, unsigned scale, unsigned one) {
   u32x4 o;
   if constexpr (FMT == kMxfp4) {
     const float s = __uint_as_float(scale);
@@ -65,7 +70,7 @@ __device__ __forceinline__ u32x4 dequant(unsigned w, unsigned scale) {
     o[2] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 2));
     o[3] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 3));
   } else {
-    constexpr unsigned mask = 0x00780078u, one = 0x41804180u;  // 16 + q: exponent of 16, q in mantissa bits 3..6
+    constexpr unsigned mask = 0x00780078u;
     o[0] = ((w << 3) & mask) | one;
     o[1] = ((w >> 1) & mask) | one;
     o[2] = ((w >> 5) & mask) | one;
@@ -155,6 +160,8 @@ __device__ __forceinline__ void pass(const GroupedArgs& a, int e, int n0, int i0
   };
 
   f32x4 acc[FT][NT] = {};
+  unsigned one = kInt4One;
+  if constexpr (FMT == kInt4) asm volatile("" : "+v"(one));
   auto multiply = [&](const Step<FMT, FT, NT>& g, const u32x4 (&w)[FT][2], int c) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -163,21 +170,24 @@ __device__ __forceinline__ void pass(const GroupedArgs& a, int e, int n0, int i0
       for (int t = 0; t < NT; ++t)
 #pragma unroll
         for (int j = 0; j < 4; ++j) x[t][j] = order<FMT>(g.x[t][i][j]);
-      // a scale past the row's end is another row's or none: zero
+      // a scale past the row's end is another row's or none: zero.  The tiles
+      // take turns: a tile's sums are a chain of dependent MFMAs.
       if constexpr (FMT == kMxfp4) {
         const bool ok = c * kStep + 128 * i + 32 * q < a.K;
+        unsigned s[FT];
 #pragma unroll
         for (int f = 0; f < FT; ++f) {
-          const unsigned lead = (s0 + 16 * f * srow) & 3u;
-          const unsigned codes = __builtin_amdgcn_alignbyte(g.s[f][i + 1], g.s[f][i], lead);
-          const unsigned s = ok ? ((codes >> (8 * q)) & 0xffu) << 23 : 0u;
+          const unsigned codes = __builtin_amdgcn_alignbyte(g.s[f][i + 1], g.s[f][i], (s0 + 16 * f * srow) & 3u);
+          s[f] = ok ? ((codes >> (8 * q)) & 0xffu) << 23 : 0u;
+        }
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const u32x4 v = dequant<FMT>(w[f][i][j], s);
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int f = 0; f < FT; ++f) {
+            const u32x4 v = dequant<FMT>(w[f][i][j], s[f], one);
 #pragma unroll
             for (int t = 0; t < NT; ++t) acc[f][t] = mfma_bf16(x[t][j], v, acc[f][t]);
           }
-        }
       } else {
         constexpr unsigned m24 = 0xc1c0c1c0u;  // a pair of bf16 -24
         f32x4 start[NT] = {};
@@ -185,24 +195,23 @@ __device__ __forceinline__ void pass(const GroupedArgs& a, int e, int n0, int i0
         for (int j = 0; j < 4; ++j)
 #pragma unroll
           for (int t = 0; t < NT; ++t) start[t] = mfma_bf16(x[t][j], u32x4{m24, m24, m24, m24}, start[t]);
+        f32x4 sum[FT][NT];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int f = 0; f < FT; ++f) {
+            const u32x4 v = dequant<FMT>(w[f][i][j], 0, one);
+#pragma unroll
+            for (int t = 0; t < NT; ++t) sum[f][t] = mfma_bf16(x[t][j], v, j == 0 ? start[t] : sum[f][t]);
+          }
 #pragma unroll
         for (int f = 0; f < FT; ++f) {
-          f32x4 sum[NT];
-#pragma unroll
-          for (int t = 0; t < NT; ++t) sum[t] = start[t];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const u32x4 v = dequant<FMT>(w[f][i][j], 0);
-#pragma unroll
-            for (int t = 0; t < NT; ++t) sum[t] = mfma_bf16(x[t][j], v, sum[t]);
-          }
-          const unsigned lead = (s0 + 16 * f * srow) & 3u;
-          const unsigned pair = __builtin_amdgcn_alignbyte(g.s[f][1], g.s[f][0], lead);
+          const unsigned pair = __builtin_amdgcn_alignbyte(g.s[f][1], g.s[f][0], (s0 + 16 * f * srow) & 3u);
           const float s = c * kStep + 128 * i < a.K ? (i ? bf16_hi(pair) : bf16_lo(pair)) : 0.0f;
 #pragma unroll
           for (int t = 0; t < NT; ++t)
 #pragma unroll
-            for (int v = 0; v < 4; ++v) acc[f][t][v] += s * sum[t][v];
+            for (int v = 0; v < 4; ++v) acc[f][t][v] += s * sum[f][t][v];
         }
       }
     }
