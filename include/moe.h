@@ -468,9 +468,9 @@ typedef enum {
  * is zero or a normal bf16) or bf16 [E,N,K/128].  The weights' values are exact
  * in the product: scales are powers of two in bf16 range (MXFP4), or applied
  * in fp32 to each group's sum (INT4, where an infinite element of a row makes
- * the row's results NaN).  4-bit weights are streamed once per 32 rows of an
- * expert: the form for decoding.  bf16 weights take a streaming or
- * a tiled kernel by the mean number of rows per expert.
+ * the row's results NaN).  4-bit weights are streamed once per 16 rows of an
+ * expert (once per 32 where R > 8 E): the form for decoding.  bf16 weights take tiles
+ * of 256 rows, or of 64 for an expert's last or only few rows.
  */
 typedef struct {
   int32_t R, E, N, K;
@@ -495,8 +495,10 @@ moe_status_t moe_grouped_gemm_dgrad(const moe_grouped_args_t* args, void* stream
 /*
  * Gradient of the weights: dw[e] = sum over expert e's rows i of
  * dy[i] in[i]^T, [E,N,K] row-major, dy of width N, in of width K; zero for an
- * expert without rows.  accumulate 1 (fp32 only, else MOE_ERR_INVALID_ARG):
- * dw[e] += that sum; experts without rows are then left as they were.
+ * expert without rows.  A row whose id is outside its matrix in either operand
+ * adds nothing, whatever the other holds.  accumulate 1 (fp32 only, else
+ * MOE_ERR_INVALID_ARG): dw[e] += that sum; experts without rows are then left
+ * as they were.
  */
 typedef struct {
   int32_t R, E, N, K;
@@ -524,8 +526,9 @@ moe_status_t moe_grouped_gemm_wgrad(const moe_grouped_wgrad_args_t* args, void* 
  * *num_rows (offsets + E of a padded grouping) are neither read nor written.
  * row_weight multiplies h before its one rounding, so that the down product's
  * results need only be added up per token.
- * I a multiple of 8 below 2^19, R*I below 2^38, gu_stride below 2^20 (else
- * MOE_ERR_UNSUPPORTED); gu, h and codes 16-byte aligned.
+ * I a multiple of 8 below 2^19, R below 2^26, R*ceil(I/32) below 2^30,
+ * gu_stride below 2^20 (else MOE_ERR_UNSUPPORTED); gu, h and codes 16-byte
+ * aligned.
  */
 moe_status_t moe_swiglu_checkpoint(const void* gu, int64_t gu_stride, const float* row_weight, int32_t R, int32_t I,
                                    const int32_t* num_rows, void* h, uint8_t* codes, uint8_t* scales, void* stream);

@@ -29,13 +29,23 @@
 //
 // One persistent workgroup per CU walks the tiles, and its loads run on into
 // the next tile: the queue stays full over a tile's epilogue, which transposes
-// the results through LDS beside the ring.  Filling the ring anew for every
-// tile, all CUs at once, cost 9 to 14 us a tile of 24 to 100.
+// the results through LDS beside the ring.
 //
 // Rows of an expert past its last whole tile make a tile of 256 x 256 (more
 // than 128 rows), 256 x 128 (more than 64) or several of 128 x 64, and each
 // kind is run after the larger ones: the small ones are bound by the stream of
-// the weights and fill the CUs that the large ones leave idle at the end.
+// the weights and fill the CUs that the large ones leave idle at the end.  Both
+// together, 8 experts of about 1024 rows: product N 4096, K 14336 973 -> 816
+// us, input gradient N 28672, K 4096 1966 -> 1709 us.
+//
+// Measured, 8 experts of 1024 rows: product N 4096, K 14336 720 us (1.34
+// PFLOP/s), N 28672, K 4096 1476 us (1.30); its input gradient 1488 us (1.29);
+// weight gradient N 4096, K 14336 in fp32 1071 us (0.90), where 16 steps share an
+// epilogue of 256 KB.  A large library product of ordinary operands reaches
+// 1.4 to 1.6 here.  What bounds the steps is power: the first of these takes
+// 585 us on zeros, and 613 to 658 on random values without operand loads.
+// 32 rows over 128 experts, N 1536, K 2048: 40 us, bound by the weights in
+// flight (4.5 TB/s over the experts used).
 #include <atomic>
 #include <type_traits>
 
@@ -50,6 +60,7 @@ typedef __attribute__((address_space(3))) u32x4 lds_u32x4;
 typedef __attribute__((address_space(3))) u32x2 lds_u32x2;
 typedef __attribute__((address_space(3))) f32x4 lds_f32x4;
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+typedef __attribute__((address_space(4))) int32_t c_int32;  // read by scalar loads
 
 constexpr int kThreads = 512;
 constexpr int kC = 64;            // contraction per step
@@ -69,6 +80,7 @@ static_assert(lds_bytes(0) <= 160 * 1024 && lds_bytes(2) <= 160 * 1024, "LDS of 
 // most this), and far enough below 2^32 that an in-row offset added to it does
 // not wrap
 constexpr unsigned kOob = 0xffc00000u;
+constexpr unsigned kMasked = kOob | 4;  // the same of a row without a place: offsets of others are multiples of 16
 
 struct TileArgs {
   int R, E, N, K;
@@ -161,8 +173,8 @@ struct TransLoads {
     return (unsigned)((lane & 15) ^ (4 * (lane >> 4))) << 4;
   }
   __device__ __forceinline__ void lane_offsets(int wave, int lane) {
-    const unsigned o = (unsigned)(row(wave, lane) * ld) + chunk(lane);
-    off = u32x2{o, o + (unsigned)(4 * ld)};
+    const unsigned o = (unsigned)row(wave, lane) * (unsigned)ld + chunk(lane);
+    off = u32x2{o, o + 4 * (unsigned)ld};
   }
   // The wave's eight ids of step s by scalar loads (vector loads would be
   // waited for together with the loads into LDS), then the lane's two.
@@ -177,7 +189,7 @@ struct TransLoads {
   }
   __device__ __forceinline__ unsigned id_offset(int f, bool in, int lane) const {
     const unsigned m = div == 1 ? (unsigned)f : (unsigned)f / (unsigned)div;
-    return in && f >= 0 && m < (unsigned)rows ? m * (unsigned)ld + chunk(lane) : kOob;
+    return in && f >= 0 && m < (unsigned)rows ? m * (unsigned)ld + chunk(lane) : kMasked;
   }
   // Columns from x0 on of a rows operand, over the rows of tile t.
   __device__ __forceinline__ void rows_of(const RowsArg& r, int w, int x0, const Tile& t, int wave, int lane) {
@@ -204,6 +216,7 @@ struct TransLoads {
       const int r = kC * s + row(wave, lane);
       off = u32x2{id_offset(f0, r < count, lane), id_offset(f1, r + 4 < count, lane)};
     } else {
+      if (IDS) lane_offsets(wave, lane);  // the other operand's ids may have masked them
       base += s ? kC * ld : 0;
       const int left = min(kC, count - kC * s);
       bytes = left > 0 ? (unsigned)((left - 1) * ld + width) : 0u;
@@ -298,14 +311,27 @@ struct Loads {
       tp.rows_of(a.p, a.K, t.p0, t, wave, lane);
       tq.rows_of(a.q, a.N, t.q0, t, wave, lane);
     }
-    if constexpr (kTransP) tp.step(0, len, wave, lane);
-    if constexpr (kTransQ) tq.step(0, len, wave, lane);
+    trans_step(wave, lane);
+  }
+  // The transposed operands to step s.  A row whose id masks it in one of the
+  // weight gradient's operands is left out of the other too, where it may hold
+  // an infinity or a NaN.
+  __device__ __forceinline__ void trans_step(int wave, int lane) {
+    if constexpr (kTransP) tp.step(s, len, wave, lane);
+    if constexpr (kTransQ) tq.step(s, len, wave, lane);
+    if constexpr (kTransQ && IDS) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const bool masked = tp.off[i] == kMasked || tq.off[i] == kMasked;
+        tp.off[i] = masked ? kMasked : tp.off[i];
+        tq.off[i] = masked ? kMasked : tq.off[i];
+      }
+    }
   }
   __device__ __forceinline__ void step(int wave) {  // to the next step of the tile
     const int lane = OP == 2 && IDS ? lane_now() : 0;
     ++s;
-    if constexpr (kTransP) tp.step(s, len, wave, lane);
-    if constexpr (kTransQ) tq.step(s, len, wave, lane);
+    trans_step(wave, lane);
   }
   __device__ __forceinline__ void end() {  // no more tiles: load nothing
     nk = 0x7fffffff;
@@ -718,7 +744,7 @@ __global__ __launch_bounds__(kThreads) void grouped_rows_kernel(TileArgs a) {
   const int lane = threadIdx.x & 63;
   // items of this XCD: [0, nf) whole tiles, [nf, nf + nh) halves, then small ones
   const int nf = (NF * PT + 7) >> 3, nh = (NH * PT + 7) >> 3, ns = (NS * PS + 7) >> 3;
-  const __attribute__((address_space(4))) int32_t* offsets = (const __attribute__((address_space(4))) int32_t*)a.offsets;
+  const c_int32* offsets = (const c_int32*)a.offsets;
   auto range = [&](Tile* t) {  // of expert t->e, by scalar loads
     const int lo = min(max(offsets[t->e], 0), a.R);
     t->lo = lo;
@@ -778,7 +804,7 @@ __global__ __launch_bounds__(kThreads) void grouped_wgrad_kernel(TileArgs a) {
   const bool last_half = a.N % kTile > 0 && a.N % kTile <= kHalf;  // the last q tile is a half
   const int QT = (a.N + kTile - 1) / kTile - last_half, PT = (a.K + kTile - 1) / kTile;
   const int x = blockIdx.x & 7;
-  const __attribute__((address_space(4))) int32_t* offsets = (const __attribute__((address_space(4))) int32_t*)a.offsets;
+  const c_int32* offsets = (const c_int32*)a.offsets;
   auto range = [&](Tile* t) {
     const int lo = min(max(offsets[t->e], 0), a.R);
     t->lo = lo;
@@ -825,7 +851,8 @@ __global__ __launch_bounds__(kThreads) void grouped_wgrad_kernel(TileArgs a) {
       if (e0 + lane < a.E) group_range(a.offsets, e0 + lane, a.R, &lo, &hi);
       for (unsigned long long m = __ballot(lo == hi); m; m &= m - 1) {
         uint8_t* o = a.dw + (e0 + __ffsll(m) - 1) * bytes;
-        for (int64_t i = ((int64_t)blockIdx.x * kThreads + threadIdx.x) * 16; i < bytes; i += (int64_t)gridDim.x * kThreads * 16)
+        const int64_t step = (int64_t)gridDim.x * kThreads * 16;
+        for (int64_t i = ((int64_t)blockIdx.x * kThreads + threadIdx.x) * 16; i < bytes; i += step)
           *(u32x4*)(o + i) = u32x4{0, 0, 0, 0};
       }
     }

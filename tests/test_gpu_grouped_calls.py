@@ -268,3 +268,38 @@ def test_refusals_of_the_binding():
         with pytest.raises(exc):
             call()
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("gather_dy,gather_a", [(True, False), (False, True), (True, True)])
+def test_masked_rows_add_nothing(gather_dy, gather_a, dtype):
+    # a row that an id masks in one operand may hold anything in the other
+    say("wgrad masked rows gather=%s,%s %s" % (gather_dy, gather_a, dtype))
+    rng = np.random.default_rng(10)
+    counts, N, K = [70, 1, 0, 333], 264, 136
+    off, R = offsets_of(counts), sum(counts)
+    kinds = [k for k, g in (("dy", gather_dy), ("a", gather_a)) if g]
+    masked = {k: rng.random(R) < 0.2 for k in kinds}
+    masked[kinds[0]][70] = True  # an expert whose only row is masked
+    masked[kinds[0]][404 - 64:] = True  # and a whole step
+    hidden = np.logical_or.reduce([masked[k] for k in kinds])
+    ops, ids, sums = {}, {}, {}
+    for k, width in (("dy", N), ("a", K)):
+        rows = bf16(rng, R, width)
+        t = rows.clone()
+        t[torch.from_numpy(hidden)] = torch.tensor([float("nan"), float("inf")], dtype=t.dtype).repeat(width // 2)
+        sums[k] = np.where(hidden[:, None], 0.0, f64(rows))
+        ids[k] = None
+        if k in kinds:
+            perm = rng.permutation(R)
+            where = np.argsort(perm).astype(np.int32)
+            t = t[torch.from_numpy(perm)]
+            where[masked[k]] = np.where(rng.random(masked[k].sum()) < 0.5, -1, R)
+            ids[k] = torch.from_numpy(where).to(DEV)
+        ops[k] = t.to(DEV)
+    got = moe.grouped_gemm_wgrad(ops["dy"], ops["a"], torch.from_numpy(off).to(DEV), dy_rows=ids["dy"],
+                                 a_rows=ids["a"], out_dtype=dtype)
+    torch.cuda.synchronize()
+    for e, n in enumerate(counts):
+        x, y = sums["dy"][off[e]:off[e + 1]], sums["a"][off[e]:off[e + 1]]
+        check(got[e], x.T @ y, np.abs(x).T @ np.abs(y), n, "expert %d" % e)
