@@ -583,8 +583,8 @@ def grouped_gemm_w4(a: torch.Tensor, w4: torch.Tensor, scales: torch.Tensor, off
     call = _Call(a, stream)
     E, N, K = w4.shape[0], w4.shape[1], 2 * w4.shape[2]
     fmt, group = (1, W4_GROUP["mxfp4"]) if scales.dtype is torch.uint8 else (2, W4_GROUP["int4"])
-    return _grouped("moe_grouped_gemm", call, a, call.need(w4, "w4", torch.uint8, (E, N, K // 2)), E, N, K, offsets, out,
-                    a_rows, a_div, out_rows, out_dtype, fmt,
+    return _grouped("moe_grouped_gemm", call, a, call.need(w4, "w4", torch.uint8, (E, N, K // 2)), E, N, K, offsets,
+                    out, a_rows, a_div, out_rows, out_dtype, fmt,
                     call.need(scales, "scales", scales.dtype, (E, N, K // group)))
 
 
@@ -610,8 +610,8 @@ def swiglu_checkpoint(gu: torch.Tensor, row_weight: Optional[torch.Tensor] = Non
         scales = call.empty((R, 2, G), torch.uint8) if scales is None else scales
     elif codes is not None or scales is not None:
         raise ValueError("codes and scales need checkpoint=True")
-    call.run("moe_swiglu_checkpoint", src.data, src.stride, call.vector(row_weight, "row_weight", torch.float32, R), R, I,
-             call.vector(num_rows, "num_rows", torch.int32, 1), call.need(h, "h", torch.bfloat16, (R, I)),
+    call.run("moe_swiglu_checkpoint", src.data, src.stride, call.vector(row_weight, "row_weight", torch.float32, R),
+             R, I, call.vector(num_rows, "num_rows", torch.int32, 1), call.need(h, "h", torch.bfloat16, (R, I)),
              call.need(codes, "codes", torch.uint8, (R, 2 * I)) if checkpoint else None,
              call.need(scales, "scales", torch.uint8, (R, 2, G)) if checkpoint else None)
     return h, codes, scales

@@ -22,7 +22,7 @@ constexpr int64_t kMaxExpertBytes = (int64_t)1 << 31;    // one expert's matrix,
 constexpr int64_t kMaxGatherBytes = ((int64_t)1 << 32) - ((int64_t)1 << 22);  // a gathered matrix, by unsigned 32-bit
                                                                               // offsets (the tiled kernels' kOob)
 constexpr int kMaxRows = 1 << 26;                        // keeps the tiled products' grids below 2^31 workgroups
-constexpr int64_t kMaxElements = (int64_t)1 << 38;  // keeps the activation's grid below 2^31 workgroups
+constexpr int64_t kMaxGroups = (int64_t)1 << 30;  // rows * scale groups: the activation's grid has under 2^32 threads
 
 bool known_out(moe_out_t t) { return t == MOE_OUT_BF16 || t == MOE_OUT_FP32; }
 
@@ -39,8 +39,14 @@ moe_status_t check_rows(const moe_rows_t& r, int R, int width, int esz, bool inp
 
 moe_status_t check_sizes(int R, int E, int N, int K) {
   if (R < 0 || E < 1 || N < 1 || K < 1) return MOE_ERR_INVALID_ARG;
-  if (R >= kMaxRows || E > kMaxExperts || N % 8 || K % 8 || (int64_t)N * K * 2 >= kMaxExpertBytes) return MOE_ERR_UNSUPPORTED;
+  if (R >= kMaxRows || E > kMaxExperts || N % 8 || K % 8 || (int64_t)N * K * 2 >= kMaxExpertBytes)
+    return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
+}
+
+bool activation_sizes(int R, int I) {
+  return I % 8 == 0 && I < kMaxStride / 2 && R < kMaxRows &&
+         (int64_t)R * ((I + kCkptGroup - 1) / kCkptGroup) < kMaxGroups;
 }
 
 RowsArg rows_arg(const moe_rows_t& r) { return RowsArg{(uint8_t*)r.data, r.stride, r.rows, r.div, r.ids}; }
@@ -104,7 +110,7 @@ moe_status_t moe_grouped_gemm_wgrad(const moe_grouped_wgrad_args_t* a, void* str
 moe_status_t moe_swiglu_checkpoint(const void* gu, int64_t gu_stride, const float* row_weight, int32_t R, int32_t I,
                                    const int32_t* num_rows, void* h, uint8_t* codes, uint8_t* scales, void* stream) {
   if (R < 0 || I < 1) return MOE_ERR_INVALID_ARG;
-  if (I % 8 || I >= kMaxStride / 2 || (int64_t)R * I >= kMaxElements) return MOE_ERR_UNSUPPORTED;
+  if (!activation_sizes(R, I)) return MOE_ERR_UNSUPPORTED;
   if (R == 0) return MOE_OK;
   if (!gu || !aligned(gu, 16) || gu_stride < 2 * (int64_t)I || gu_stride % 8) return MOE_ERR_INVALID_ARG;
   if (gu_stride >= kMaxStride) return MOE_ERR_UNSUPPORTED;
@@ -120,7 +126,7 @@ moe_status_t moe_swiglu_checkpoint_grad(const uint8_t* codes, const uint8_t* sca
                                         const float* row_weight, int32_t R, int32_t I, const int32_t* num_rows,
                                         void* dgu, void* h, float* dweight, void* stream) {
   if (R < 0 || I < 1) return MOE_ERR_INVALID_ARG;
-  if (I % 8 || I >= kMaxStride / 2 || (int64_t)R * I >= kMaxElements) return MOE_ERR_UNSUPPORTED;
+  if (!activation_sizes(R, I)) return MOE_ERR_UNSUPPORTED;
   if (R == 0) return MOE_OK;
   if (!codes || !scales || !dh || !dgu) return MOE_ERR_INVALID_ARG;
   if (!aligned(codes, 16) || !aligned(dh, 16) || !aligned(dgu, 16) || !aligned(h, 16) || !aligned(row_weight, 4) ||

@@ -188,17 +188,20 @@ __global__ __launch_bounds__(WPR < 4 ? 256 : 64 * WPR) void swiglu_grad_kernel(
   }
 }
 
-inline void launch_swiglu_checkpoint(const uint8_t* gu, int64_t stride, const float* w, int R, int I, const int32_t* num_rows,
-                              uint8_t* h, uint8_t* codes, uint8_t* scales, hipStream_t st) {
+inline void launch_swiglu_checkpoint(const uint8_t* gu, int64_t stride, const float* w, int R, int I,
+                                     const int32_t* num_rows, uint8_t* h, uint8_t* codes, uint8_t* scales,
+                                     hipStream_t st) {
   const int64_t threads = (int64_t)R * ((I + kCkptGroup - 1) / kCkptGroup) * kCkptQuad;
   swiglu_checkpoint_kernel<<<(unsigned)((threads + 255) / 256), 256, 0, st>>>(gu, stride, w, R, I, num_rows, h, codes,
                                                                               scales);
 }
 
-inline void launch_swiglu_grad(const uint8_t* codes, const uint8_t* scales, const uint8_t* dh, const float* w, int R, int I,
-                        const int32_t* num_rows, uint8_t* dgu, uint8_t* h, float* dweight, hipStream_t st) {
+inline void launch_swiglu_grad(const uint8_t* codes, const uint8_t* scales, const uint8_t* dh, const float* w, int R,
+                               int I, const int32_t* num_rows, uint8_t* dgu, uint8_t* h, float* dweight,
+                               hipStream_t st) {
   if (I <= 2048)
-    swiglu_grad_kernel<1><<<(unsigned)((R + 3) / 4), 256, 0, st>>>(codes, scales, dh, w, R, I, num_rows, dgu, h, dweight);
+    swiglu_grad_kernel<1><<<(unsigned)((R + 3) / 4), 256, 0, st>>>(codes, scales, dh, w, R, I, num_rows, dgu, h,
+                                                                   dweight);
   else
     swiglu_grad_kernel<4><<<(unsigned)R, 256, 0, st>>>(codes, scales, dh, w, R, I, num_rows, dgu, h, dweight);
 }

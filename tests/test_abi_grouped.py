@@ -124,3 +124,10 @@ def test_binding_refuses_cpu_tensors(m):
         m.grouped_gemm_wgrad(a, a, off)
     with pytest.raises(ValueError):
         m.swiglu_checkpoint(a)
+
+
+@pytest.mark.parametrize("R,I", [(1 << 26, 8), (1 << 25, 1032), (1 << 24, 2048), ((1 << 31) - 1, 8)])
+def test_activation_sizes(m, R, I):
+    # more rows or elements than a grid of 2^32 threads covers
+    assert m.load().moe_swiglu_checkpoint(P, 2 * I, None, R, I, None, P, P, P, None) == UNSUPPORTED
+    assert m.load().moe_swiglu_checkpoint_grad(P, P, P, None, R, I, None, P, P, P, None) == UNSUPPORTED
