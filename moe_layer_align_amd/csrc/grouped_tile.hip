@@ -116,6 +116,12 @@ __device__ __forceinline__ unsigned extent(int64_t rows, int64_t ld, int64_t wid
   return rows > 0 && width > 0 ? (unsigned)((rows - 1) * ld + width) : 0u;
 }
 
+#ifdef __OPTIMIZE__
+constexpr bool kCountLoads = true;
+#else  // an unoptimised build does not hold uniform values in scalar registers, which the instruction takes
+constexpr bool kCountLoads = false;
+#endif
+
 // 16 bytes per lane from base + off (zeros past `bytes`) to dst + 16 * lane.
 // The compiler makes a transpose read from LDS wait for every tracked load into
 // LDS, which would empty the queue of loads in each phase: kernels with
@@ -123,7 +129,7 @@ __device__ __forceinline__ unsigned extent(int64_t rows, int64_t ld, int64_t wid
 // register) and wait for them by count themselves.
 template <bool TRACKED>
 __device__ __forceinline__ void load_lds(const uint8_t* base, unsigned bytes, lds_u8* dst, unsigned off) {
-  if constexpr (TRACKED) {
+  if constexpr (TRACKED || !kCountLoads) {
     const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc((void*)base, (short)0, (int)bytes, kBufferWord3);
     __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (void __attribute__((address_space(3)))*)dst, 16, (int)off, 0, 0, 0);
   } else {
