@@ -14,13 +14,14 @@ struct RowsArg {
   const int32_t* ids;
 };
 
-// Matrix row of grouped row i, or -1 when its id is outside the matrix.
-__device__ __forceinline__ int row_of(const RowsArg& r, int i) {
+// Matrix row of grouped row i with id f (read only where there are ids), or -1
+// when its id is outside the matrix.
+__device__ __forceinline__ int row_of(const RowsArg& r, int i, int f) {
   if (!r.ids) return i < r.rows ? i : -1;
-  const int f = r.ids[i];
   const int m = f < 0 ? -1 : (r.div == 1 ? f : (int)((unsigned)f / (unsigned)r.div));
   return m < r.rows ? m : -1;
 }
+__device__ __forceinline__ int row_of(const RowsArg& r, int i) { return row_of(r, i, r.ids ? r.ids[i] : 0); }
 
 struct GroupedArgs {
   int R, E, N, K;

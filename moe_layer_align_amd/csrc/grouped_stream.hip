@@ -96,6 +96,33 @@ struct Step {
   unsigned s[FT][FMT == kMxfp4 ? 3 : 2];
 };
 
+// A wave's fragments of a stage, from two addresses on (i = 0, 1).  Ahead of a
+// read that it knows of, the compiler waits for all loads into LDS, those of the
+// other stage too.
+template <int FT>
+__device__ __forceinline__ void read_stage(u32x4 (&w)[FT][2], unsigned a0, unsigned a1) {
+  static_assert(FT == 2 || FT == 4, "tiles of a wave");
+  if constexpr (FT == 4)
+    asm volatile(
+        "ds_read_b128 %0, %8\n\tds_read_b128 %1, %9\n\t"
+        "ds_read_b128 %2, %8 offset:2048\n\tds_read_b128 %3, %9 offset:2048\n\t"
+        "ds_read_b128 %4, %8 offset:4096\n\tds_read_b128 %5, %9 offset:4096\n\t"
+        "ds_read_b128 %6, %8 offset:6144\n\tds_read_b128 %7, %9 offset:6144\n\t"
+        "s_waitcnt lgkmcnt(0)"
+        : "=&v"(w[0][0]), "=&v"(w[0][1]), "=&v"(w[1][0]), "=&v"(w[1][1]), "=&v"(w[2][0]), "=&v"(w[2][1]),
+          "=&v"(w[3][0]), "=&v"(w[3][1])
+        : "v"(a0), "v"(a1)
+        : "memory");
+  else
+    asm volatile(
+        "ds_read_b128 %0, %4\n\tds_read_b128 %1, %5\n\t"
+        "ds_read_b128 %2, %4 offset:2048\n\tds_read_b128 %3, %5 offset:2048\n\t"
+        "s_waitcnt lgkmcnt(0)"
+        : "=&v"(w[0][0]), "=&v"(w[0][1]), "=&v"(w[1][0]), "=&v"(w[1][1])
+        : "v"(a0), "v"(a1)
+        : "memory");
+}
+
 // Grouped rows [i0, i0 + 16 NT) of expert e, of which those below hi are
 // written.
 template <int FMT, bool F32, int WK, int FT, int NT>
@@ -216,14 +243,9 @@ __device__ __forceinline__ void pass(const GroupedArgs& a, int e, int n0, int i0
       }
     }
   };
-  const int fa = r16 * 128, fx = pf_mix(r16);  // fragment row of tile f at f * 2048
-  auto read_w = [&](u32x4 (&w)[FT][2], int b) {
-#pragma unroll
-    for (int f = 0; f < FT; ++f)
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-        w[f][i] = *(const lds_u32x4*)(stage + b * kStage + f * 2048 + fa + (((4 * i + q) ^ fx) << 4));
-  };
+  // Fragments of a stage: tile f's row at f * 2048, chunk 4 i + q.
+  const unsigned frag = (unsigned)(uintptr_t)stage + r16 * 128;
+  const unsigned frag0 = frag + ((q ^ pf_mix(r16)) << 4), frag1 = frag + (((4 + q) ^ pf_mix(r16)) << 4);
 
   // One step: its weights have landed when at most the loads issued after them
   // are outstanding, those of the next step (the loads are issued in this order
@@ -241,8 +263,7 @@ __device__ __forceinline__ void pass(const GroupedArgs& a, int e, int n0, int i0
     wait_vm<kLater>();
     fence();
     u32x4 w[FT][2];
-    read_w(w, b);
-    __builtin_amdgcn_s_waitcnt(0xc07f);  // the stage is read: load it again
+    read_stage<FT>(w, frag0 + b * kStage, frag1 + b * kStage);  // the stage is read: load it again
     fence();
     load_w(c + 2 * WK, b);
     fence();
@@ -251,12 +272,24 @@ __device__ __forceinline__ void pass(const GroupedArgs& a, int e, int n0, int i0
     load_rest(g, c + 2 * WK);
     fence();
   };
+  // The rows' ids first: loads return in order, and what follows from them
+  // would wait for weights loaded ahead of them.
+  constexpr int kPer = F32 ? 4 : 8;  // results per thread and store
+  constexpr int kCols = kBand / kPer;
+  constexpr int kStores = (16 * NT * kCols + 255) / 256;  // of the first threads
+  const int last = hi - 1;
+  int in_id[NT], out_id[kStores];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) in_id[t] = a.in.ids ? a.in.ids[min(i0 + 16 * t + r16, last)] : 0;
+#pragma unroll
+  for (int u = 0; u < kStores; ++u) out_id[u] = a.out.ids ? a.out.ids[min(i0 + (u * 256 + tid) / kCols, last)] : 0;
+  fence();
   load_w(wk, 0);
   fence();
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
     const int i = i0 + 16 * t + r16;
-    const int m = i < hi ? (a.in.ids ? row_of(a.in, i) : i - i0) : -1;
+    const int m = i < hi ? (a.in.ids ? row_of(a.in, i, in_id[t]) : i - i0) : -1;
     x0[t] = m >= 0 ? (unsigned)m * (unsigned)(a.in.stride * 2) + 64 * q : kOob;
   }
   load_rest(g0, wk);
@@ -264,10 +297,12 @@ __device__ __forceinline__ void pass(const GroupedArgs& a, int e, int n0, int i0
   load_w(wk + WK, 1);
   fence();
   load_rest(g1, wk + WK);
-  for (int c = wk; c < nstep; c += 2 * WK) {  // loads past the last step read nothing
+  int c = wk;
+  for (; c + WK < nstep; c += 2 * WK) {  // loads past the last step read nothing
     step(g0, c, 0);
     step(g1, c + WK, 1);
   }
+  if (c < nstep) step(g0, c, 0);
   fence();
   wait_vm<0>();  // those loads still write LDS
   lds_f32* const red = (lds_f32*)smem;
@@ -281,12 +316,11 @@ __device__ __forceinline__ void pass(const GroupedArgs& a, int e, int n0, int i0
       for (int v = 0; v < 4; ++v)
         red[(wk * 16 * NT + 16 * t + 4 * q + v) * kLd + 16 * (FT * wb + f) + r16] = acc[f][t][v];
   __syncthreads();
-  constexpr int kPer = F32 ? 4 : 8;  // results per thread and store
-  constexpr int kCols = kBand / kPer;
-  for (int u = tid; u < 16 * NT * kCols; u += 256) {
-    const int row = u / kCols, col = (u % kCols) * kPer, i = i0 + row;
-    if (i >= hi || n0 + col >= a.N) continue;
-    const int m = row_of(a.out, i);
+#pragma unroll
+  for (int u = 0; u < kStores; ++u) {
+    const int at_u = u * 256 + tid, row = at_u / kCols, col = (at_u % kCols) * kPer, i = i0 + row;
+    if (row >= 16 * NT || i >= hi || n0 + col >= a.N) continue;
+    const int m = row_of(a.out, i, out_id[u]);
     if (m < 0) continue;
     f32x4 v[kPer / 4];
 #pragma unroll
