@@ -31,6 +31,8 @@
 // Each wave holds two or four tiles of 16 weight rows, which share the loads of
 // the rows' elements; WK waves split K, step by step, and the others the band;
 // partial sums meet in LDS and are added in wave order.
+#include <type_traits>
+
 #include "grouped.h"
 #include "mfma_tile.h"
 
@@ -258,20 +260,22 @@ __device__ __forceinline__ void pass(const GroupedArgs& a, int e, int n0, int i0
     __builtin_amdgcn_sched_barrier(0);
   };
   Step<FMT, FT, NT> g0, g1;
-  auto step = [&](Step<FMT, FT, NT>& g, int c, int b) {
+  auto step = [&](Step<FMT, FT, NT>& g, int c, int b, auto later, auto more) {
     fence();
-    wait_vm<kLater>();
+    wait_vm<later()>();
     fence();
     u32x4 w[FT][2];
     read_stage<FT>(w, frag0 + b * kStage, frag1 + b * kStage);  // the stage is read: load it again
     fence();
-    load_w(c + 2 * WK, b);
+    if constexpr (more()) load_w(c + 2 * WK, b);
     fence();
     multiply(g, w, c);
     fence();
-    load_rest(g, c + 2 * WK);
+    if constexpr (more()) load_rest(g, c + 2 * WK);
     fence();
   };
+  constexpr std::integral_constant<int, kLater> next_in_flight{};
+  constexpr std::integral_constant<int, 0> none_in_flight{};
   // The rows' ids first: loads return in order, and what follows from them
   // would wait for weights loaded ahead of them.
   constexpr int kPer = F32 ? 4 : 8;  // results per thread and store
@@ -298,13 +302,14 @@ __device__ __forceinline__ void pass(const GroupedArgs& a, int e, int n0, int i0
   fence();
   load_rest(g1, wk + WK);
   int c = wk;
-  for (; c + WK < nstep; c += 2 * WK) {  // loads past the last step read nothing
-    step(g0, c, 0);
-    step(g1, c + WK, 1);
+  for (; c + 2 * WK < nstep; c += 2 * WK) {  // loads past the last step read nothing
+    step(g0, c, 0, next_in_flight, std::true_type{});
+    step(g1, c + WK, 1, next_in_flight, std::true_type{});
   }
-  if (c < nstep) step(g0, c, 0);
+  if (c < nstep) step(g0, c, 0, next_in_flight, std::false_type{});
+  if (c + WK < nstep) step(g1, c + WK, 1, none_in_flight, std::false_type{});
   fence();
-  wait_vm<0>();  // those loads still write LDS
+  wait_vm<0>();  // loads past the last step still write LDS
   lds_f32* const red = (lds_f32*)smem;
   // partial sums: [wk][row][weight row], over the stages
   __syncthreads();
