@@ -8,7 +8,9 @@
 // straight into the MFMA's layout (a lane per row) look up a line per lane and
 // were held to 3 TB/s by it.  The fragments of a stage go to registers at once
 // and its slot is loaded again, so that nearly two stages per wave are in
-// flight.
+// flight.  64 tokens over 256 MXFP4 experts of 4096 x 7168 (2.7 GB): 426 us,
+// 6.4 TB/s; one token through 8 of 28672 x 4096 (125 MB) 30 us, a third of it
+// start and end of the launch and of its waves.
 //
 // A step is 256 of K.  In its chunk i (0, 1) of 128, lane l holds the codes of
 // weight row l%16 at k = 128 i + 32 * (l/16) + 0..31, and its dword j (8 codes)
@@ -408,11 +410,13 @@ void launch(hipStream_t st, const GroupedArgs& a) {
       <<<dim3((a.N + kBand - 1) / kBand, a.R < a.E ? a.R : a.E), 256, 0, st>>>(a);
 }
 
-// Two waves split K where that leaves each two steps (one token, 8 experts of
-// 28672 x 4096: 31 us, 30 to 33 with one to four waves; 64 tokens, 256 experts
-// of 4096 x 7168: 450 us against 490 with one and 463 with four).  Few
+// Waves that split K, by its steps of 256 (1, 2, 4 waves): one where they are
+// few (32 tokens over 128 experts, N 4096: K 1024 50, 50, 68 us; K 2048 96, 86,
+// 91 us), four where they are many and one tile of rows leaves the registers
+// (64 tokens, 256 experts of 4096 x 7168: 479, 432, 426 us; 8 tokens 144, 130,
+// 125; 128 tokens over 32 experts of 4096 x 4096, two tiles: 86, 92, 105).  Few
 // weight rows leave CUs idle: bands of 32 rows with K over four waves (one
-// token, 8 experts of 4096 x 14336: 15 us against 21 with bands of 64 and 35 of
+// token, 8 experts of 4096 x 14336: 14 us against 21 with bands of 64 and 35 of
 // 128).  Passes of 32 rows read the weights once where experts hold more than
 // 8 rows on average; they need too many registers for two waves per SIMD.
 template <int FMT, bool F32, int NT>
@@ -421,6 +425,8 @@ void pick(hipStream_t st, const GroupedArgs& a) {
   const int64_t rows = (int64_t)(a.R < a.E ? a.R : a.E) * a.N;  // weight rows that may be read
   if (rows < 256 * 64)
     launch<FMT, F32, 4, 2, NT>(st, a);
+  else if (NT == 1 && steps >= 24)
+    launch<FMT, F32, 4, 4, 1>(st, a);
   else if (steps >= 4)
     launch<FMT, F32, 2, 4, NT>(st, a);
   else

@@ -267,3 +267,18 @@ def w4_case(fmt, name, N, K, gather, scatter, dtype):
     written[place[:total]] = True
     canvas.check_untouched(written)
     check(canvas.t[torch.from_numpy(place[:total].astype(np.int64)).to(DEV)], ref[:total], mag[:total], n, name)
+
+
+@pytest.mark.parametrize("fmt,K", [("mxfp4", 6016), ("mxfp4", 6208), ("int4", 6016), ("int4", 6272)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_w4_long(fmt, K, dtype):
+    # K split over all four waves of a wide band
+    w4_case(fmt, "many_small", 1544, K, True, False, dtype)
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "int4"])
+@pytest.mark.parametrize("K", [128, 256, 512, 768, 1024, 1280])
+@pytest.mark.parametrize("name", ["many_small", "edges_64"])
+def test_w4_steps(fmt, K, name):
+    # every number of steps from one to five, and a part of one
+    w4_case(fmt, name, 2056, K, False, True, torch.bfloat16)
