@@ -889,10 +889,107 @@ __global__ __launch_bounds__(kThreads) void grouped_wgrad_kernel(TileArgs a) {
   }
 }
 
+// The product for at most 64 rows in all where tiles of 128 p would leave CUs
+// idle: a workgroup per 64 p and expert with rows, whose waves also split each
+// step's c in two (32 p x 32 q each), eight steps of 16 KB in a ring, seven of
+// them in flight.  One token, top-2 of 8 experts, 4096 x 14336: 59 us against 85
+// with tiles of 128 p; top-1, 144 x 2992 13 against 16; top-8 of 128, 1536 x
+// 2048 11.7 against 13.1.
+constexpr int kNarrow = 64;  // p and q of a tile
+constexpr int kNarrowStages = 8;
+constexpr int kNarrowStage = 2 * kNarrow * kC * 2;
+constexpr int kNarrowLds = kNarrowStages * kNarrowStage + 64;
+
+template <bool F32>
+__global__ __launch_bounds__(kThreads) void grouped_narrow_kernel(TileArgs a) {
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  lds_u8* smem = (lds_u8*)smem_raw;
+  const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
+  Tile t;
+  {  // the blockIdx.y-th expert that holds rows
+    lds_int* found = (lds_int*)(smem + kNarrowStages * kNarrowStage);  // e, lo, hi; rows per wave
+    int lo = 0, hi = 0;
+    if (tid < a.E) group_range(a.offsets, tid, a.R, &lo, &hi);
+    const unsigned long long m = __ballot(lo < hi);
+    if (lane == 0) found[4 + wave] = __popcll(m);
+    if (tid == 0) found[0] = a.E;
+    __syncthreads();
+    int before = __popcll(m & lanemask_lt(lane));
+#pragma unroll
+    for (int w = 0; w < 8; ++w) before += w < wave ? found[4 + w] : 0;
+    if (lo < hi && before == (int)blockIdx.y) {
+      found[0] = tid;
+      found[1] = lo;
+      found[2] = hi;
+    }
+    __syncthreads();
+    t.e = uniform(found[0]);
+    if (t.e >= a.E) return;
+    t.lo = t.q0 = uniform(found[1]);
+    t.hi = uniform(found[2]);
+    t.p0 = blockIdx.x * kNarrow;
+  }
+  const int wp = wave & 1, wq = (wave >> 1) & 1, wc = wave >> 2;
+  // wave w loads rows 8w + lane/8 of both operands, lane l the chunk (l%8) ^ pf_mix(row)
+  const int r = 8 * wave + (lane >> 3), chunk = (lane & 7) ^ (lane >> 3) ^ (wave & 1);
+  const int64_t ld = (int64_t)a.K * 2;
+  const uint8_t* pbase = a.w + ((int64_t)t.e * a.N + t.p0) * ld;
+  const unsigned pbytes = extent(min(kNarrow, a.N - t.p0), ld, ld);
+  const unsigned poff = (unsigned)r * (unsigned)ld + (chunk << 4);
+  const uint8_t* qbase = a.q.ids ? a.q.p : a.q.p + t.q0 * a.q.stride * 2;
+  const int m = t.q0 + r < t.hi ? (a.q.ids ? row_of(a.q, t.q0 + r) : r) : -1;
+  const unsigned qoff = m >= 0 ? (unsigned)m * (unsigned)(a.q.stride * 2) + (chunk << 4) : kOob;
+  const int nk = steps_of<2>(a.K);
+  auto issue = [&](int s, int stage) {
+    lds_u8* dst = smem + stage * kNarrowStage + wave * 1024;
+    const bool in = chunk << 3 < a.K - kC * s;
+    load_lds<false>(pbase, pbytes, dst, in ? poff + (unsigned)(s * (kC * 2)) : kOob);
+    load_lds<false>(qbase, kOob, dst + kNarrowStage / 2, in ? qoff + (unsigned)(s * (kC * 2)) : kOob);
+  };
+  const int pa = natural_at(32 * wp, lane) ^ (64 * wc), qa = natural_at(32 * wq, lane) ^ (64 * wc);
+  f32x16 acc;
+#pragma unroll
+  for (int v = 0; v < 16; ++v) acc[v] = 0.0f;
+  for (int i = 0; i < kNarrowStages - 1; ++i) issue(i, i);
+  for (int s = 0; s < nk; ++s) {
+    phase_begin<2 * (kNarrowStages - 2)>();
+    const lds_u8* at = smem + s % kNarrowStages * kNarrowStage;
+    u32x4 p[2], q[2];
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk) {
+      p[kk] = *(const lds_u32x4*)(at + (pa ^ (32 * kk)));
+      q[kk] = *(const lds_u32x4*)(at + kNarrowStage / 2 + (qa ^ (32 * kk)));
+    }
+    issue(s + kNarrowStages - 1, (s + kNarrowStages - 1) % kNarrowStages);  // the slot whose reads the barrier ended
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk) acc = mfma32_bf16(p[kk], q[kk], acc);
+  }
+  phase_begin<0>();  // the loads past the last step (zeros)
+  // the two halves of c: [wave % 4][4 results][lane]
+  lds_f32x4* sums = (lds_f32x4*)smem + (wave & 3) * 256 + lane;
+  if (wc)
+#pragma unroll
+    for (int g = 0; g < 4; ++g) sums[64 * g] = f32x4{acc[4 * g], acc[4 * g + 1], acc[4 * g + 2], acc[4 * g + 3]};
+  __syncthreads();
+  if (wc) return;
+  uint8_t* o = out_row<0, F32>(a, t, 32 * wq + (lane & 31));
+  if (!o) return;
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+    const int p = t.p0 + 32 * wp + 8 * g + 4 * (lane >> 5);
+    if (p >= a.N) continue;
+    const f32x4 v = f32x4{acc[4 * g], acc[4 * g + 1], acc[4 * g + 2], acc[4 * g + 3]} + sums[64 * g];
+    if constexpr (F32)
+      *(f32x4*)(o + (int64_t)p * 4) = v;
+    else
+      *(u32x2*)(o + (int64_t)p * 2) = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+  }
+}
+
 // Launch with `lds` bytes of dynamic LDS; the kernel's ceiling is raised once
 // per device.
 template <typename Kernel>
-bool launch(Kernel kernel, int lds, std::atomic<bool> (&lds_set)[64], int64_t grid, hipStream_t st, const TileArgs& a) {
+bool launch(Kernel kernel, int lds, std::atomic<bool> (&lds_set)[64], dim3 grid, hipStream_t st, const TileArgs& a) {
   int dev = 0;
   if (hipGetDevice(&dev) != hipSuccess || dev < 0) return false;
   if (dev >= 64 || !lds_set[dev].load(std::memory_order_acquire)) {
@@ -900,20 +997,26 @@ bool launch(Kernel kernel, int lds, std::atomic<bool> (&lds_set)[64], int64_t gr
       return false;
     if (dev < 64) lds_set[dev].store(true, std::memory_order_release);
   }
-  kernel<<<(unsigned)grid, kThreads, lds, st>>>(a);
+  kernel<<<grid, kThreads, lds, st>>>(a);
   return true;
 }
 
 template <int OP, bool F32>
 bool launch_rows(int64_t grid, hipStream_t st, const TileArgs& a) {
   static std::atomic<bool> lds_set[64];
-  return launch(grouped_rows_kernel<OP, F32>, lds_bytes(OP), lds_set, grid, st, a);
+  return launch(grouped_rows_kernel<OP, F32>, lds_bytes(OP), lds_set, dim3((unsigned)grid), st, a);
+}
+
+template <bool F32>
+bool launch_narrow(int experts, hipStream_t st, const TileArgs& a) {
+  static std::atomic<bool> lds_set[64];
+  return launch(grouped_narrow_kernel<F32>, kNarrowLds, lds_set, dim3((a.N + kNarrow - 1) / kNarrow, experts), st, a);
 }
 
 template <bool F32, bool ACC, bool IDS>
 bool launch_weights(int64_t grid, hipStream_t st, const TileArgs& a) {
   static std::atomic<bool> lds_set[64];
-  return launch(grouped_wgrad_kernel<F32, ACC, IDS>, lds_bytes(2), lds_set, grid, st, a);
+  return launch(grouped_wgrad_kernel<F32, ACC, IDS>, lds_bytes(2), lds_set, dim3((unsigned)grid), st, a);
 }
 template <bool F32, bool ACC>
 bool launch_weights(int64_t grid, hipStream_t st, const TileArgs& a) {
@@ -948,7 +1051,10 @@ bool launch_grouped_tile(bool dgrad, bool f32, hipStream_t st, const GroupedArgs
   t.w = a.w;
   t.out = a.out;
   // at most R/256 whole row tiles and one rest per expert that holds rows
-  const int64_t rows = a.R / kTile + (a.R < a.E ? a.R : a.E);
+  const int experts = a.R < a.E ? a.R : a.E;
+  const int64_t rows = a.R / kTile + experts;
+  if (!dgrad && a.R <= kNarrow && experts * cdiv(a.N, kHalf) < 8 * kSlots)
+    return f32 ? launch_narrow<true>(experts, st, t) : launch_narrow<false>(experts, st, t);
   const int64_t grid = persistent_grid(rows * cdiv(dgrad ? a.K : a.N, kHalf));
   if (dgrad) return f32 ? launch_rows<1, true>(grid, st, t) : launch_rows<1, false>(grid, st, t);
   return f32 ? launch_rows<0, true>(grid, st, t) : launch_rows<0, false>(grid, st, t);

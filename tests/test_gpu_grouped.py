@@ -282,3 +282,17 @@ def test_w4_long(fmt, K, dtype):
 def test_w4_steps(fmt, K, name):
     # every number of steps from one to five, and a part of one
     w4_case(fmt, name, 2056, K, False, True, torch.bfloat16)
+
+
+NARROW = {"one": [1], "full": [64], "first_of_many": [0] * 5 + [1] + [0] * 506, "some": [3, 0, 17, 1, 0, 33, 5],
+          "last": [0, 0, 0, 2]}
+
+
+@pytest.mark.parametrize("name", list(NARROW))
+@pytest.mark.parametrize("N,K", [(8, 8), (72, 64), (136, 200), (264, 520), (200, 1088)])
+@pytest.mark.parametrize("dtype,scatter", [(torch.bfloat16, False), (torch.float32, True)])
+def test_product_few_rows(name, N, K, dtype, scatter, monkeypatch):
+    # narrow results of at most 64 rows, with the bound on the rows as small as it may be
+    monkeypatch.setitem(COUNTS, name, NARROW[name])
+    monkeypatch.setitem(globals(), "EXTRA", 0)
+    run_product("fwd", name, N, K, scatter, scatter, dtype)
