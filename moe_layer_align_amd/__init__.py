@@ -165,6 +165,24 @@ def _keep_for(t: torch.Tensor, stream) -> None:
         t.record_stream(s)
 
 
+def _empty(shape, dtype, index: int, stream) -> torch.Tensor:
+    """A tensor on GPU `index` for a call on `stream` (None: the current one) to
+    write.  For another stream than the current one it comes from that stream's
+    own memory: a block that was freed on the current stream may still be read by
+    work queued there, which the call does not wait for.  The current stream,
+    where the caller goes on to use it, is recorded on it."""
+    dev = torch.device("cuda", index)
+    if stream is None or _stream(stream) == torch._C._cuda_getCurrentRawStream(index):
+        return torch.empty(shape, dtype=dtype, device=dev)
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = _stream(stream)
+        stream = torch.cuda.ExternalStream(handle, device=dev) if handle else torch.cuda.default_stream(dev)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=dev)
+    t.record_stream(torch.cuda.current_stream(dev))
+    return t
+
+
 def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
     return None if t is None else t.data_ptr()
 
@@ -419,9 +437,9 @@ def fused_forward(x: torch.Tensor, logits: Optional[torch.Tensor], w13: torch.Te
 # ------------------------------------------------------------------ grouped products and the checkpointed activation
 class _Call:
     """The tensors of one call: all on one GPU, whose current stream (or
-    `stream`) it runs on; outputs made here for a side stream are recorded
-    on it.  A decode-sized call takes about ten microseconds on the GPU, so the
-    checks are written for few Python steps."""
+    `stream`) it runs on; outputs made here are from that stream's memory.  A
+    decode-sized call takes about ten microseconds on the GPU, so the checks are
+    written for few Python steps."""
 
     __slots__ = ("index", "given", "stream")
 
@@ -443,10 +461,7 @@ class _Call:
         raise ValueError("%s is on %s, the other operands on cuda:%d" % (name, t.device, self.index))
 
     def empty(self, shape, dtype):
-        t = torch.empty(shape, dtype=dtype, device=torch.device("cuda", self.index))
-        if self.given is not None and self.stream != torch._C._cuda_getCurrentRawStream(self.index):
-            t.record_stream(torch.cuda.ExternalStream(self.stream, device=t.device))
-        return t
+        return _empty(shape, dtype, self.index, self.given)
 
     def vector(self, t, name, dtype, n):
         return None if t is None else self.need(t, name, dtype, (n,))
