@@ -153,24 +153,13 @@ def _stream(stream) -> int:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
-def _keep_for(t: torch.Tensor, stream) -> None:
-    """For a tensor the binding allocates and drops while the call that uses
-    it runs on another stream than the current one: tell torch's caching
-    allocator, so that the memory is not handed out again before that
-    stream's work is done."""
-    if stream is None:
-        return
-    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(_stream(stream))
-    if s.cuda_stream != torch.cuda.current_stream(t.device).cuda_stream:
-        t.record_stream(s)
-
-
-def _empty(shape, dtype, index: int, stream) -> torch.Tensor:
+def _empty(shape, dtype, index: int, stream, scratch: bool = False) -> torch.Tensor:
     """A tensor on GPU `index` for a call on `stream` (None: the current one) to
     write.  For another stream than the current one it comes from that stream's
     own memory: a block that was freed on the current stream may still be read by
     work queued there, which the call does not wait for.  The current stream,
-    where the caller goes on to use it, is recorded on it."""
+    where the caller goes on to use it, is recorded on it, unless it is scratch
+    memory that the call alone uses."""
     dev = torch.device("cuda", index)
     if stream is None or _stream(stream) == torch._C._cuda_getCurrentRawStream(index):
         return torch.empty(shape, dtype=dtype, device=dev)
@@ -179,7 +168,8 @@ def _empty(shape, dtype, index: int, stream) -> torch.Tensor:
         stream = torch.cuda.ExternalStream(handle, device=dev) if handle else torch.cuda.default_stream(dev)
     with torch.cuda.stream(stream):
         t = torch.empty(shape, dtype=dtype, device=dev)
-    t.record_stream(torch.cuda.current_stream(dev))
+    if not scratch:
+        t.record_stream(torch.cuda.current_stream(dev))
     return t
 
 
@@ -206,9 +196,9 @@ def route_topk(logits: torch.Tensor, top_k: int, ids: Optional[torch.Tensor] = N
     M, E = logits.shape
     _need(logits, "logits", torch.float32, (M, E))
     if ids is None:
-        ids = torch.empty(M, top_k, dtype=torch.int32, device=logits.device)
+        ids = _empty((M, top_k), torch.int32, logits.get_device(), stream)
     if weights is None:
-        weights = torch.empty(M, top_k, dtype=torch.float32, device=logits.device)
+        weights = _empty((M, top_k), torch.float32, logits.get_device(), stream)
     _need(ids, "ids", torch.int32, (M, top_k))
     _need(weights, "weights", torch.float32, (M, top_k))
     _check("moe_route_topk", load().moe_route_topk(_ptr(logits), M, E, top_k, _ptr(ids), _ptr(weights),
@@ -224,7 +214,7 @@ def router_logits(x: torch.Tensor, router_w: torch.Tensor, out: Optional[torch.T
     _need(x, "x", torch.bfloat16, (M, H))
     _need(router_w, "router_w", torch.bfloat16, (E, H))
     if out is None:
-        out = torch.empty(M, E, dtype=torch.float32, device=x.device)
+        out = _empty((M, E), torch.float32, x.get_device(), stream)
     _need(out, "out", torch.float32, (M, E))
     _check("moe_router_logits", load().moe_router_logits(_ptr(x), _ptr(router_w), M, E, H, _ptr(out), _stream(stream)))
     return out
@@ -239,12 +229,8 @@ def align(ids: torch.Tensor, E: int, block: int, stream=None):
     M, k = ids.shape
     _need(ids, "ids", torch.int32, (M, k))
     cap = align_capacity(M, k, E, block)
-    dev = ids.device
-    counts = torch.empty(E, dtype=torch.int32, device=dev)
-    offsets = torch.empty(E + 1, dtype=torch.int32, device=dev)
-    sorted_ids = torch.empty(max(cap, 1), dtype=torch.int32, device=dev)
-    block_expert = torch.empty(max(cap // block, 1), dtype=torch.int32, device=dev)
-    num = torch.empty(1, dtype=torch.int32, device=dev)
+    counts, offsets, sorted_ids, block_expert, num = (
+        _empty((n,), torch.int32, ids.get_device(), stream) for n in (E, E + 1, max(cap, 1), max(cap // block, 1), 1))
     _check("moe_align", load().moe_align(_ptr(ids), M, k, E, block, _ptr(counts), _ptr(offsets), _ptr(sorted_ids),
                                          _ptr(block_expert), _ptr(num), _stream(stream)))
     return dict(counts=counts, offsets=offsets, sorted_ids=sorted_ids[:cap], block_expert=block_expert[:cap // block],
@@ -256,7 +242,7 @@ def quant_e4m3(x: torch.Tensor, scale: torch.Tensor, out: Optional[torch.Tensor]
     _need(x, "x", torch.float32, x.shape)
     _need(scale, "scale", torch.float32, (1,))
     if out is None:
-        out = torch.empty(x.shape, dtype=torch.uint8, device=x.device)
+        out = _empty(x.shape, torch.uint8, x.get_device(), stream)
     _need(out, "out", torch.uint8, x.shape)
     _check("moe_quant_e4m3", load().moe_quant_e4m3(_ptr(x), x.numel(), _ptr(scale), _ptr(out), _stream(stream)))
     return out
@@ -374,7 +360,7 @@ def fused_forward(x: torch.Tensor, logits: Optional[torch.Tensor], w13: torch.Te
     if out is None:
         if noalloc:
             raise ValueError("the no-alloc call needs `out`")
-        out = torch.empty(M, H, dtype=torch.bfloat16, device=x.device)
+        out = _empty((M, H), torch.bfloat16, x.get_device(), stream)
     _need(out, "out", torch.bfloat16, (M, H))
     if topk_ids is not None:
         _need(topk_ids, "topk_ids", torch.int32, (M, KS))
@@ -401,8 +387,7 @@ def fused_forward(x: torch.Tensor, logits: Optional[torch.Tensor], w13: torch.Te
     else:
         need = int(lib.moe_fused_workspace_size(M, ES, H, I, KS, DTYPE_FP8 if fp8 else DTYPE_BF16))
         if workspace is None:
-            workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=x.device)
-            _keep_for(workspace, stream)
+            workspace = _empty((max(need, 256),), torch.uint8, x.get_device(), stream, scratch=True)
         if workspace.dtype != torch.uint8 or workspace.device.type != "cuda" or not workspace.is_contiguous():
             raise ValueError("workspace must be a contiguous uint8 GPU tensor")
     args = _FusedArgs(

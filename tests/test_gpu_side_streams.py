@@ -122,3 +122,53 @@ def test_side_stream_call_inside_a_capture(ops):
         assert torch.equal(y, want) and torch.equal(z, want)
         ops["checkpoint"](None)  # eager work between the replays
         torch.cuda.synchronize()
+
+
+def layer_calls():
+    M, LE, k, H, I = 300, 16, 4, 512, 256
+    rng = np.random.default_rng(2)
+    x, logits = bf16(rng, M, H).to(DEV), torch.from_numpy(rng.standard_normal((M, LE)).astype(np.float32)).to(DEV)
+    w13 = bf16(rng, LE, 2 * I, H, scale=H ** -0.5).to(DEV)
+    w2, rw = bf16(rng, LE, H, I, scale=I ** -0.5).to(DEV), bf16(rng, LE, H).to(DEV)
+    ids, _ = moe.route_topk(logits, k)
+    data, scale = logits.flatten().contiguous(), torch.ones(1, device=DEV)
+
+    def align(s):
+        al = moe.align(ids, LE, 16, stream=s)
+        return [al["counts"], al["offsets"], al["num_padded"]]
+
+    return {
+        "route_topk": lambda s: moe.route_topk(logits, k, stream=s),
+        "router_logits": lambda s: moe.router_logits(x, rw, stream=s),
+        "align": align,
+        "quant_e4m3": lambda s: moe.quant_e4m3(data, scale, stream=s),
+        "fused_forward": lambda s: moe.fused_forward(x, logits, w13, w2, k, "bf16", stream=s),
+    }
+
+
+@pytest.mark.parametrize("name", ["route_topk", "router_logits", "align", "quant_e4m3", "fused_forward"])
+def test_the_layers_own_calls(name):
+    # the same of the layer's calls; the workspace that fused_forward makes would be among what overwrites `tmp`
+    say("side-stream memory: %s" % name)
+    call = layer_calls()[name]
+    want = [t.clone() for t in tensors(call(None))]
+    torch.cuda.synchronize()
+    side, big = torch.cuda.Stream(), torch.zeros(64 << 20, device=DEV)
+    sizes = [t.numel() * t.element_size() for t in want] + [
+        moe.workspace_size(300, 16, 512, 256, 4, "bf16")] * (name == "fused_forward")
+    tmp = [torch.full((n,), 3 + i, dtype=torch.uint8, device=DEV) for i, n in enumerate(sizes)]
+    torch.cuda.synchronize()
+    for _ in range(40):
+        big.add_(1.0)
+    sums = [t.to(torch.int32).sum() for t in tmp]
+    freed = [t.data_ptr() for t in tmp]
+    del tmp
+    got = tensors(call(side))
+    for g in got:
+        b = g.numel() * g.element_size()
+        assert not any(p < g.data_ptr() + b and g.data_ptr() < p + n for p, n in zip(freed, sizes)), \
+            "an output lies in memory that queued work reads"
+    torch.cuda.synchronize()
+    assert [int(s) for s in sums] == [(3 + i) * n for i, n in enumerate(sizes)]
+    for g, w in zip(got, want):
+        assert torch.equal(g.view(torch.uint8), w.view(torch.uint8))
