@@ -546,14 +546,17 @@ def grouped_gemm_wgrad(dy: torch.Tensor, a: torch.Tensor, offsets: torch.Tensor,
     """Gradient of grouped_gemm's weights, out[e] = sum of dy[i] a[i]^T over
     expert e's rows (moe_grouped_gemm_wgrad), zeros for an expert without rows:
     dy bf16 [R,N], a bf16 [R,K] -> out [E,N,K] fp32 or bf16.  accumulate: add
-    to `out` (fp32) instead.  Rows may be gathered as in grouped_gemm."""
+    to `out` (fp32) instead.  Rows may be gathered as in grouped_gemm: R is then
+    the number of ids, and an operand without ids holds at least R rows."""
     call = _Call(dy, stream)
     if not isinstance(a, torch.Tensor) or dy.dim() != 2 or a.dim() != 2:
         raise ValueError("dy and a must be [rows, width] tensors")
     E, N, K = offsets.numel() - 1, dy.shape[1], a.shape[1]
     off = call.need(offsets, "offsets", torch.int32, (E + 1,))
-    R = (dy_rows.numel() if dy_rows is not None else a_rows.numel() if a_rows is not None
-         else min(dy.shape[0], a.shape[0]))
+    ids = dy_rows if dy_rows is not None else a_rows
+    R = dy.shape[0] if ids is None else ids.numel()
+    if ids is None and a.shape[0] != R:
+        raise ValueError("without row ids dy and a must have the same number of rows, got %d and %d" % (R, a.shape[0]))
     if out is None:
         if accumulate:
             raise ValueError("accumulate needs `out`")
