@@ -22,7 +22,7 @@ constexpr int64_t kMaxExpertBytes = (int64_t)1 << 31;    // one expert's matrix,
 constexpr int64_t kMaxGatherBytes = ((int64_t)1 << 32) - ((int64_t)1 << 22);  // a gathered matrix, by unsigned 32-bit
                                                                               // offsets (the tiled kernels' kOob)
 constexpr int kMaxRows = 1 << 26;                        // keeps the tiled products' grids below 2^31 workgroups
-constexpr int64_t kMaxGroups = (int64_t)1 << 30;  // rows * scale groups: the activation's grid has under 2^32 threads
+constexpr int64_t kMaxGroups = (int64_t)1 << 30;  // rows * scale groups: the activation's grid has at most 2^32 threads
 
 bool known_out(moe_out_t t) { return t == MOE_OUT_BF16 || t == MOE_OUT_FP32; }
 

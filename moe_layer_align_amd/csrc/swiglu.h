@@ -96,6 +96,14 @@ __device__ __forceinline__ float sigmoid_fast(float x) {
   return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-x * 1.4426950408889634f));
 }
 
+// A launch's workgroups, in two rows of the grid where one would have 2^32
+// threads, which a grid's dimension cannot hold.
+inline dim3 ckpt_grid(int64_t blocks) {
+  const unsigned y = blocks >> 23 ? 2 : 1;
+  return dim3((unsigned)((blocks + y - 1) / y), y);
+}
+__device__ __forceinline__ int ckpt_block() { return (int)(blockIdx.x + blockIdx.y * gridDim.x); }
+
 // Threads run over (row, chunk of 8 columns), the chunks of a row padded to
 // whole quads.
 static __global__ __launch_bounds__(256) void swiglu_checkpoint_kernel(const uint8_t* __restrict__ gu, int64_t stride,
@@ -104,7 +112,7 @@ static __global__ __launch_bounds__(256) void swiglu_checkpoint_kernel(const uin
                                                                 uint8_t* __restrict__ h, uint8_t* __restrict__ codes,
                                                                 uint8_t* __restrict__ scales) {
   const int groups = (I + kCkptGroup - 1) / kCkptGroup, per_row = groups * kCkptQuad;
-  const int64_t base = (int64_t)blockIdx.x * 256;
+  const int64_t base = (int64_t)ckpt_block() * 256;
   const int row0 = (int)(base / per_row);
   const unsigned local = (unsigned)(base - (int64_t)row0 * per_row) + threadIdx.x;
   const int row = row0 + (int)(local / (unsigned)per_row), chunk = (int)(local % (unsigned)per_row);
@@ -148,7 +156,7 @@ __global__ __launch_bounds__(WPR < 4 ? 256 : 64 * WPR) void swiglu_grad_kernel(
   constexpr int kRows = WPR < 4 ? 4 / WPR : 1;  // rows per workgroup
   __shared__ float part[WPR * kRows];
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  const int row = blockIdx.x * kRows + wave / WPR, wr = wave % WPR;
+  const int row0 = ckpt_block() * kRows, row = row0 + wave / WPR, wr = wave % WPR;
   const int groups = (I + kCkptGroup - 1) / kCkptGroup;
   const int limit = num_rows ? min(R, *num_rows) : R;
   float sum = 0.0f;
@@ -180,11 +188,11 @@ __global__ __launch_bounds__(WPR < 4 ? 256 : 64 * WPR) void swiglu_grad_kernel(
   sum = wave_sum(sum);
   if (lane == 0) part[wave] = sum;
   __syncthreads();
-  if (threadIdx.x < kRows && (int)(blockIdx.x * kRows + threadIdx.x) < limit) {
+  if (threadIdx.x < kRows && row0 + (int)threadIdx.x < limit) {
     float t = 0.0f;
 #pragma unroll
     for (int i = 0; i < WPR; ++i) t += part[threadIdx.x * WPR + i];
-    dweight[blockIdx.x * kRows + threadIdx.x] = t;
+    dweight[row0 + threadIdx.x] = t;
   }
 }
 
@@ -192,18 +200,18 @@ inline void launch_swiglu_checkpoint(const uint8_t* gu, int64_t stride, const fl
                                      const int32_t* num_rows, uint8_t* h, uint8_t* codes, uint8_t* scales,
                                      hipStream_t st) {
   const int64_t threads = (int64_t)R * ((I + kCkptGroup - 1) / kCkptGroup) * kCkptQuad;
-  swiglu_checkpoint_kernel<<<(unsigned)((threads + 255) / 256), 256, 0, st>>>(gu, stride, w, R, I, num_rows, h, codes,
-                                                                              scales);
+  swiglu_checkpoint_kernel<<<ckpt_grid((threads + 255) / 256), 256, 0, st>>>(gu, stride, w, R, I, num_rows, h, codes,
+                                                                             scales);
 }
 
 inline void launch_swiglu_grad(const uint8_t* codes, const uint8_t* scales, const uint8_t* dh, const float* w, int R,
                                int I, const int32_t* num_rows, uint8_t* dgu, uint8_t* h, float* dweight,
                                hipStream_t st) {
   if (I <= 2048)
-    swiglu_grad_kernel<1><<<(unsigned)((R + 3) / 4), 256, 0, st>>>(codes, scales, dh, w, R, I, num_rows, dgu, h,
-                                                                   dweight);
+    swiglu_grad_kernel<1><<<ckpt_grid((R + 3) / 4), 256, 0, st>>>(codes, scales, dh, w, R, I, num_rows, dgu, h,
+                                                                  dweight);
   else
-    swiglu_grad_kernel<4><<<(unsigned)R, 256, 0, st>>>(codes, scales, dh, w, R, I, num_rows, dgu, h, dweight);
+    swiglu_grad_kernel<4><<<ckpt_grid(R), 256, 0, st>>>(codes, scales, dh, w, R, I, num_rows, dgu, h, dweight);
 }
 
 }  // namespace moe

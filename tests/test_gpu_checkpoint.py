@@ -325,3 +325,52 @@ def test_training_step(block, M, E, k, H, I):
     near(f64(dw13), DW13, 2, "dw13")
     near(f64(dw2), DW2, 1, "dw2")
     near(got_wt, DWT, 1, "dweight")
+
+
+@pytest.mark.parametrize("R", [(1 << 26) - 1, (1 << 26) - 3, (1 << 26) - 4])
+def test_most_rows(R):
+    # the most rows there may be, of the shortest length: a grid of 2^32 threads
+    say("checkpoint and gradient of %d rows" % R)
+    I, n = 8, 4096
+    rng, gu = inputs(n, I, 8, 1.0)
+    gu, dh, wt = gu.to(DEV), bf16(rng, n, I).to(DEV), torch.from_numpy(rng.uniform(0.2, 1, n).astype(np.float32)).to(DEV)
+    reps = -(-R // n)
+    want = moe.swiglu_checkpoint(gu, wt)
+    got = moe.swiglu_checkpoint(gu.repeat(reps, 1)[:R], wt.repeat(reps)[:R])
+    for g, w in zip(got, want):
+        for lo in (0, R // 2 // n * n, R // n * n - n, R // n * n):
+            m = min(n, R - lo)
+            assert torch.equal(g[lo:lo + m], w[:m])
+    del got
+    want = moe.swiglu_checkpoint_grad(want[1], want[2], dh, wt)
+    _, codes, scales = moe.swiglu_checkpoint(gu)
+    got = moe.swiglu_checkpoint_grad(codes.repeat(reps, 1)[:R], scales.repeat(reps, 1, 1)[:R], dh.repeat(reps, 1)[:R],
+                                     wt.repeat(reps)[:R])
+    for g, w in zip(got, want):
+        for lo in (0, R // 2 // n * n, R // n * n - n, R // n * n):
+            m = min(n, R - lo)
+            assert torch.equal(g[lo:lo + m], w[:m])
+
+
+def test_most_groups():
+    # a bound of almost 2^30 rows times groups, of which the device's own count leaves five rows
+    I, G, n = 544, 17, 5
+    R = ((1 << 30) - 1) // G
+    say("checkpoint and gradient of at most %d rows of %d" % (R, I))
+    rng, gu = inputs(n, I, 9, 1.0)
+    gu, dh = gu.to(DEV), bf16(rng, n, I).to(DEV)
+    num = torch.tensor([n], dtype=torch.int32, device=DEV)
+    h, codes, scales = (torch.zeros(s, dtype=t, device=DEV) for s, t in (
+        ((n, I), torch.bfloat16), ((n, 2 * I), torch.uint8), ((n, 2, G), torch.uint8)))
+    lib = moe.load()
+    stream = torch.cuda.current_stream().cuda_stream
+    assert lib.moe_swiglu_checkpoint(gu.data_ptr(), 2 * I, None, R, I, num.data_ptr(), h.data_ptr(), codes.data_ptr(),
+                                     scales.data_ptr(), stream) == 0
+    for g, w in zip((h, codes, scales), moe.swiglu_checkpoint(gu)):
+        assert torch.equal(g, w)
+    dgu, hw = torch.zeros(n, 2 * I, dtype=torch.bfloat16, device=DEV), torch.zeros_like(h)
+    dwt = torch.zeros(n, device=DEV)
+    assert lib.moe_swiglu_checkpoint_grad(codes.data_ptr(), scales.data_ptr(), dh.data_ptr(), None, R, I, num.data_ptr(),
+                                          dgu.data_ptr(), hw.data_ptr(), dwt.data_ptr(), stream) == 0
+    for g, w in zip((dgu, hw, dwt), moe.swiglu_checkpoint_grad(codes, scales, dh)):
+        assert torch.equal(g, w)
