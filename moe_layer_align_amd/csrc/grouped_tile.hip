@@ -134,13 +134,16 @@ __device__ __forceinline__ void load_lds(const uint8_t* base, unsigned bytes, ld
     __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (void __attribute__((address_space(3)))*)dst, 16, (int)off, 0, 0, 0);
   } else {
     // the no-op is the wait that a vector load needs after its descriptor or m0
-    // was written, which the compiler does not see here
+    // was written, which the compiler does not see here.  m0 is reserved: the
+    // compiler keeps no value in it and does not take it as a clobber, but it
+    // would not know that one it set for its own instruction is gone.  A kernel
+    // has either these loads or its own, and a test of the assembly sees to it.
     const uint64_t p = (uint64_t)base;
     const u32x4 r = {(unsigned)uniform((int)(unsigned)p), (unsigned)uniform((int)((unsigned)(p >> 32) & 0xffffu)),
                      (unsigned)uniform((int)bytes), (unsigned)kBufferWord3};
     const unsigned at = (unsigned)uniform((int)(unsigned)(uintptr_t)dst);
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(at), "v"(off), "s"(r)
-                 : "memory");  // m0: nothing else in these kernels uses it
+                 : "memory");
   }
 }
 

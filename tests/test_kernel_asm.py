@@ -207,3 +207,39 @@ def test_no_kernel_uses_scratch(assembly):
         assert len(sizes) >= 1 and len(names) >= len(sizes), unit
         spill += [(unit, n) for n, v in zip(names, sizes) if v != 0]
     assert not spill, spill[:10]
+
+
+def m0_uses(ins):
+    """(hand-written loads into LDS, other instructions that name m0) of a
+    kernel's instructions: the former are three in a row, the write of m0, the
+    wait and the load."""
+    hand, other, i = 0, [], 0
+    while i < len(ins):
+        if ins[i].startswith("s_mov_b32 m0") and ins[i + 1:i + 2] == ["s_nop 4"] and ins[i + 2].endswith("offen lds"):
+            hand, i = hand + 1, i + 3
+            continue
+        if re.search(r"\bm0\b", ins[i]):
+            other.append(ins[i])
+        i += 1
+    return hand, other
+
+
+def test_scanner_tells_whose_m0_it_is():
+    load = ["s_mov_b32 m0, s3", "s_nop 4", "buffer_load_dwordx4 v1, s[4:7], 0 offen lds"]
+    assert m0_uses(load + ["v_add_u32 v1, v2, v3"] + load) == (2, [])
+    assert m0_uses(load + ["s_add_i32 m0, s87, 0x400", "buffer_load_dwordx4 v1, s[4:7], 0 offen lds"]) == (
+        1, ["s_add_i32 m0, s87, 0x400"])
+
+
+def test_kernels_that_write_m0_by_hand_use_it_for_nothing_else(assembly):
+    # m0 is a reserved register, which an asm statement cannot declare as overwritten: were the compiler to set it for
+    # an instruction of its own ahead of a hand-written load, that instruction would get the load's address
+    found, mixed = 0, []
+    for unit, text in assembly.items():
+        for func in parse_functions(text):
+            hand, other = m0_uses([i for label in func["order"] for i in func["blocks"][label]])
+            found += hand > 0
+            if hand and other:
+                mixed.append((unit, func["name"][:80], other[:3]))
+    assert found >= 10  # the input and weight gradients and the narrow product
+    assert not mixed, mixed
