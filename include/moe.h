@@ -464,11 +464,13 @@ typedef enum {
  * Grouped product: out[i] = W[e] in[i] for every grouped row i of expert e,
  * W [E,N,K] row-major, in of width K, out of width N.
  * 4-bit weights: two codes per byte along K, the low nibble first, rows of
- * K/2 bytes; w_scale E8M0 [E,N,K/32] (codes 2..252, under which every weight
- * is zero or a normal bf16) or bf16 [E,N,K/128].  The weights' values are exact
- * in the product: scales are powers of two in bf16 range (MXFP4), or applied
- * in fp32 to each group's sum (INT4, where an infinite element of a row makes
- * the row's results NaN).  4-bit weights are streamed once per 16 rows of an
+ * K/2 bytes; w_scale E8M0 [E,N,K/32] (code 255 makes its group NaN, as the
+ * format has it) or bf16 [E,N,K/128].  The weights' values are exact in the
+ * product: each is a bf16 (MXFP4; under the scale codes 253 and 254 those of
+ * 2^128 and more, past that type and fp32, are infinities), or the scale is
+ * applied in fp32 to each group's sum (INT4, whose sums take 24 times the
+ * row's elements: a row with an infinite element, or with ones of 2^116 and
+ * more, may give NaN or infinities).  4-bit weights are streamed once per 16 rows of an
  * expert (once per 32 where R > 8 E): the form for decoding.  bf16 weights take tiles
  * of 256 rows, or of 64 for an expert's last or only few rows.
  */

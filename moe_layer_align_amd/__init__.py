@@ -586,8 +586,9 @@ def grouped_gemm_w4(a: torch.Tensor, w4: torch.Tensor, scales: torch.Tensor, off
                     out_rows: Optional[torch.Tensor] = None, out_dtype=torch.bfloat16, stream=None) -> torch.Tensor:
     """grouped_gemm with 4-bit weights, streamed for a few rows per expert:
     w4 uint8 [E,N,K/2], two codes per byte along K (low nibble first).  scales
-    uint8 [E,N,K/32]: OCP MXFP4 (e2m1 codes, E8M0 scales); scales bf16
-    [E,N,K/128]: integers 0..15 standing for -8..7."""
+    uint8 [E,N,K/32]: OCP MXFP4 (e2m1 codes, E8M0 scales; a scale of 255 is NaN,
+    weights of 2^128 and more are infinities); scales bf16 [E,N,K/128]:
+    integers 0..15 standing for -8..7, for rows of elements below 2^116."""
     if not isinstance(w4, torch.Tensor) or w4.dim() != 3:
         raise ValueError("the weights must be a tensor [E, N, K/2]")
     if not isinstance(scales, torch.Tensor) or scales.dtype not in (torch.uint8, torch.bfloat16):
