@@ -466,7 +466,8 @@ class _Call:
         ptr = None
         if ids is not None:
             ptr = self.need(ids, name + "'s row ids", torch.int32, (R,)) or None
-        _sizes(shape[0])
+        if shape[0] >> 31:
+            _sizes(shape[0])
         # one row has no stride of its own, no row at all no address
         return _Rows(t.data_ptr() or 16, step[0] if shape[0] > 1 else width, shape[0], div if ptr else 1, ptr)
 
@@ -481,10 +482,11 @@ class _Call:
             raise MoEError(fn, code)
 
 
-def _sizes(*values):
-    """Sizes that the library takes as int32: ctypes would drop the bits above."""
-    if max(values) > 0x7FFFFFFF or min(values) < -0x80000000:
-        raise ValueError("a size, or a divisor, does not fit 32 bits: %s" % (values,))
+def _sizes(bits: int):
+    """`bits`: the bitwise or of what the library takes as int32, sizes and at
+    most one divisor; ctypes would drop the bits above."""
+    if bits >> 31 not in (0, -1):
+        raise ValueError("a size, or a divisor, does not fit 32 bits")
 
 
 _OUT_TYPE = {torch.bfloat16: 0, torch.float32: 1}
@@ -500,7 +502,7 @@ def _grouped(fn, call, a, w, E, N, K, offsets, out, in_rows, in_div, out_rows, o
     src, dst = (N, K) if fn == "moe_grouped_gemm_dgrad" else (K, N)
     off = call.need(offsets, "offsets", torch.int32, (E + 1,))
     R = a.shape[0] if in_rows is None else in_rows.numel()
-    _sizes(R, E, N, K, in_div)
+    _sizes(R | E | N | K | in_div)
     if out is None:
         out_type = _out_type(out_dtype, "out_dtype")
         out = call.empty((R, dst), out_dtype)
@@ -565,7 +567,8 @@ def grouped_gemm_wgrad(dy: torch.Tensor, a: torch.Tensor, offsets: torch.Tensor,
     R = dy.shape[0] if ids is None else ids.numel()
     if ids is None and a.shape[0] != R:
         raise ValueError("without row ids dy and a must have the same number of rows, got %d and %d" % (R, a.shape[0]))
-    _sizes(R, E, N, K, dy_div, a_div)
+    _sizes(R | E | N | K | dy_div)
+    _sizes(a_div)
     if out is None:
         if accumulate:
             raise ValueError("accumulate needs `out`")
@@ -614,7 +617,7 @@ def swiglu_checkpoint(gu: torch.Tensor, row_weight: Optional[torch.Tensor] = Non
     if gu.dim() != 2 or gu.shape[1] % 2:
         raise ValueError("gu must have shape (rows, 2*I), got %s" % (tuple(gu.shape),))
     R, I = gu.shape[0], gu.shape[1] // 2
-    _sizes(R, I)
+    _sizes(R | I)
     src = call.rows(gu, "gu", torch.bfloat16, 2 * I, None, 1, R)
     if h is None:
         h = call.empty((R, I), torch.bfloat16)
@@ -642,7 +645,7 @@ def swiglu_checkpoint_grad(codes: torch.Tensor, scales: torch.Tensor, dh: torch.
     if dh.dim() != 2:
         raise ValueError("dh must have shape (rows, I), got %s" % (tuple(dh.shape),))
     R, I = dh.shape
-    _sizes(R, I)
+    _sizes(R | I)
     if dgu is None:
         dgu = call.empty((R, 2 * I), torch.bfloat16)
     if h is None:
