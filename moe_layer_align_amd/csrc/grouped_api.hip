@@ -21,7 +21,8 @@ constexpr int64_t kMaxStride = (int64_t)1 << 20;         // elements of a row st
 constexpr int64_t kMaxExpertBytes = (int64_t)1 << 31;    // one expert's matrix, addressed by 32-bit offsets
 constexpr int64_t kMaxGatherBytes = ((int64_t)1 << 32) - ((int64_t)1 << 22);  // a gathered matrix, by unsigned 32-bit
                                                                               // offsets (the tiled kernels' kOob)
-constexpr int kMaxRows = 1 << 26;                        // keeps the tiled products' grids below 2^31 workgroups
+constexpr int kMaxRows = 1 << 26;                        // keeps the tiled products' row tiles times column tiles,
+                                                         // which workgroups number in 32 bits, below 2^31
 constexpr int64_t kMaxGroups = (int64_t)1 << 30;  // rows * scale groups: the activation's grid has at most 2^32 threads
 
 bool known_out(moe_out_t t) { return t == MOE_OUT_BF16 || t == MOE_OUT_FP32; }

@@ -8,8 +8,8 @@
 // straight into the MFMA's layout (a lane per row) look up a line per lane and
 // were held to 3 TB/s by it.  The fragments of a stage go to registers at once
 // and its slot is loaded again, so that nearly two stages per wave are in
-// flight.  64 tokens over 256 MXFP4 experts of 4096 x 7168 (2.7 GB): 426 us,
-// 6.4 TB/s; one token through 8 of 28672 x 4096 (125 MB) 30 us, a third of it
+// flight.  64 tokens over 256 MXFP4 experts of 4096 x 7168 (2.7 GB): 424 to 458
+// us by machine, 5.9 to 6.4 TB/s; one token through 8 of 28672 x 4096 (125 MB) 29 us, a third of it
 // start and end of the launch and of its waves.
 //
 // A step is 256 of K.  In its chunk i (0, 1) of 128, lane l holds the codes of
@@ -413,8 +413,13 @@ void launch(hipStream_t st, const GroupedArgs& a) {
 // Waves that split K, by its steps of 256 (1, 2, 4 waves): one where they are
 // few (32 tokens over 128 experts, N 4096: K 1024 50, 50, 68 us; K 2048 96, 86,
 // 91 us), four where they are many and one tile of rows leaves the registers
-// (64 tokens, 256 experts of 4096 x 7168: 479, 432, 426 us; 8 tokens 144, 130,
-// 125; 128 tokens over 32 experts of 4096 x 4096, two tiles: 86, 92, 105).  Few
+// (128 tokens over 32 experts of 4096 x 4096, two tiles: 86, 92, 105).  Four
+// against two waves, medians of 14 rounds in turn whose quartiles lie within
+// 0.5 % (int4 2 %), over 64 and 8 tokens top-8 of 256 experts with N 4096, 32
+// tokens top-8 of 128 with N 2048 and one token top-2 of 8 with N 28672: time
+// of four 1.01 to 1.21 of two's at 6 and 9 steps, 0.89 to 1.06 at 14 and 20, and
+// at 24, 28 and 40 steps 0.89 to 0.99 (MXFP4) and 0.92 to 1.02 (int4); 8 tokens,
+// K 6144, MXFP4: 138 against 153 us.  Few
 // weight rows leave CUs idle: bands of 32 rows with K over four waves (one
 // token, 8 experts of 4096 x 14336: 14 us against 21 with bands of 64 and 35 of
 // 128).  Passes of 32 rows read the weights once where experts hold more than

@@ -36,15 +36,20 @@
 // kind is run after the larger ones: the small ones are bound by the stream of
 // the weights and fill the CUs that the large ones leave idle at the end.  Both
 // together, 8 experts of about 1024 rows: product N 4096, K 14336 973 -> 816
-// us, input gradient N 28672, K 4096 1966 -> 1709 us.
+// us, input gradient N 28672, K 4096 1966 -> 1709 us.  At most 64 rows in all
+// that make few tiles have a kernel of their own (grouped_narrow_kernel below).
 //
-// Measured, 8 experts of 1024 rows: product N 4096, K 14336 720 us (1.34
-// PFLOP/s), N 28672, K 4096 1476 us (1.30); its input gradient 1488 us (1.29);
-// weight gradient N 4096, K 14336 in fp32 1071 us (0.90), where 16 steps share an
-// epilogue of 256 KB.  A large library product of ordinary operands reaches
-// 1.4 to 1.6 here.  What bounds the steps is power: the first of these takes
-// 585 us on zeros, and 613 to 658 on random values without operand loads.
-// 32 rows over 128 experts, N 1536, K 2048: 40 us, bound by the weights in
+// Measured, 8 experts of 1024 rows, medians on two machines: product N 4096, K
+// 14336 759 us (1.27 PFLOP/s; single launches from 720 to 844), N 28672, K 4096
+// 1493 to 1508 us (1.28); its input gradient 1541 to 1549 us (1.24); weight
+// gradient N 4096, K 14336 in fp32 1039 us (0.93), where 16 steps share an
+// epilogue of 256 KB; with gathered rows each step also loads, divides and
+// masks ids: 1069 us in place, 1184 with dy gathered, 1177 with `in`, 1296 with
+// both (experts of about 1024 rows), and 1471 in place when it accumulates.  A
+// library product of 8192 cubed takes 699 to 716 us (1.54 to 1.57 PFLOP/s).
+// What bounds the steps is power: the first of these takes 566 us on zeros,
+// and took 613 to 658 on random values without operand loads.  32 rows over
+// 128 experts, N 1536, K 2048: 41 to 49 us by machine, bound by the weights in
 // flight (4.5 TB/s over the experts used).
 #include <atomic>
 #include <type_traits>
@@ -895,9 +900,13 @@ __global__ __launch_bounds__(kThreads) void grouped_wgrad_kernel(TileArgs a) {
 // The product for at most 64 rows in all where tiles of 128 p would leave CUs
 // idle: a workgroup per 64 p and expert with rows, whose waves also split each
 // step's c in two (32 p x 32 q each), eight steps of 16 KB in a ring, seven of
-// them in flight.  One token, top-2 of 8 experts, 4096 x 14336: 59 us against 85
-// with tiles of 128 p; top-1, 144 x 2992 13 against 16; top-8 of 128, 1536 x
-// 2048 11.7 against 13.1.
+// them in flight.  Against tiles of 128 p (medians of 14 rounds in turn, whose
+// quartiles lie within 1 %): one token, top-2 of 8 experts, 4096 x 14336 63.9
+// against 87.0 us; top-1, 144 x 2992 12.2 against 15.4; top-8 of 128, 1536 x 2048
+// 11.7 against 12.9; 32 tokens, top-2 of 8, 2048 x 2048 13.5 against 14.0.  Near
+// the rule's border it loses what the wider tiles save in rows' loads: two tokens,
+// top-8 of 128, 1536 x 2048 (192 tiles of 128) 22.1 against 20.6; one token, top-2
+// of 8, 14336 x 4096 (224) 51.9 against 51.3.
 constexpr int kNarrow = 64;  // p and q of a tile
 constexpr int kNarrowStages = 8;
 constexpr int kNarrowStage = 2 * kNarrow * kC * 2;
