@@ -1,0 +1,337 @@
+"""Measured cases of the tokens' way to their experts and back (with the
+gradients of both and of the router), and of the expert products in 8-bit
+integers: what each computes in plain torch, and the calls a user makes of the
+library for the same.
+
+The routing draws top_k experts per token from random logits (some with a
+Zipf-like preference); pair f = token * top_k + slot.  `local` experts of E are
+this process's own, as under expert parallelism: pairs of the others are left
+out here.  Rows are grouped by expert, in pair order within one.
+
+Operators ("op"):
+  dispatch  the tokens' hidden states copied to their experts' rows; the rows' ranges, each pair's row, each row's pair
+  combine   y of a token = sum of routing weight * row over its pairs
+  back      gradients of combine (rows and routing weights), and of the top-k softmax from the latter (logits)
+  int8      y = W[e] a with a quantised per token in the call; 8-bit integer weights with a scale per output channel
+  down      y = W[e] h, h = w SiLU(g) u quantised per row, the same weights
+"""
+import math
+
+import torch
+
+own = False
+
+
+def _routed(op, name, tokens, top_k, E, H, skew, local=0, dtype="bf16"):
+    return dict(name=name, op=op, tokens=tokens, top_k=top_k, E=E, local=local or E, H=H, skew=skew, dtype=dtype)
+
+
+def _product(op, name, tokens, top_k, E, N, K, skew, scatter=False, out="bf16", weighted=False):
+    return dict(name=name, op=op, tokens=tokens, top_k=top_k, E=E, local=E, N=N, K=K, skew=skew, scatter=scatter,
+                out=out, weighted=weighted)
+
+
+def listed():
+    return [
+        # 32 decoding users of a 128-expert layer: launches and latency
+        _routed("dispatch", "dispatch_decode", 32, 8, 128, 2048, 0.0),
+        # the same layer's 4096-token training batch
+        _routed("dispatch", "dispatch_training", 4096, 8, 128, 2048, 0.5),
+        # one of eight processes that share 256 experts, 16384 tokens gathered from all of them
+        _routed("dispatch", "dispatch_shared_256", 16384, 8, 256, 7168, 0.5, local=32),
+        # one decoding user of an 8-expert layer
+        _routed("combine", "combine_one_token", 1, 2, 8, 4096, 0.0),
+        # the 8-expert layer's batch, down products kept in fp32
+        _routed("combine", "combine_8", 8192, 2, 8, 4096, 0.0, dtype="fp32"),
+        # a small layer of odd sizes, some experts nearly empty
+        _routed("back", "back_small_odd", 333, 3, 7, 1032, 1.0),
+        # gradients through the 128-expert layer's combine and router
+        _routed("back", "back_training", 4096, 8, 128, 2048, 0.5),
+        # one decoding user, gate and up products of two of eight experts: the weights' stream
+        _product("int8", "int8_one_token_8", 1, 2, 8, 28672, 4096, 0.0),
+        # 64 users of the 256-expert layer
+        _product("int8", "int8_gate_up_256", 64, 8, 256, 4096, 7168, 0.5),
+        # a prompt of 4096 tokens through the 128-expert layer
+        _product("int8", "int8_prompt_128", 4096, 8, 128, 1536, 2048, 0.5),
+        # a prompt's activations and down products, 8-expert layer
+        _product("down", "down_prompt_8", 4096, 2, 8, 4096, 14336, 0.0),
+        # the same of a small layer of odd sizes, rows weighted and back in pair order
+        _product("down", "down_small_odd", 77, 2, 8, 520, 272, 1.0, True, "bf16", True),
+    ]
+
+
+def _log(rng, lo, hi, step=1):
+    return max(step, int(round(math.exp(rng.uniform(math.log(lo), math.log(hi))) / step)) * step)
+
+
+def draw(rng):
+    op = rng.choice(("dispatch", "dispatch", "combine", "combine", "back", "back", "int8", "int8", "int8", "down",
+                     "down"))
+    skew = rng.choice((0.0, 0.5, 1.0))
+    while True:
+        E = _log(rng, 2, 256)
+        top_k = rng.randint(1, min(8, E))
+        if op in ("int8", "down"):
+            N, K = _log(rng, 128, 16384, 8), _log(rng, 128, 16384, 16)
+            tokens = _log(rng, 1, 8192)
+            if E * N * K <= 256 * 4096 * 7168 and tokens * top_k * N * K <= 8192 * 4096 * 14336:
+                # an activation next to a border between two codes may take either: bf16 results hide that, fp32 would not
+                case = _product(op, "", tokens, top_k, E, N, K, skew, rng.random() < 0.3,
+                                "fp32" if op == "int8" and rng.random() < 0.3 else "bf16", op == "down" and rng.random() < 0.5)
+                break
+        else:
+            tokens, H = _log(rng, 1, 32768), _log(rng, 64, 8192, 8)
+            local = E if rng.random() < 0.7 else rng.randint(1, E)
+            if tokens * top_k * H <= 16384 * 8 * 7168:
+                case = _routed(op, "", tokens, top_k, E, H, skew, local,
+                               "fp32" if op == "combine" and rng.random() < 0.3 else "bf16")
+                break
+    del case["name"]
+    return case
+
+
+def _active(case):
+    """Expected number of experts that hold rows (uniform routing)."""
+    return case["E"] * (1.0 - (1.0 - case["top_k"] / case["E"]) ** case["tokens"])
+
+
+def work(case):
+    T, k, E = case["tokens"], case["top_k"], case["E"]
+    P = T * k
+    if case["op"] in ("dispatch", "combine", "back"):
+        H, share = case["H"], case["local"] / E
+        rows = P * share
+        used = T * (1.0 - (1.0 - share) ** k)  # tokens with a pair here
+        if case["op"] == "dispatch":
+            return {"bytes": int(2 * H * (used + rows) + 12 * P + 4 * case["local"]), "flops": P}
+        if case["op"] == "combine":
+            return {"bytes": int((4 if case["dtype"] == "fp32" else 2) * H * rows + 2 * H * T + 8 * P),
+                    "flops": int(2 * rows * H)}
+        return {"bytes": int(2 * H * (used + 2 * rows) + 16 * P + 4 * T * E), "flops": int(3 * rows * H + 5 * P)}
+    N, K = case["N"], case["K"]
+    ins = 2 * T * K if case["op"] == "int8" else 4 * P * K
+    index = 4 * P * (int(case["op"] == "int8") + int(case["scatter"]) + int(case["weighted"])) + 4 * (E + 1)
+    weights = _active(case) * N * (K + 4)
+    return {"bytes": int(ins + weights + (4 if case["out"] == "fp32" else 2) * P * N + index), "flops": 2 * P * N * K}
+
+
+def _normal(g, *shape, dtype=torch.bfloat16):
+    return torch.randn(*shape, generator=g, device="cuda", dtype=dtype)
+
+
+def prepare(case, seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed * 7919 + 17)
+    T, k, E, local = case["tokens"], case["top_k"], case["E"], case["local"]
+    P, first = T * k, 0 if case["local"] == case["E"] else min(case["local"], case["E"] - case["local"])
+    st = {"case": case, "first": first}
+    logits = torch.randn(T, E, generator=g, device="cuda")
+    # a Zipf-like preference over the experts in an order of their own, so that no process's experts are all popular
+    rank = torch.randperm(E, generator=g, device="cuda").float() + 1.0
+    logits -= case["skew"] * torch.log(rank)
+    top, experts = torch.topk(logits, k, dim=1)
+    experts = experts.to(torch.int32)
+    weights = torch.softmax(top, dim=1)
+    # the grouping as an earlier call of the program has it
+    here = experts.reshape(-1).long() - first
+    here = torch.where((here >= 0) & (here < local), here, local)
+    order = torch.argsort(here, stable=True)
+    offsets = torch.zeros(local + 1, dtype=torch.int32, device="cuda")
+    offsets[1:] = torch.cumsum(torch.bincount(here, minlength=local + 1)[:local], 0).to(torch.int32)
+    place = torch.empty(P, dtype=torch.int64, device="cuda")
+    place[order] = torch.arange(P, device="cuda")
+    positions = torch.where(here < local, place, -1).to(torch.int32).view(T, k)
+    if case["op"] in ("dispatch", "combine", "back"):
+        H = case["H"]
+        st.update(ids=experts, weights=weights)
+        if case["op"] == "dispatch":
+            st["x"] = _normal(g, T, H)
+        else:
+            st["positions"] = positions
+            st["rows"] = _normal(g, P, H, dtype=torch.float32 if case["dtype"] == "fp32" else torch.bfloat16)
+            st["rows"][offsets[local]:] = 0.0
+        if case["op"] == "back":
+            st["dy"] = _normal(g, T, H) * 0.125
+        # with experts elsewhere, the rows behind the last one stay as they are in the program's buffer
+        st["buffer"] = None
+        if local < E:
+            st["buffer"] = torch.zeros(P, H, dtype=torch.bfloat16, device="cuda")
+        return st
+    N, K = case["N"], case["K"]
+    st.update(offsets=offsets, bounds=offsets.tolist(), pairs=order.to(torch.int32))
+    # codes of normal weights whose largest lie near 127, and a scale per channel that makes unit-variance results
+    st["w"] = (_normal(g, E, N, K) * 30.0).round_().clamp_(-127, 127).to(torch.int8)
+    st["w_scale"] = (0.5 + torch.rand(E, N, generator=g, device="cuda")) * (K ** -0.5 / 30.0)
+    if case["op"] == "int8":
+        # hidden states: tokens of different size
+        st["a"] = _normal(g, T, K) * torch.exp(0.5 * _normal(g, T, 1))
+    else:
+        st["a"] = _normal(g, P, 2 * K) * torch.exp(0.5 * _normal(g, P, 1))
+        st["row_weight"] = torch.rand(P, generator=g, device="cuda") if case["weighted"] else None
+    return st
+
+
+# ------------------------------------------------------------------ plain forms
+def _dispatch_plain(st):
+    c, x = st["case"], st["x"]
+    k, local = c["top_k"], c["local"]
+    P = c["tokens"] * k
+    e = st["ids"].view(-1).long() - st["first"]
+    e = torch.where((e >= 0) & (e < local), e, local)
+    order = torch.argsort(e, stable=True)
+    row = torch.arange(P, device=x.device)
+    counts = (e[:, None] == torch.arange(local, device=x.device)).sum(0)
+    offsets = torch.zeros(local + 1, dtype=torch.int64, device=x.device)
+    offsets[1:] = torch.cumsum(counts, 0)
+    here = row < offsets[local]
+    rows = torch.where(here[:, None], x[order // k], 0.0).to(x.dtype)
+    positions = torch.empty_like(row)
+    positions[order] = torch.where(here, row, -1)
+    return {"rows": rows, "offsets": offsets.to(torch.int32), "positions": positions.to(torch.int32).view(-1, k),
+            "pairs": torch.where(here, order, -1).to(torch.int32)}
+
+
+def _combine_plain(st):
+    pos, w = st["positions"].long(), st["weights"]
+    terms = torch.where(pos >= 0, w, 0.0)[:, :, None] * st["rows"][pos.clamp(min=0)].float()
+    return terms.sum(1).to(torch.bfloat16)
+
+
+def _back_plain(st):
+    c = st["case"]
+    pos, w, ids = st["positions"].long(), st["weights"], st["ids"].long()
+    dy, here = st["dy"].float()[:, None, :], st["positions"] >= 0
+    dweights = torch.where(here, (dy * st["rows"][pos.clamp(min=0)].float()).sum(2), 0.0)
+    drows = torch.zeros_like(st["rows"])
+    drows[pos[here]] = (dy * w[:, :, None]).to(drows.dtype)[here]
+    dlogits = torch.zeros(c["tokens"], c["E"], device=w.device)
+    dlogits.scatter_(1, ids, w * (dweights - (w * dweights).sum(1, keepdim=True)))
+    return {"drows": drows, "dweights": dweights, "dlogits": dlogits}
+
+
+def _quantised(v):
+    """Rows of float64 -> the integers round(127 v / max|v|), ties to even, and the fp32 scales max|v| / 127."""
+    top = v.abs().amax(1, keepdim=True)
+    return torch.round(127.0 * v / top.clamp(min=1e-300)).float(), (top / 127.0).float()
+
+
+def _product_plain(st):
+    c = st["case"]
+    K = c["K"]
+    if c["op"] == "int8":
+        codes, scale = _quantised(st["a"].double())
+        token = st["pairs"].long() // c["top_k"]
+        codes, scale = codes[token], scale[token]
+    else:
+        g, u = st["a"][:, :K].double(), st["a"][:, K:].double()
+        codes, scale = _quantised(g / (1.0 + torch.exp(-g)) * u)
+        if c["weighted"]:
+            scale = scale * st["row_weight"][:, None]
+    out = torch.empty(c["tokens"] * c["top_k"], c["N"], device=codes.device)
+    # one matrix product for each expert that holds rows
+    for e, (lo, hi) in enumerate(zip(st["bounds"], st["bounds"][1:])):
+        if lo < hi:
+            out[lo:hi] = (codes[lo:hi] @ st["w"][e].float().t()) * scale[lo:hi] * st["w_scale"][e]
+    out = out.to(torch.float32 if c["out"] == "fp32" else torch.bfloat16)
+    if c["scatter"]:
+        placed = torch.empty_like(out)
+        placed[st["pairs"].long()] = out
+        return placed
+    return out
+
+
+# ------------------------------------------------------------------ one pass
+def run(state):
+    c = state["case"]
+    if not own:
+        return {"dispatch": _dispatch_plain, "combine": _combine_plain, "back": _back_plain}.get(
+            c["op"], _product_plain)(state)
+    import moe_layer_align_amd as moe
+    if c["op"] == "dispatch":
+        rows, offsets, positions, pairs = moe.dispatch(state["x"], state["ids"], c["local"], state["buffer"],
+                                                       first_expert=state["first"])
+        return {"rows": rows, "offsets": offsets, "positions": positions, "pairs": pairs}
+    if c["op"] == "combine":
+        return moe.combine(state["rows"], state["positions"], state["weights"], out_dtype=torch.bfloat16)
+    if c["op"] == "back":
+        drows, dweights = moe.combine_grad(state["dy"], state["rows"], state["positions"], state["weights"],
+                                           state["buffer"])
+        return {"drows": drows, "dweights": dweights,
+                "dlogits": moe.route_topk_grad(state["ids"], state["weights"], dweights, c["E"])}
+    dtype = torch.float32 if c["out"] == "fp32" else torch.bfloat16
+    to = state["pairs"] if c["scatter"] else None
+    if c["op"] == "int8":
+        return moe.grouped_gemm_int8(state["a"], state["w"], state["w_scale"], state["offsets"],
+                                     a_rows=state["pairs"], a_div=c["top_k"], out_rows=to, out_dtype=dtype)
+    codes, scales = moe.swiglu_int8(state["a"], state["row_weight"])
+    return moe.grouped_gemm_int8(codes, state["w"], state["w_scale"], state["offsets"], a_scale=scales, out_rows=to,
+                                 out_dtype=dtype)
+
+
+# ------------------------------------------------------------------ 64 bits
+def exact(case, seed):
+    st = prepare(case, seed)
+    d = torch.float64
+    T, k, E, local, first = case["tokens"], case["top_k"], case["E"], case["local"], st["first"]
+    P = T * k
+    if case["op"] == "dispatch":
+        # a pair's row: the pairs of earlier experts, and those of its own expert before it
+        flat = st["ids"].reshape(-1).tolist()
+        held = [[] for _ in range(local)]
+        for f, e in enumerate(flat):
+            if first <= e < first + local:
+                held[e - first].append(f)
+        pairs, offsets = [], [0]
+        for h in held:
+            pairs += h
+            offsets.append(len(pairs))
+        rows = torch.zeros(P, case["H"], dtype=d, device="cuda")
+        at = torch.tensor(pairs, dtype=torch.int64, device="cuda")
+        rows[:len(pairs)] = st["x"].to(d)[torch.div(at, k, rounding_mode="floor")]
+        positions = torch.full((P,), -1, dtype=torch.int64, device="cuda")
+        positions[at] = torch.arange(len(pairs), device="cuda")
+        return {"rows": rows, "offsets": torch.tensor(offsets, dtype=torch.int32),
+                "positions": positions.to(torch.int32).view(T, k),
+                "pairs": torch.tensor(pairs + [-1] * (P - len(pairs)), dtype=torch.int32)}
+    if case["op"] in ("combine", "back"):
+        H, w = case["H"], st["weights"].to(d)
+        pos, pair = st["positions"].reshape(-1), torch.arange(P, device="cuda")
+        pair = pair[pos >= 0]
+        pos, token = pos[pos >= 0].long(), torch.div(pair, k, rounding_mode="floor")
+        if case["op"] == "combine":
+            y = torch.zeros(T, H, dtype=d, device="cuda")
+            for j in range(k):  # a token's slots one after the other: no two equal places in one step
+                m = pair % k == j
+                y[token[m]] += w.reshape(-1)[pair[m], None] * st["rows"][pos[m]].to(d)
+            return y
+        dw = torch.zeros(P, dtype=d, device="cuda")
+        drows = torch.zeros(P, H, dtype=d, device="cuda")
+        for part in torch.split(torch.arange(len(pair), device="cuda"), 8192):
+            dy = st["dy"][token[part]].to(d)
+            dw[pair[part]] = torch.matmul(dy[:, None, :], st["rows"][pos[part]].to(d)[:, :, None])[:, 0, 0]
+            drows[pos[part]] = w.reshape(-1)[pair[part], None] * dy
+        dw = dw.view(T, k)
+        # the softmax's Jacobian: diag(w) - w w^T
+        jac = torch.diag_embed(w) - w[:, :, None] * w[:, None, :]
+        dlogits = torch.zeros(T, E, dtype=d, device="cuda")
+        dlogits[torch.arange(T, device="cuda")[:, None], st["ids"].long()] = torch.matmul(jac, dw[:, :, None])[:, :, 0]
+        return {"drows": drows, "dweights": dw, "dlogits": dlogits}
+    N, K = case["N"], case["K"]
+    out = torch.zeros(P, N, dtype=d, device="cuda")
+    for e, (lo, hi) in enumerate(zip(st["bounds"], st["bounds"][1:])):
+        if lo == hi:
+            continue
+        if case["op"] == "int8":
+            v = st["a"][torch.div(st["pairs"][lo:hi].long(), k, rounding_mode="floor")].to(d)
+        else:
+            g, u = st["a"][lo:hi].to(d).split(K, dim=1)
+            v = g * torch.sigmoid(g) * u
+        step = v.abs().max(dim=1, keepdim=True).values / 127.0
+        whole = torch.floor(v * 127.0 / (step * 127.0))
+        part = v * 127.0 / (step * 127.0) - whole
+        up = (part > 0.5) | ((part == 0.5) & (whole % 2 != 0))
+        r = torch.matmul(whole + up.to(d), st["w"][e].to(d).t()) * step * st["w_scale"][e].to(d)
+        if case["op"] == "down" and case["weighted"]:
+            r = r * st["row_weight"][lo:hi, None].to(d)
+        out[st["pairs"][lo:hi].long() if case["scatter"] else slice(lo, hi)] = r
+    return out
