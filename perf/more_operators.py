@@ -75,9 +75,11 @@ def draw(rng):
             N, K = _log(rng, 128, 16384, 8), _log(rng, 128, 16384, 16)
             tokens = _log(rng, 1, 8192)
             if E * N * K <= 256 * 4096 * 7168 and tokens * top_k * N * K <= 8192 * 4096 * 14336:
-                # an activation next to a border between two codes may take either: bf16 results hide that, fp32 would not
-                case = _product(op, "", tokens, top_k, E, N, K, skew, rng.random() < 0.3,
-                                "fp32" if op == "int8" and rng.random() < 0.3 else "bf16", op == "down" and rng.random() < 0.5)
+                # an activation next to a border between two codes may take either: bf16 results hide that, and
+                # fp32 would not
+                out = "fp32" if op == "int8" and rng.random() < 0.3 else "bf16"
+                case = _product(op, "", tokens, top_k, E, N, K, skew, rng.random() < 0.3, out,
+                                op == "down" and rng.random() < 0.5)
                 break
         else:
             tokens, H = _log(rng, 1, 32768), _log(rng, 64, 8192, 8)
