@@ -551,6 +551,172 @@ moe_status_t moe_swiglu_checkpoint_grad(const uint8_t* codes, const uint8_t* sca
                                         const float* row_weight, int32_t R, int32_t I, const int32_t* num_rows,
                                         void* dgu, void* h, float* dweight, void* stream);
 
+/* ------------------------------------------------------------------------
+ * The tokens' way to their experts and back as operators of their own, with
+ * the gradients, and the router's: what stands around the grouped products in
+ * a training step, and around the exchange of tokens between processes that
+ * each hold some of the experts.
+ *
+ * Conventions, besides those at the top:
+ *  - Pair f = t*top_k + j is slot j of token t; `positions` [M,top_k] names its
+ *    grouped row, or a negative number (or one >= R) where it has none.
+ *  - Sums are in fp32 in an order fixed by the sizes, rounded once to the
+ *    output's type: the same bits on every call.  No floating-point atomics.
+ *  - MOE_ERR_UNSUPPORTED: M*top_k >= 2^26, top_k > 16, E > 512, H not a
+ *    multiple of 8 (dispatch: row_bytes not one of 16), a row stride of 2^22
+ *    bytes or more.  MOE_ERR_INVALID_ARG: NULL or misaligned pointers (16
+ *    bytes; 4 for int32 and fp32 vectors), negative sizes, a stride below the
+ *    width or not a multiple of 16 bytes, an unknown type.
+ *  - Outputs must not overlap inputs or each other.
+ */
+
+/*
+ * Dispatch: the tokens' rows copied to rows grouped by expert.  The experts
+ * are first_expert .. first_expert+E-1 of those that the ids name; a pair whose
+ * id is outside is left out (an expert of another process, a token of the
+ * padding with id -1).
+ *   offsets   [E+1]      rows of expert first_expert+e: offsets[e] <= i < offsets[e+1]
+ *   positions [M,top_k]  the pair's row, -1 for a pair left out
+ *   pairs     [M*top_k]  the row's pair, -1 for rows at or beyond offsets[E]
+ *   rows      row positions[t,j] = row t of x, byte for byte; rows at or beyond
+ *             offsets[E] are not written
+ * An expert's rows are in the order of their pairs.  The ids of a token may be
+ * equal.  The gradient of x is moe_combine of the rows' gradients without
+ * weights.
+ * workspace: moe_dispatch_workspace_size bytes (0 for up to 4096 pairs), 16-byte
+ * aligned, its contents without meaning before and after the call.
+ */
+typedef struct {
+  int32_t M, top_k, E, first_expert;
+  const int32_t* ids;  /* [M,top_k] */
+  const void* x;       /* [M] rows of row_bytes */
+  int64_t x_stride;    /* bytes */
+  int32_t row_bytes;
+  void* rows;          /* [M*top_k] rows of row_bytes */
+  int64_t rows_stride; /* bytes */
+  int32_t* offsets;
+  int32_t* positions;
+  int32_t* pairs;
+  void* workspace;
+  size_t workspace_bytes;
+} moe_dispatch_args_t;
+
+/* Host-only; 0 for invalid or unsupported sizes too. */
+size_t moe_dispatch_workspace_size(int32_t M, int32_t top_k, int32_t E);
+moe_status_t moe_dispatch(const moe_dispatch_args_t* args, void* stream);
+
+/*
+ * Combine: y[t] = sum over j of weights[t,j] * rows[positions[t,j]], over the
+ * slots that have a row (none: zeros), in the order of the slots.  weights NULL:
+ * ones.  A row or weight without a place in the sum is not read into it,
+ * whatever it holds.
+ */
+typedef struct {
+  int32_t M, top_k, H, R;   /* rows holds R rows */
+  const void* rows;         /* [R,H] bf16 or fp32 */
+  int64_t rows_stride;      /* elements */
+  moe_out_t rows_type;
+  const int32_t* positions; /* [M,top_k] */
+  const float* weights;     /* [M,top_k] or NULL */
+  void* y;                  /* [M,H] bf16 or fp32 */
+  int64_t y_stride;         /* elements */
+  moe_out_t y_type;
+} moe_combine_args_t;
+
+moe_status_t moe_combine(const moe_combine_args_t* args, void* stream);
+
+/*
+ * Gradient of moe_combine, from dy, the gradient of y:
+ *   drows[positions[t,j]] = weights[t,j] * dy[t]; rows that no position names
+ *   are not written (two equal positions leave either's result); NULL = not wanted
+ *   dweights[t,j] = sum over the columns of dy[t] * rows[positions[t,j]], 0 for
+ *   a slot without a row; NULL, with rows NULL, = not wanted
+ */
+typedef struct {
+  int32_t M, top_k, H, R;
+  const void* dy;           /* [M,H] bf16 or fp32 */
+  int64_t dy_stride;        /* elements */
+  moe_out_t dy_type;
+  const void* rows;         /* [R,H] bf16 or fp32, as given to moe_combine */
+  int64_t rows_stride;
+  moe_out_t rows_type;
+  const int32_t* positions; /* [M,top_k] */
+  const float* weights;     /* [M,top_k] or NULL (ones) */
+  void* drows;              /* [R,H] bf16 or fp32 */
+  int64_t drows_stride;
+  moe_out_t drows_type;
+  float* dweights;          /* [M,top_k] */
+} moe_combine_grad_args_t;
+
+moe_status_t moe_combine_grad(const moe_combine_grad_args_t* args, void* stream);
+
+/*
+ * Gradient of moe_route_topk's weights: with w = topk_weights[t], d =
+ * dweights[t], dlogits[t, topk_ids[t,j]] = w_j (d_j - sum_i w_i d_i) and zero
+ * for the other experts; dlogits fp32 [M,E].  Slots whose id is outside [0,E)
+ * take no part.
+ */
+moe_status_t moe_route_topk_grad(const int32_t* topk_ids, const float* topk_weights, const float* dweights, int32_t M,
+                                 int32_t E, int32_t top_k, float* dlogits, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Expert products in 8-bit integers: activations with one scale per row
+ * (token), weights with one per output channel, both symmetric.
+ *
+ * Rows to 8 bits, x [M,K] bf16 with a row stride in elements:
+ *   top = max |x[i]|, scales[i] = top/127, codes[i,k] = 127*x[i,k]/top rounded
+ *   to the nearest integer, ties to even (exactly: the quotient is not rounded
+ *   before).  A row of zeros: scale 1.  A row that holds an infinity or a NaN:
+ *   scale NaN, codes 0.
+ * The same call lays out weights: a row of W is an output channel.
+ * codes int8 [M,K], scales fp32 [M].  K a multiple of 16 and at most 2^16, M
+ * below 2^26, x_stride below 2^20 (else MOE_ERR_UNSUPPORTED).
+ */
+moe_status_t moe_quant_int8(const void* x, int64_t x_stride, int32_t M, int32_t K, int8_t* codes, float* scales,
+                            void* stream);
+
+/*
+ * Gated activation to 8 bits: h = SiLU(g)*u of gu [R,2I] bf16 (columns [0,I)
+ * gate, [I,2I) up; row stride gu_stride) in fp32, then rows to 8 bits as above;
+ * scales[i] is multiplied by row_weight[i] (fp32 [R], NULL: ones), so that the
+ * down product comes out weighted.  num_rows: device int32 or NULL; rows at or
+ * beyond *num_rows are neither read nor written.  I a multiple of 16 and at
+ * most 2^16, R below 2^26, gu_stride below 2^20.
+ */
+moe_status_t moe_swiglu_int8(const void* gu, int64_t gu_stride, const float* row_weight, int32_t R, int32_t I,
+                             const int32_t* num_rows, int8_t* codes, float* scales, void* stream);
+
+/*
+ * Grouped product of 8-bit integers: with q the codes of grouped row i of
+ * expert e and s its scale,
+ *   out[i,n] = s * w_scale[e,n] * sum over k of q[k] * w[e,n,k]
+ * the sum in int32, exact.  in.data: codes int8 with in_scale fp32 [in.rows]
+ * (one per row of the matrix that the ids choose from), or, with in_scale NULL,
+ * bf16 rows, which the call turns to 8 bits itself (moe_quant_int8 of all
+ * in.rows rows) in `workspace` (moe_grouped_int8_workspace_size bytes, 256-byte
+ * aligned).  in.stride counts elements of their type.  The other conventions
+ * are the grouped products' (rows, offsets, ids, out, errors); K is a multiple
+ * of 16 below 2^17 (bf16 rows: at most 2^16), N of 8, an expert's matrix below
+ * 2^31 bytes, in.rows below 2^26.
+ */
+typedef struct {
+  int32_t R, E, N, K;
+  const int32_t* offsets; /* [E+1] */
+  moe_rows_t in;          /* [in.rows,K] */
+  const float* in_scale;
+  const int8_t* w;        /* [E,N,K] */
+  const float* w_scale;   /* [E,N], 16-byte aligned */
+  moe_rows_t out;         /* bf16 or fp32 */
+  moe_out_t out_type;
+  void* workspace;
+  size_t workspace_bytes;
+} moe_grouped_int8_args_t;
+
+/* Host-only: bytes that moe_grouped_gemm_int8 needs for bf16 rows; 0 for invalid
+ * or unsupported sizes. */
+size_t moe_grouped_int8_workspace_size(int32_t rows, int32_t K);
+moe_status_t moe_grouped_gemm_int8(const moe_grouped_int8_args_t* args, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -38,6 +38,15 @@ struct GroupedWgradArgs {
   uint8_t* dw;
 };
 
+struct GroupedInt8Args {
+  int R, E, N, K;
+  const int32_t* offsets;
+  RowsArg in, out;
+  const float* in_scale;  // by matrix row
+  const uint8_t* w;
+  const float* w_scale;   // [E,N]
+};
+
 // Row range of expert e, its ends clamped so that no offset leads outside
 // [0, R].
 __device__ __forceinline__ void group_range(const int32_t* offsets, int e, int R, int* lo, int* hi) {
@@ -50,5 +59,7 @@ __device__ __forceinline__ void group_range(const int32_t* offsets, int e, int R
 bool launch_grouped_tile(bool dgrad, bool f32, hipStream_t st, const GroupedArgs& a);
 bool launch_grouped_wgrad(bool f32, bool accumulate, hipStream_t st, const GroupedWgradArgs& a);
 bool launch_grouped_stream(int format, bool f32, hipStream_t st, const GroupedArgs& a);
+bool launch_grouped_int8(bool f32, hipStream_t st, const GroupedInt8Args& a);
+bool launch_grouped_tile_int8(bool f32, hipStream_t st, const GroupedInt8Args& a);
 
 }  // namespace moe

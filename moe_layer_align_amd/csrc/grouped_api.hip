@@ -7,6 +7,7 @@
 
 #include "moe.h"
 #include "grouped.h"
+#include "int8.h"
 #include "swiglu.h"
 
 using namespace moe;
@@ -24,6 +25,8 @@ constexpr int64_t kMaxGatherBytes = ((int64_t)1 << 32) - ((int64_t)1 << 22);  //
 constexpr int kMaxRows = 1 << 26;                        // keeps the tiled products' row tiles times column tiles,
                                                          // which workgroups number in 32 bits, below 2^31
 constexpr int64_t kMaxGroups = (int64_t)1 << 30;  // rows * scale groups: the activation's grid has at most 2^32 threads
+
+constexpr int kMaxInt8Sum = 1 << 17;  // terms of a sum of products of 8-bit integers: |sum| < 2^31
 
 bool known_out(moe_out_t t) { return t == MOE_OUT_BF16 || t == MOE_OUT_FP32; }
 
@@ -49,6 +52,11 @@ bool activation_sizes(int R, int I) {
   return I % 8 == 0 && I < kMaxStride / 2 && R < kMaxRows &&
          (int64_t)R * ((I + kCkptGroup - 1) / kCkptGroup) < kMaxGroups;
 }
+
+// Rows to 8-bit integers: M rows of K codes.
+bool int8_sizes(int M, int K) { return M < kMaxRows && K % kInt8Chunk == 0 && K <= kInt8MaxRow; }
+
+size_t int8_scales_at(int rows, int K) { return ((size_t)rows * K + 255) / 256 * 256; }  // in the workspace
 
 RowsArg rows_arg(const moe_rows_t& r) { return RowsArg{(uint8_t*)r.data, r.stride, r.rows, r.div, r.ids}; }
 
@@ -136,6 +144,74 @@ moe_status_t moe_swiglu_checkpoint_grad(const uint8_t* codes, const uint8_t* sca
   launch_swiglu_grad(codes, scales, (const uint8_t*)dh, row_weight, R, I, num_rows, (uint8_t*)dgu, (uint8_t*)h,
                      dweight, (hipStream_t)stream);
   return launch_status();
+}
+
+moe_status_t moe_quant_int8(const void* x, int64_t x_stride, int32_t M, int32_t K, int8_t* codes, float* scales,
+                            void* stream) {
+  if (M < 0 || K < 1) return MOE_ERR_INVALID_ARG;
+  if (!int8_sizes(M, K)) return MOE_ERR_UNSUPPORTED;
+  if (M == 0) return MOE_OK;
+  if (!x || !aligned(x, 16) || x_stride < K || x_stride % 8) return MOE_ERR_INVALID_ARG;
+  if (x_stride >= kMaxStride) return MOE_ERR_UNSUPPORTED;
+  if (!codes || !aligned(codes, 16) || !scales || !aligned(scales, 4)) return MOE_ERR_INVALID_ARG;
+  launch_int8_rows<false>(Int8Args{(const uint8_t*)x, x_stride, M, K, nullptr, nullptr, (uint8_t*)codes, scales},
+                          (hipStream_t)stream);
+  return launch_status();
+}
+
+moe_status_t moe_swiglu_int8(const void* gu, int64_t gu_stride, const float* row_weight, int32_t R, int32_t I,
+                             const int32_t* num_rows, int8_t* codes, float* scales, void* stream) {
+  if (R < 0 || I < 1) return MOE_ERR_INVALID_ARG;
+  if (!int8_sizes(R, I)) return MOE_ERR_UNSUPPORTED;
+  if (R == 0) return MOE_OK;
+  if (!gu || !aligned(gu, 16) || gu_stride < 2 * (int64_t)I || gu_stride % 8) return MOE_ERR_INVALID_ARG;
+  if (gu_stride >= kMaxStride) return MOE_ERR_UNSUPPORTED;
+  if (!codes || !aligned(codes, 16) || !scales || !aligned(scales, 4) || !aligned(row_weight, 4) ||
+      !aligned(num_rows, 4))
+    return MOE_ERR_INVALID_ARG;
+  launch_int8_rows<true>(
+      Int8Args{(const uint8_t*)gu, gu_stride, R, I, row_weight, num_rows, (uint8_t*)codes, scales},
+      (hipStream_t)stream);
+  return launch_status();
+}
+
+size_t moe_grouped_int8_workspace_size(int32_t rows, int32_t K) {
+  if (rows < 0 || K < 1 || !int8_sizes(rows, K)) return 0;
+  return int8_scales_at(rows, K) + (size_t)rows * 4;
+}
+
+moe_status_t moe_grouped_gemm_int8(const moe_grouped_int8_args_t* a, void* stream) {
+  if (!a) return MOE_ERR_INVALID_ARG;
+  const bool quantised = a->in_scale != nullptr;
+  if (a->R < 0 || a->E < 1 || a->N < 1 || a->K < 1 || !known_out(a->out_type)) return MOE_ERR_INVALID_ARG;
+  if (a->R >= kMaxRows || a->E > kMaxExperts || a->N % 8 || a->K % kInt8Chunk || a->K >= kMaxInt8Sum ||
+      (int64_t)a->N * a->K >= kMaxExpertBytes || a->in.rows >= kMaxRows || (!quantised && a->K > kInt8MaxRow))
+    return MOE_ERR_UNSUPPORTED;
+  if (a->R == 0) return MOE_OK;
+  if (!a->offsets || !aligned(a->offsets, 4) || !a->w || !aligned(a->w, 16) || !a->w_scale ||
+      !aligned(a->w_scale, 16) || !aligned(a->in_scale, 4))
+    return MOE_ERR_INVALID_ARG;
+  const bool f32 = a->out_type == MOE_OUT_FP32;
+  moe_status_t rc;
+  if ((rc = check_rows(a->in, a->R, a->K, quantised ? 1 : 2, true)) != MOE_OK) return rc;
+  if ((rc = check_rows(a->out, a->R, a->N, f32 ? 4 : 2, false)) != MOE_OK) return rc;
+  const hipStream_t st = (hipStream_t)stream;
+  GroupedInt8Args g{a->R,          a->E, a->N, a->K, a->offsets, rows_arg(a->in), rows_arg(a->out), a->in_scale,
+                    (const uint8_t*)a->w, a->w_scale};
+  if (!quantised) {
+    if (!a->workspace || !aligned(a->workspace, 256)) return MOE_ERR_INVALID_ARG;
+    if (a->workspace_bytes < moe_grouped_int8_workspace_size(a->in.rows, a->K)) return MOE_ERR_WORKSPACE_TOO_SMALL;
+    uint8_t* const codes = (uint8_t*)a->workspace;
+    float* const scales = (float*)(codes + int8_scales_at(a->in.rows, a->K));
+    if (a->in.rows > 0)
+      launch_int8_rows<false>(Int8Args{g.in.p, a->in.stride, a->in.rows, a->K, nullptr, nullptr, codes, scales}, st);
+    g.in.p = codes;
+    g.in.stride = a->K;
+    g.in_scale = scales;
+  }
+  const bool ok = launch_grouped_int8(f32, st, g);
+  const moe_status_t launched = launch_status();
+  return ok ? launched : MOE_ERR_DEVICE;
 }
 
 }  // extern "C"

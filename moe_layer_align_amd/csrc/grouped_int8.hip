@@ -1,0 +1,237 @@
+// Grouped expert products of 8-bit integers for the few rows per expert of
+// decoding: bound by the stream of the weights.
+//
+// As in the 4-bit products a workgroup multiplies a band of one expert's weight
+// rows by that expert's rows, 16 or 32 of them per pass, and each wave streams
+// its own part of the band through a private pair of LDS stages by direct-to-LDS
+// loads of whole lines.  A step is 128 of K, 128 bytes of a weight row: lane l
+// holds bytes 64 i + 16 (l/16) .. + 15 (i = 0, 1) of weight row l%16, and the
+// same of the rows' codes, so that 16x16x64 MFMAs multiply them as they lie.
+// The weights are the B operand: a lane's four results are four rows' sums for
+// one weight row.  Sums are exact in int32; the scales join once, at the end.
+//
+// WK waves split K, step by step, and the others the band; partial sums meet in
+// LDS.
+#include <type_traits>
+
+#include "grouped_stream.h"
+
+namespace moe {
+namespace {
+
+constexpr int kStep = 128;  // K per step
+
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) int lds_i32;
+typedef __attribute__((address_space(3))) i32x4 lds_i32x4;
+
+__device__ __forceinline__ i32x4 mfma_i8(u32x4 a, u32x4 b, i32x4 c) {
+  return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, a), __builtin_bit_cast(i32x4, b), c, 0, 0, 0);
+}
+
+// Grouped rows [i0, i0 + 16 NT) of expert e, of which those below hi are
+// written.
+template <bool F32, int WK, int FT, int NT>
+__device__ __forceinline__ void pass(const GroupedInt8Args& a, int e, int n0, int i0, int hi, lds_u8* smem) {
+  constexpr int kBand = 16 * FT * (4 / WK);  // weight rows of the workgroup
+  constexpr int kLd = kBand + 4;              // row stride of the partial sums
+  constexpr int kStage = stage_bytes(FT);
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wk = wave % WK, wb = wave / WK;
+  const int r16 = lane & 15, q = lane >> 4;
+  const int nstep = (a.K + kStep - 1) / kStep;
+  const unsigned wrow = (unsigned)a.K;
+  const __amdgpu_buffer_rsrc_t rw = buffer(a.w + (int64_t)e * a.N * wrow, (unsigned)a.N * wrow);
+  const __amdgpu_buffer_rsrc_t rx = buffer(a.in.ids ? a.in.p : a.in.p + (int64_t)i0 * a.in.stride, kOob);
+  lds_u8* const stage = smem + wave * (2 * kStage);
+  const int nb = n0 + 16 * FT * wb;  // the wave's first weight row
+
+  // weights: load d of a step takes rows nb + 8d + lane/8, lane l the 16-byte
+  // chunk (l%8) ^ pf_mix(row) of their 128 bytes; rows at or past N lie past
+  // the buffer, chunks past K take kOob
+  const int wchunk = (lane & 7) ^ (lane >> 3);
+  const unsigned w0 = (unsigned)(nb + (lane >> 3)) * wrow + (wchunk << 4);
+  const unsigned w1 = (unsigned)(nb + (lane >> 3)) * wrow + ((wchunk ^ 1) << 4);
+  auto load_w = [&](int c, int b) {
+    const int left = a.K - c * kStep;  // bytes of a row from this step on
+    const bool ok0 = (wchunk << 4) < left, ok1 = ((wchunk ^ 1) << 4) < left;
+#pragma unroll
+    for (int d = 0; d < 2 * FT; ++d)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(
+          rw, (void __attribute__((address_space(3)))*)(stage + b * kStage + d * 1024), 16,
+          (int)((d & 1 ? ok1 : ok0) ? (d & 1 ? w1 : w0) + (unsigned)(8 * d) * wrow + c * kStep : kOob), 0, 0, 0);
+  };
+  unsigned x0[NT];
+  struct Step {
+    u32x4 x[NT][2];
+  };
+  auto load_x = [&](Step& g, int c) {
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        g.x[t][i] = load16(rx, c * kStep + 64 * i + 16 * q < a.K ? x0[t] + c * kStep + 64 * i : kOob);
+  };
+  i32x4 acc[FT][NT] = {};
+  // Fragments of a stage: tile f's row at f * 2048, chunk 4 i + q.
+  const unsigned frag = (unsigned)(uintptr_t)stage + r16 * 128;
+  const unsigned frag0 = frag + ((q ^ pf_mix(r16)) << 4), frag1 = frag + (((4 + q) ^ pf_mix(r16)) << 4);
+
+  // One step: its loads have landed when at most those of the next step are
+  // outstanding (they are issued in this order and kept in it by the fences).
+  constexpr int kLater = 2 * FT + 2 * NT;  // loads of a step
+  static_assert(kLater < 64, "vmcnt range");
+  auto fence = [] {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  Step g0, g1;
+  auto step = [&](Step& g, int c, int b, auto later, auto more) {
+    fence();
+    wait_vm<later()>();
+    fence();
+    u32x4 w[FT][2];
+    read_stage<FT>(w, frag0 + b * kStage, frag1 + b * kStage);  // the stage is read: load it again
+    fence();
+    if constexpr (more()) load_w(c + 2 * WK, b);
+    fence();
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int f = 0; f < FT; ++f)
+#pragma unroll
+        for (int t = 0; t < NT; ++t) acc[f][t] = mfma_i8(g.x[t][i], w[f][i], acc[f][t]);
+    fence();
+    if constexpr (more()) load_x(g, c + 2 * WK);
+    fence();
+  };
+  constexpr std::integral_constant<int, kLater> next_in_flight{};
+  constexpr std::integral_constant<int, 0> none_in_flight{};
+  // The rows' ids first: loads return in order, and what follows from them
+  // would wait for weights loaded ahead of them.
+  constexpr int kPer = F32 ? 4 : 8;  // results per thread and store
+  constexpr int kCols = kBand / kPer;
+  constexpr int kStores = (16 * NT * kCols + 255) / 256;  // of the first threads
+  const int last = hi - 1;
+  int in_id[NT], from_id[kStores], out_id[kStores];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) in_id[t] = a.in.ids ? a.in.ids[min(i0 + 16 * t + r16, last)] : 0;
+#pragma unroll
+  for (int u = 0; u < kStores; ++u) {
+    const int i = min(i0 + (u * 256 + tid) / kCols, last);
+    from_id[u] = a.in.ids ? a.in.ids[i] : 0;
+    out_id[u] = a.out.ids ? a.out.ids[i] : 0;
+  }
+  fence();
+  load_w(wk, 0);
+  fence();
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    const int i = i0 + 16 * t + r16;
+    const int m = i < hi ? (a.in.ids ? row_of(a.in, i, in_id[t]) : i - i0) : -1;
+    x0[t] = m >= 0 ? (unsigned)m * (unsigned)a.in.stride + 16 * q : kOob;
+  }
+  load_x(g0, wk);
+  fence();
+  // the scales of the thread's results
+  float sa[kStores];
+  f32x4 sw[kStores][kPer / 4];
+#pragma unroll
+  for (int u = 0; u < kStores; ++u) {
+    const int at_u = u * 256 + tid, i = min(i0 + at_u / kCols, last), n = min(n0 + (at_u % kCols) * kPer, a.N - kPer);
+    const int m = row_of(a.in, i, from_id[u]);
+    sa[u] = m < 0 ? 0.0f : a.in_scale[m];
+#pragma unroll
+    for (int h = 0; h < kPer / 4; ++h) sw[u][h] = *(const f32x4*)(a.w_scale + (int64_t)e * a.N + n + 4 * h);
+  }
+  fence();
+  load_w(wk + WK, 1);
+  fence();
+  load_x(g1, wk + WK);
+  int c = wk;
+  for (; c + 2 * WK < nstep; c += 2 * WK) {  // loads past the last step read nothing
+    step(g0, c, 0, next_in_flight, std::true_type{});
+    step(g1, c + WK, 1, next_in_flight, std::true_type{});
+  }
+  if (c < nstep) step(g0, c, 0, next_in_flight, std::false_type{});
+  if (c + WK < nstep) step(g1, c + WK, 1, none_in_flight, std::false_type{});
+  fence();
+  wait_vm<0>();  // loads past the last step still write LDS
+  lds_i32* const red = (lds_i32*)smem;
+  // partial sums: [wk][row][weight row], over the stages
+  __syncthreads();
+#pragma unroll
+  for (int f = 0; f < FT; ++f)
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int v = 0; v < 4; ++v)
+        red[(wk * 16 * NT + 16 * t + 4 * q + v) * kLd + 16 * (FT * wb + f) + r16] = acc[f][t][v];
+  __syncthreads();
+#pragma unroll
+  for (int u = 0; u < kStores; ++u) {
+    const int at_u = u * 256 + tid, row = at_u / kCols, col = (at_u % kCols) * kPer, i = i0 + row;
+    if (row >= 16 * NT || i >= hi || n0 + col >= a.N) continue;
+    const int m = row_of(a.out, i, out_id[u]);
+    if (m < 0) continue;
+    f32x4 v[kPer / 4];
+#pragma unroll
+    for (int h = 0; h < kPer / 4; ++h) {
+      i32x4 s = *(const lds_i32x4*)(red + row * kLd + col + 4 * h);
+#pragma unroll
+      for (int k = 1; k < WK; ++k) s += *(const lds_i32x4*)(red + (k * 16 * NT + row) * kLd + col + 4 * h);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[h][j] = (float)s[j] * sa[u] * sw[u][h][j];
+    }
+    const int64_t at = (int64_t)m * a.out.stride + n0 + col;
+    if constexpr (F32)
+      *(f32x4*)(a.out.p + at * 4) = v[0];
+    else
+      *(u32x4*)(a.out.p + at * 2) = u32x4{pack_bf16x2(v[0][0], v[0][1]), pack_bf16x2(v[0][2], v[0][3]),
+                                          pack_bf16x2(v[1][0], v[1][1]), pack_bf16x2(v[1][2], v[1][3])};
+  }
+  __syncthreads();  // the next pass loads over the partial sums
+}
+
+template <bool F32, int WK, int FT, int NT>
+__global__ __launch_bounds__(256, 2) void grouped_int8_kernel(GroupedInt8Args a) {
+  constexpr int kBand = 16 * FT * (4 / WK);
+  constexpr int kSums = WK * 16 * NT * (kBand + 4) * 4, kStages = 8 * stage_bytes(FT);
+  __shared__ __align__(16) uint8_t smem[kStages];
+  static_assert(kSums <= kStages, "the partial sums fit the stages");
+  const Found f = find_expert(a.offsets, a.R, a.E);
+  if (f.e >= a.E) return;
+  for (int i0 = f.lo; i0 < f.hi; i0 += 16 * NT)
+    pass<F32, WK, FT, NT>(a, f.e, blockIdx.x * kBand, i0, f.hi, (lds_u8*)smem);
+}
+
+template <bool F32, int WK, int FT, int NT>
+void launch(hipStream_t st, const GroupedInt8Args& a) {
+  constexpr int kBand = 16 * FT * (4 / WK);
+  grouped_int8_kernel<F32, WK, FT, NT><<<dim3((a.N + kBand - 1) / kBand, a.R < a.E ? a.R : a.E), 256, 0, st>>>(a);
+}
+
+template <bool F32, int NT>
+void pick(hipStream_t st, const GroupedInt8Args& a) {
+  const int steps = (a.K + kStep - 1) / kStep;
+  const int64_t rows = (int64_t)(a.R < a.E ? a.R : a.E) * a.N;  // weight rows that may be read
+  if (rows < 256 * 64)
+    launch<F32, 4, 2, NT>(st, a);
+  else if (steps >= 8)
+    launch<F32, 4, 4, NT>(st, a);
+  else
+    launch<F32, 2, 4, NT>(st, a);
+}
+
+}  // namespace
+
+bool launch_grouped_int8(bool f32, hipStream_t st, const GroupedInt8Args& a) {
+  if (a.R > 16 * (int64_t)a.E) return launch_grouped_tile_int8(f32, st, a);
+  if (a.R <= 8 * (int64_t)a.E)
+    f32 ? pick<true, 1>(st, a) : pick<false, 1>(st, a);
+  else
+    f32 ? pick<true, 2>(st, a) : pick<false, 2>(st, a);
+  return true;
+}
+
+}  // namespace moe

@@ -63,6 +63,7 @@ namespace {
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) u32x4 lds_u32x4;
 typedef __attribute__((address_space(3))) u32x2 lds_u32x2;
+typedef __attribute__((address_space(3))) float lds_f32;
 typedef __attribute__((address_space(3))) f32x4 lds_f32x4;
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 typedef __attribute__((address_space(4))) int32_t c_int32;  // read by scalar loads
@@ -80,7 +81,14 @@ constexpr int lds_bytes(int op) {
   return op == 2 ? kRing + 8 * epilogue_bytes(2) : kTable + 2 * kMaxExperts * 4 + 64;
 }
 constexpr int kSlots = 32;              // most workgroups per XCD: one per CU
-static_assert(lds_bytes(0) <= 160 * 1024 && lds_bytes(2) <= 160 * 1024, "LDS of one gfx950 CU");
+// 8-bit integers: scales of a tile's 256 weight rows and 256 grouped rows.  The
+// loads' tile is at most two ahead of the one that is multiplied (tiles have at
+// least two steps), so three tiles' scales are held.
+constexpr int kScales = lds_bytes(0);
+constexpr int kScaleBytes = 2 * kTile * 4;
+constexpr int kLdsInt8 = kScales + 3 * kScaleBytes;
+static_assert(kLdsInt8 <= 160 * 1024 && lds_bytes(2) <= 160 * 1024, "LDS of one gfx950 CU");
+static_assert(kScales % 16 == 0, "scales are read 16 bytes at a time");
 // offset of a lane that loads nothing: past every buffer (their sizes are at
 // most this), and far enough below 2^32 that an in-row offset added to it does
 // not wrap
@@ -95,6 +103,9 @@ struct TileArgs {
   const uint8_t* w;  // OP 0, 1
   RowsArg out;       // OP 0, 1
   uint8_t* dw;       // OP 2
+  // 8-bit integers (OP 0): K and q's stride count pairs of them
+  const float* q_scale;  // by q's matrix row
+  const float* p_scale;  // [E,N]
 };
 
 // One tile: expert e with rows [lo, hi), first q (a grouped row, or n) and
@@ -126,6 +137,26 @@ constexpr bool kCountLoads = true;
 #else  // an unoptimised build does not hold uniform values in scalar registers, which the instruction takes
 constexpr bool kCountLoads = false;
 #endif
+
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x16 __attribute__((ext_vector_type(16)));
+
+// 32x32x32 signed 8-bit integers -> int32.  A: lane l holds 16 bytes of row l%32
+// at k = 16*(l/32); B: the same k of column l%32.  C as for mfma32_bf16, and the
+// same bytes per lane and cycles: a step of 128 bytes takes as long as in bf16.
+__device__ __forceinline__ i32x16 mfma32(u32x4 a, u32x4 b, i32x16 c) {
+  return __builtin_amdgcn_mfma_i32_32x32x32_i8(__builtin_bit_cast(i32x4, a), __builtin_bit_cast(i32x4, b), c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x16 mfma32(u32x4 a, u32x4 b, f32x16 c) { return mfma32_bf16(a, b, c); }
+
+// Four of a lane's results, rows p..p+3 of one q: 8-bit integers take their scales.
+__device__ __forceinline__ f32x4 results(const f32x16& c, int g, float, f32x4) {
+  return f32x4{c[4 * g], c[4 * g + 1], c[4 * g + 2], c[4 * g + 3]};
+}
+__device__ __forceinline__ f32x4 results(const i32x16& c, int g, float q, f32x4 p) {
+  return f32x4{(float)c[4 * g] * q * p[0], (float)c[4 * g + 1] * q * p[1], (float)c[4 * g + 2] * q * p[2],
+               (float)c[4 * g + 3] * q * p[3]};
+}
 
 // 16 bytes per lane from base + off (zeros past `bytes`) to dst + 16 * lane.
 // The compiler makes a transpose read from LDS wait for every tracked load into
@@ -414,9 +445,27 @@ __device__ __forceinline__ uint8_t* out_row(const TileArgs& a, const Tile& t, in
   }
 }
 
+// The scales of a tile of 8-bit integers to LDS: those of its 256 weight rows by
+// waves 0 to 3, of its grouped rows by the others (zeros for what is not there).
+__device__ __forceinline__ void load_scales(const TileArgs& a, const Tile& t, lds_u8* dst, int wave) {
+  const int i = 64 * (wave & 3) + lane_now();
+  const float* base = a.q_scale;
+  unsigned off = kOob;
+  if (wave < 4) {
+    base = a.p_scale + (int64_t)t.e * a.N;
+    if (t.p0 + i < a.N) off = (unsigned)(t.p0 + i) * 4;
+  } else if (t.q0 + i < t.hi) {
+    const int m = row_of(a.q, t.q0 + i);
+    if (m >= 0) off = (unsigned)m * 4;
+  }
+  const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc((void*)base, (short)0, (int)kOob, kBufferWord3);
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (void __attribute__((address_space(3)))*)(dst + wave * 256), 4, (int)off,
+                                           0, 0, 0);
+}
+
 // All tiles of one kind (HALF: at most 128 q) of a workgroup: items(u, &tile)
 // moves u to the next item from u on, or returns false.
-template <int OP, bool F32, bool ACC, bool HALF, bool IDS, typename Items>
+template <int OP, bool F32, bool ACC, bool HALF, bool IDS, bool I8, typename Items>
 __device__ __forceinline__ void run_tiles(const TileArgs& a, lds_u8* smem, int& u, const Items& items) {
   constexpr bool kTransP = OP != 0, kTransQ = OP == 2;
   constexpr int kReadsP = kTransP ? 16 : 8, kReadsQ = kTransQ ? 8 : 4;  // LDS reads of a half
@@ -429,11 +478,17 @@ __device__ __forceinline__ void run_tiles(const TileArgs& a, lds_u8* smem, int& 
   Tile lt = t;  // the loads' tile
   int lu = u;
   L.init(a, wave, lane);
+  int lscale = 0, scale = 0;  // the loads' and the results' scales, offsets from kScales
   auto load_tile = [&](bool have) {
-    if (have)
+    if (have) {
       L.tile(a, lt, wave);
-    else
+      if constexpr (I8) {
+        load_scales(a, lt, smem + kScales + lscale, wave);
+        lscale = lscale == 2 * kScaleBytes ? 0 : lscale + kScaleBytes;
+      }
+    } else {
       L.end();
+    }
   };
   // After a step: to the next tile where it was the last.  L.step itself is
   // scheduled among the MFMAs; past the last step it changes nothing that the
@@ -478,7 +533,8 @@ __device__ __forceinline__ void run_tiles(const TileArgs& a, lds_u8* smem, int& 
       f[kk] = kTransQ ? tr_frag(s + (qa ^ o) + kk * 4096) : *(const lds_u32x4*)(s + (qa ^ (32 * kk)));
   };
 
-  f32x16 acc[2][HALF ? 1 : 2][2];  // [P half][Q half][tile]
+  typedef std::conditional_t<I8, i32x16, f32x16> Acc;
+  Acc acc[2][HALF ? 1 : 2][2];  // [P half][Q half][tile]
   auto clear = [&] {
 #pragma unroll
     for (int i = 0; i < 2; ++i)
@@ -487,14 +543,14 @@ __device__ __forceinline__ void run_tiles(const TileArgs& a, lds_u8* smem, int& 
 #pragma unroll
         for (int k = 0; k < 2; ++k)
 #pragma unroll
-          for (int v = 0; v < 16; ++v) acc[i][j][k][v] = 0.0f;
+          for (int v = 0; v < 16; ++v) acc[i][j][k][v] = 0;
   };
   u32x4 A0[2][4], A1[2][4], F0[4], F1[4];
-  auto mma = [&](f32x16 (&c)[2], const u32x4 (&p)[2][4], const u32x4 (&q)[4]) {
+  auto mma = [&](Acc (&c)[2], const u32x4 (&p)[2][4], const u32x4 (&q)[4]) {
 #pragma unroll
     for (int kk = 0; kk < 4; ++kk)
 #pragma unroll
-      for (int i = 0; i < 2; ++i) c[i] = mfma32_bf16(p[i][kk], q[kk], c[i]);
+      for (int i = 0; i < 2; ++i) c[i] = mfma32(p[i][kk], q[kk], c[i]);
   };
   auto fence = [] { __builtin_amdgcn_sched_barrier(0); };
   // A phase waits until at most the loads of the last six phases (HALF: the
@@ -623,12 +679,16 @@ __device__ __forceinline__ void run_tiles(const TileArgs& a, lds_u8* smem, int& 
         for (int i = 0; i < 2; ++i) {
           if (kQ == 32 || ef / kQ == z) {
             const int x = ef % kQ;
+            float qs = 0.0f;
+            const lds_u8* const sc = smem + kScales + scale;
+            if constexpr (I8) qs = *(const lds_f32*)(sc + (kTile + kHalf * j + 32 * wc + ef) * 4);
 #pragma unroll
             for (int k = 0; k < 2; ++k)
 #pragma unroll
               for (int g = 0; g < 4; ++g) {
-                const f32x16& c = acc[i][j][k];
-                const f32x4 v = {c[4 * g], c[4 * g + 1], c[4 * g + 2], c[4 * g + 3]};
+                f32x4 ps = {};
+                if constexpr (I8) ps = *(const lds_f32x4*)(sc + (kHalf * i + 64 * wr + 32 * k + 8 * g + 4 * eh) * 4);
+                const f32x4 v = results(acc[i][j][k], g, qs, ps);
                 if constexpr (F32)
                   *(lds_f32x4*)(ep + x * kRowB + (((8 * k + 2 * g + eh) ^ (x & kX)) << 4)) = v;
                 else
@@ -653,6 +713,7 @@ __device__ __forceinline__ void run_tiles(const TileArgs& a, lds_u8* smem, int& 
           }
           wave_exchange();
         }
+    if constexpr (I8) scale = scale == 2 * kScaleBytes ? 0 : scale + kScaleBytes;
     u += slots();
     if (!items(u, &t)) break;
   }
@@ -666,7 +727,7 @@ constexpr int kSmallStages = 5;
 constexpr int kSmallStage = kPiece + kSmallQ * kC * 2;
 static_assert(kSmallStages * kSmallStage <= kRing, "the small tiles' ring");
 
-template <int OP, bool F32, typename Items>
+template <int OP, bool F32, bool I8, typename Items>
 __device__ __forceinline__ void run_small(const TileArgs& a, lds_u8* smem, int& u, const Items& items) {
   constexpr bool kTransP = OP != 0;
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
@@ -689,9 +750,9 @@ __device__ __forceinline__ void run_small(const TileArgs& a, lds_u8* smem, int& 
                          qc << 3 < len - kC * L.s ? qoff + (unsigned)(L.s * (kC * 2)) : kOob);
       L.step(wave);
     };
-    f32x16 acc;
+    std::conditional_t<I8, i32x16, f32x16> acc;
 #pragma unroll
-    for (int v = 0; v < 16; ++v) acc[v] = 0.0f;
+    for (int v = 0; v < 16; ++v) acc[v] = 0;
     for (int i = 0; i < kSmallStages - 1; ++i) issue(i);
     int stage = 0;
     for (int s = 0; s < nk; ++s) {
@@ -706,16 +767,24 @@ __device__ __forceinline__ void run_small(const TileArgs& a, lds_u8* smem, int& 
       issue(stage == 0 ? kSmallStages - 1 : stage - 1);  // the slot whose reads the barrier ended
       stage = stage == kSmallStages - 1 ? 0 : stage + 1;
 #pragma unroll
-      for (int kk = 0; kk < 4; ++kk) acc = mfma32_bf16(p[kk], q[kk], acc);
+      for (int kk = 0; kk < 4; ++kk) acc = mfma32(p[kk], q[kk], acc);
     }
     phase_begin<0>();  // the loads past the last step (zeros)
-    uint8_t* o = out_row<OP, F32>(a, t, 32 * wq + (lane & 31));
+    const int i = 32 * wq + (lane & 31);
+    uint8_t* o = out_row<OP, F32>(a, t, i);
+    float qs = 0.0f;
+    if constexpr (I8) {
+      const int m = t.q0 + i < t.hi ? row_of(a.q, t.q0 + i) : -1;
+      if (m >= 0) qs = a.q_scale[m];
+    }
     if (o)
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
         const int p = t.p0 + 32 * wp + 8 * g + 4 * (lane >> 5);
         if (p >= width) continue;
-        const f32x4 v = {acc[4 * g], acc[4 * g + 1], acc[4 * g + 2], acc[4 * g + 3]};
+        f32x4 ps = {};
+        if constexpr (I8) ps = *(const f32x4*)(a.p_scale + (int64_t)t.e * a.N + p);
+        const f32x4 v = results(acc, g, qs, ps);
         if constexpr (F32)
           *(f32x4*)(o + (int64_t)p * 4) = v;
         else
@@ -746,7 +815,7 @@ __device__ __forceinline__ int expert_of(const lds_int* tab, int E, int shift, i
 // kind on its own; an XCD takes an eighth of a kind's tiles, whole ones and
 // halves in groups of four row tiles with p tiles outer, so that the ~32
 // workgroups that run together on an XCD share operands in its L2.
-template <int OP, bool F32>
+template <int OP, bool F32, bool I8>
 __global__ __launch_bounds__(kThreads) void grouped_rows_kernel(TileArgs a) {
   extern __shared__ __align__(16) uint8_t smem_raw[];
   lds_u8* smem = (lds_u8*)smem_raw;
@@ -824,11 +893,11 @@ __global__ __launch_bounds__(kThreads) void grouped_rows_kernel(TileArgs a) {
     return true;
   };
   int u = blockIdx.x >> 3;
-  run_tiles<OP, F32, false, false, true>(a, smem, u, whole);
+  run_tiles<OP, F32, false, false, true, I8>(a, smem, u, whole);
   while (u < nf) u += slots();  // an XCD's last items can be missing
-  run_tiles<OP, F32, false, true, true>(a, smem, u, half);
+  run_tiles<OP, F32, false, true, true, I8>(a, smem, u, half);
   while (u < nf + nh) u += slots();
-  run_small<OP, F32>(a, smem, u, small);
+  run_small<OP, F32, I8>(a, smem, u, small);
 }
 
 // Weight gradient: the tiles of an expert are split over the XCDs (experts
@@ -877,9 +946,9 @@ __global__ __launch_bounds__(kThreads) void grouped_wgrad_kernel(TileArgs a) {
     return false;
   };
   int u = blockIdx.x >> 3;
-  run_tiles<2, F32, ACC, false, IDS>(a, smem, u, whole);
+  run_tiles<2, F32, ACC, false, IDS, false>(a, smem, u, whole);
   while (u < nf) u += slots();
-  run_tiles<2, F32, ACC, true, IDS>(a, smem, u, half);
+  run_tiles<2, F32, ACC, true, IDS, false>(a, smem, u, half);
   // experts without rows: zeros, or nothing to add
   if constexpr (!ACC) {
     const int64_t bytes = (int64_t)a.N * a.K * (F32 ? 4 : 2);
@@ -1013,10 +1082,10 @@ bool launch(Kernel kernel, int lds, std::atomic<bool> (&lds_set)[64], dim3 grid,
   return true;
 }
 
-template <int OP, bool F32>
+template <int OP, bool F32, bool I8 = false>
 bool launch_rows(int64_t grid, hipStream_t st, const TileArgs& a) {
   static std::atomic<bool> lds_set[64];
-  return launch(grouped_rows_kernel<OP, F32>, lds_bytes(OP), lds_set, dim3((unsigned)grid), st, a);
+  return launch(grouped_rows_kernel<OP, F32, I8>, I8 ? kLdsInt8 : lds_bytes(OP), lds_set, dim3((unsigned)grid), st, a);
 }
 
 template <bool F32>
@@ -1070,6 +1139,24 @@ bool launch_grouped_tile(bool dgrad, bool f32, hipStream_t st, const GroupedArgs
   const int64_t grid = persistent_grid(rows * cdiv(dgrad ? a.K : a.N, kHalf));
   if (dgrad) return f32 ? launch_rows<1, true>(grid, st, t) : launch_rows<1, false>(grid, st, t);
   return f32 ? launch_rows<0, true>(grid, st, t) : launch_rows<0, false>(grid, st, t);
+}
+
+bool launch_grouped_tile_int8(bool f32, hipStream_t st, const GroupedInt8Args& a) {
+  TileArgs t = {};
+  t.R = a.R;
+  t.E = a.E;
+  t.N = a.N;
+  t.K = a.K / 2;
+  t.offsets = a.offsets;
+  t.q = a.in;
+  t.q.stride = a.in.stride / 2;
+  t.w = a.w;
+  t.out = a.out;
+  t.q_scale = a.in_scale;
+  t.p_scale = a.w_scale;
+  const int experts = a.R < a.E ? a.R : a.E;
+  const int64_t grid = persistent_grid((a.R / kTile + experts) * cdiv(a.N, kHalf));
+  return f32 ? launch_rows<0, true, true>(grid, st, t) : launch_rows<0, false, true>(grid, st, t);
 }
 
 bool launch_grouped_wgrad(bool f32, bool accumulate, hipStream_t st, const GroupedWgradArgs& a) {

@@ -1,0 +1,596 @@
+// The tokens' way to their experts and back, with the gradients (include/moe.h):
+// the copy of the hidden states to rows grouped by expert, the weighted sum of a
+// token's rows, the gradient of that sum, and the gradient of the top-k softmax.
+//
+// All of it is bound by memory: a few operations per element, and what is read
+// and written once sets the floor.
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+#include "grouped.h"
+#include "moe.h"
+
+using namespace moe;
+
+namespace {
+
+constexpr int kThreads = 256;
+
+// ---------------------------------------------------------------- dispatch
+// A counting sort of the pairs by expert, stable in the pair index, and the copy
+// of the tokens' rows to where it puts them, in one kernel: workgroup x owns
+// `group` tokens, finds their pairs' rows and copies each token's row, which it
+// reads once for all its pairs (a copy that runs over the sorted rows would read
+// it again for every pair).
+//
+// How many pairs of each expert there are, and how many before a workgroup's
+// own, comes by the number of pairs from
+//   kCountAll   a count of all ids by every workgroup itself: one launch, for
+//               decoding, where it takes less than a second launch would
+//   kSumChunks  the counts of chunks of kChunk pairs, made by a launch before
+//               this one: every workgroup adds up those of all chunks
+//   kScanned    the same, added up by a launch between the two
+// and in the latter two a count of the ids of its own chunk before its first.
+enum Counts { kCountAll, kSumChunks, kScanned };
+
+constexpr int kChunk = 1024;           // pairs per chunk of the counts
+constexpr int kOwn = 64;               // pairs of a workgroup at most: one wave ranks them
+constexpr int kCountAllPairs = 4096;   // at most so many pairs are counted by every workgroup
+constexpr int kSumChunksCounts = 8192; // at most so many counts are added up by every workgroup
+
+struct DispatchArgs {
+  const uint8_t* x;
+  int64_t x_stride;    // bytes
+  const int32_t* ids;  // [M*k]
+  int M, k, E, first, group;
+  int row_bytes;       // multiple of 16
+  uint8_t* rows;
+  int64_t rows_stride;  // bytes
+  int32_t* offsets;     // [E+1]
+  int32_t* positions;   // [M*k]
+  int32_t* pairs;       // [M*k]
+  int32_t* counts;      // [chunks][E] counts, or (scanned) those of the chunks before, and [E] the totals behind them
+  int chunks;
+};
+
+__device__ __forceinline__ bool local_expert(int id, int first, int E, int* e) {
+  *e = (int)((unsigned)id - (unsigned)first);  // ids below `first` wrap past E
+  return (unsigned)*e < (unsigned)E;
+}
+
+__global__ __launch_bounds__(kThreads) void count_chunks_kernel(const int32_t* __restrict__ ids, int P, int E,
+                                                                int first, int32_t* __restrict__ counts) {
+  __shared__ int count[kMaxExperts];
+  for (int e = threadIdx.x; e < E; e += kThreads) count[e] = 0;
+  __syncthreads();
+  const int f0 = blockIdx.x * kChunk + threadIdx.x;
+  int id[kChunk / kThreads];
+#pragma unroll
+  for (int i = 0; i < kChunk / kThreads; ++i) id[i] = f0 + i * kThreads < P ? ids[f0 + i * kThreads] : 0;
+#pragma unroll
+  for (int i = 0; i < kChunk / kThreads; ++i) {
+    int e;
+    if (f0 + i * kThreads < P && local_expert(id[i], first, E, &e)) atomicAdd(&count[e], 1);
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < E; e += kThreads) counts[(int64_t)blockIdx.x * E + e] = count[e];
+}
+
+// Each expert's counts become sums over the chunks before, a lane per expert
+// (whole lines of experts at a step); the totals go behind the last chunk.
+// The 16 waves of a workgroup split the chunks: their sums first, then the
+// running sums from them on.
+__global__ __launch_bounds__(1024) void scan_chunks_kernel(int32_t* __restrict__ counts, int chunks, int E) {
+  __shared__ int sum[16][kWave];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int e = blockIdx.x * kWave + lane;
+  const int per = (chunks + 15) / 16, c0 = min(wave * per, chunks), c1 = min(c0 + per, chunks);
+  constexpr int kBatch = 8;  // loads in flight
+  int n[kBatch], s = 0;
+  auto load = [&](int c) {
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) n[i] = e < E && c + i < c1 ? counts[(int64_t)(c + i) * E + e] : 0;
+  };
+  for (int c = c0; c < c1; c += kBatch) {
+    load(c);
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) s += n[i];
+  }
+  sum[wave][lane] = s;
+  __syncthreads();
+  int run = 0, total = 0;
+  for (int w = 0; w < 16; ++w) {
+    run += w < wave ? sum[w][lane] : 0;
+    total += sum[w][lane];
+  }
+  if (e >= E) return;
+  for (int c = c0; c < c1; c += kBatch) {
+    load(c);
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      if (c + i < c1) counts[(int64_t)(c + i) * E + e] = run;
+      run += n[i];
+    }
+  }
+  if (wave == 0) counts[(int64_t)chunks * E + e] = total;
+}
+
+template <int COUNTS>
+__global__ __launch_bounds__(kThreads) void dispatch_kernel(DispatchArgs a) {
+  __shared__ int total[kMaxExperts];   // pairs of each expert
+  __shared__ int before[kMaxExperts];  // those ahead of the workgroup's own, then the expert's first free row
+  __shared__ int wave_sum_[4];
+  __shared__ int place[kOwn];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int P = a.M * a.k;
+  const int t0 = blockIdx.x * a.group, t1 = min(t0 + a.group, a.M);
+  const int f0 = t0 * a.k, f1 = t1 * a.k;  // the workgroup's own pairs
+  const int chunk = f0 / kChunk;
+  for (int e = tid; e < a.E; e += kThreads) {
+    int n = 0, b = 0;
+    if constexpr (COUNTS == kSumChunks)
+      for (int c = 0; c < a.chunks; ++c) {
+        const int v = a.counts[c * a.E + e];
+        n += v;
+        b += c < chunk ? v : 0;
+      }
+    if constexpr (COUNTS == kScanned) {
+      n = a.counts[(int64_t)a.chunks * a.E + e];
+      b = a.counts[(int64_t)chunk * a.E + e];
+    }
+    total[e] = n;
+    before[e] = b;
+  }
+  __syncthreads();
+  constexpr int kBatch = 8;  // loads in flight
+  const int c0 = COUNTS == kCountAll ? 0 : chunk * kChunk, c1 = COUNTS == kCountAll ? P : f0;
+  for (int f = c0 + tid; f < c1; f += kBatch * kThreads) {
+    int id[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) id[i] = f + i * kThreads < c1 ? a.ids[f + i * kThreads] : 0;
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      int e;
+      if (f + i * kThreads >= c1 || !local_expert(id[i], a.first, a.E, &e)) continue;
+      if constexpr (COUNTS == kCountAll) atomicAdd(&total[e], 1);
+      if (COUNTS != kCountAll || f + i * kThreads < f0) atomicAdd(&before[e], 1);
+    }
+  }
+  __syncthreads();
+  // the experts' first rows: a scan of two experts a thread
+  {
+    const int e = 2 * tid;
+    const int n0 = e < a.E ? total[e] : 0, n1 = e + 1 < a.E ? total[e + 1] : 0;
+    const int incl = wave_incl_scan(n0 + n1);
+    if (lane == 63) wave_sum_[wave] = incl;
+    __syncthreads();
+    int start = incl - n0 - n1;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) start += w < wave ? wave_sum_[w] : 0;
+    if (e < a.E) before[e] += start;
+    if (e + 1 < a.E) before[e + 1] += start + n0;
+    if (blockIdx.x == 0 && blockIdx.y == 0) {
+      if (e < a.E) a.offsets[e] = start;
+      if (e + 1 < a.E) a.offsets[e + 1] = start + n0;
+      if (tid == 0) a.offsets[a.E] = wave_sum_[0] + wave_sum_[1] + wave_sum_[2] + wave_sum_[3];
+    }
+  }
+  __syncthreads();
+  const int held = wave_sum_[0] + wave_sum_[1] + wave_sum_[2] + wave_sum_[3];
+  if (wave == 0) {  // a pair's row: its rank among the lanes of the same expert, by a match over the bits of its number
+    const int f = f0 + lane;
+    int e = 0;
+    const bool ok = f < f1 && local_expert(a.ids[f], a.first, a.E, &e);
+    unsigned long long same = __ballot(ok);
+    for (int b = 0; (1 << b) < a.E; ++b) {
+      const bool bit = ok && ((e >> b) & 1);
+      const unsigned long long m = __ballot(bit);
+      same &= bit ? m : ~m;
+    }
+    const int p = ok ? before[e] + __popcll(same & lanemask_lt(lane)) : -1;
+    place[lane] = p;
+    if (blockIdx.y == 0 && f < f1) {
+      a.positions[f] = p;
+      if (ok) a.pairs[p] = f;
+      if (f >= held) a.pairs[f] = -1;  // the rows behind the last expert's
+    }
+  }
+  __syncthreads();
+  // the copy: 16 bytes of a token's row per thread and step, to every place of its
+  const int per_row = a.row_bytes / 16, n = (t1 - t0) * per_row;
+  for (int i = blockIdx.y * kThreads + tid; i < n; i += gridDim.y * kThreads) {
+    const int t = i / per_row, c = i - t * per_row;
+    const u32x4 v = *(const u32x4*)(a.x + (t0 + t) * a.x_stride + c * 16);
+    for (int j = 0; j < a.k; ++j) {
+      const int p = place[t * a.k + j];
+      if (p >= 0) *(u32x4*)(a.rows + p * a.rows_stride + c * 16) = v;
+    }
+  }
+}
+
+// ---------------------------------------------------------------- combine
+template <bool F32>
+__device__ __forceinline__ void load8(const uint8_t* p, float (&v)[8]) {
+  if constexpr (F32) {
+    const f32x4 lo = *(const f32x4*)p, hi = *(const f32x4*)(p + 16);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[i] = lo[i];
+      v[4 + i] = hi[i];
+    }
+  } else {
+    const u32x4 w = *(const u32x4*)p;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = bf16_lo(w[i]);
+      v[2 * i + 1] = bf16_hi(w[i]);
+    }
+  }
+}
+__device__ __forceinline__ void store8(uint8_t* p, bool f32, const float (&v)[8]) {
+  if (f32) {
+    *(f32x4*)p = f32x4{v[0], v[1], v[2], v[3]};
+    *(f32x4*)(p + 16) = f32x4{v[4], v[5], v[6], v[7]};
+  } else {
+    *(u32x4*)p = u32x4{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                       pack_bf16x2(v[6], v[7])};
+  }
+}
+
+struct CombineArgs {
+  const uint8_t* rows;
+  int64_t rows_stride;  // bytes
+  int R;
+  const int32_t* positions;
+  const float* weights;  // null: ones
+  int M, k, H;
+  uint8_t* y;
+  int64_t y_stride;  // bytes
+  int y_f32;
+  int per_wg;  // tokens of a workgroup at a time
+};
+
+// Eight columns of a token per thread.  The loads of up to KB slots are in
+// flight together; the sum runs over the slots in order, in fp32.
+template <bool F32, int KB>
+__global__ __launch_bounds__(kThreads) void combine_kernel(CombineArgs a) {
+  const int cols = a.H / 8;
+  const int of = a.per_wg > 1 ? threadIdx.x / cols : 0;
+  const int col = a.per_wg > 1 ? threadIdx.x - of * cols : blockIdx.y * kThreads + threadIdx.x;
+  if (of >= a.per_wg || col >= cols) return;
+  for (int t = blockIdx.x * a.per_wg + of; t < a.M; t += gridDim.x * a.per_wg) {
+    const int32_t* pos = a.positions + (int64_t)t * a.k;
+    const float* w = a.weights ? a.weights + (int64_t)t * a.k : nullptr;
+    float sum[8] = {};
+    for (int j0 = 0; j0 < a.k; j0 += KB) {
+      float v[KB][8], wj[KB];
+      bool ok[KB];
+#pragma unroll
+      for (int j = 0; j < KB; ++j) {
+        const int p = j0 + j < a.k ? pos[j0 + j] : -1;
+        ok[j] = (unsigned)p < (unsigned)a.R;
+        wj[j] = ok[j] && w ? w[j0 + j] : 1.0f;
+        if (ok[j]) load8<F32>(a.rows + p * a.rows_stride + (int64_t)col * (F32 ? 32 : 16), v[j]);
+      }
+#pragma unroll
+      for (int j = 0; j < KB; ++j)
+        if (ok[j])
+#pragma unroll
+          for (int i = 0; i < 8; ++i) sum[i] += wj[j] * v[j][i];
+    }
+    store8(a.y + t * a.y_stride + (int64_t)col * (a.y_f32 ? 32 : 16), a.y_f32, sum);
+  }
+}
+
+struct CombineGradArgs {
+  const uint8_t* dy;
+  int64_t dy_stride;
+  int dy_f32;
+  const uint8_t* rows;  // null: dweights not wanted
+  int64_t rows_stride;
+  int R;
+  const int32_t* positions;
+  const float* weights;
+  int M, k, H;
+  uint8_t* drows;  // null: not wanted
+  int64_t drows_stride;
+  int drows_f32;
+  float* dweights;
+};
+
+// WPT waves work on one token (so that each of its dweights is one sum in a
+// fixed order), 512 columns per wave and step, whose dy is read once for up to
+// KB slots.
+template <bool F32, int KB, int WPT>
+__global__ __launch_bounds__(kThreads) void combine_grad_kernel(CombineGradArgs a) {
+  constexpr int kTokens = 4 / WPT;  // per workgroup
+  __shared__ float part[4][KB];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wt = wave % WPT;
+  for (int t0 = blockIdx.x * kTokens; t0 < a.M; t0 += gridDim.x * kTokens) {
+    const int t = t0 + wave / WPT;
+    for (int j0 = 0; j0 < a.k; j0 += KB) {
+      int p[KB];
+      float w[KB], dot[KB];
+#pragma unroll
+      for (int j = 0; j < KB; ++j) {
+        const bool in = t < a.M && j0 + j < a.k;
+        p[j] = in ? a.positions[(int64_t)t * a.k + j0 + j] : -1;
+        if ((unsigned)p[j] >= (unsigned)a.R) p[j] = -1;
+        w[j] = in && a.weights ? a.weights[(int64_t)t * a.k + j0 + j] : 1.0f;
+        dot[j] = 0.0f;
+      }
+      if (t < a.M)
+        for (int col = (wt * 64 + lane) * 8; col < a.H; col += WPT * 512) {
+          float d[8];
+          const uint8_t* dp = a.dy + t * a.dy_stride;
+          if (a.dy_f32)
+            load8<true>(dp + (int64_t)col * 4, d);
+          else
+            load8<false>(dp + (int64_t)col * 2, d);
+          float v[KB][8];
+          if (a.rows)
+#pragma unroll
+            for (int j = 0; j < KB; ++j)
+              if (p[j] >= 0) load8<F32>(a.rows + p[j] * a.rows_stride + (int64_t)col * (F32 ? 4 : 2), v[j]);
+#pragma unroll
+          for (int j = 0; j < KB; ++j) {
+            if (p[j] < 0) continue;
+            if (a.rows)
+#pragma unroll
+              for (int i = 0; i < 8; ++i) dot[j] += d[i] * v[j][i];
+            if (a.drows) {
+              float o[8];
+#pragma unroll
+              for (int i = 0; i < 8; ++i) o[i] = w[j] * d[i];
+              store8(a.drows + p[j] * a.drows_stride + (int64_t)col * (a.drows_f32 ? 4 : 2), a.drows_f32, o);
+            }
+          }
+        }
+      if (!a.dweights) continue;
+#pragma unroll
+      for (int j = 0; j < KB; ++j) dot[j] = wave_sum(dot[j]);
+      if constexpr (WPT > 1) {
+        if (lane == 0)
+#pragma unroll
+          for (int j = 0; j < KB; ++j) part[wave][j] = dot[j];
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < KB; ++j) {
+          dot[j] = part[wave - wt][j];
+#pragma unroll
+          for (int i = 1; i < WPT; ++i) dot[j] += part[wave - wt + i][j];
+        }
+        __syncthreads();
+      }
+      if (wt == 0 && lane == 0 && t < a.M)
+#pragma unroll
+        for (int j = 0; j < KB; ++j)
+          if (j0 + j < a.k) a.dweights[(int64_t)t * a.k + j0 + j] = dot[j];
+    }
+  }
+}
+
+// ---------------------------------------------------------------- router
+// dlogits of a token: w_j (dw_j - sum_i w_i dw_i) at its selected experts, zero
+// at the others.  A wave per token: lane j holds slot j, every lane adds up the
+// slots that name its experts (equal ids add up).
+__global__ __launch_bounds__(kThreads) void route_grad_kernel(const int32_t* __restrict__ ids,
+                                                              const float* __restrict__ w,
+                                                              const float* __restrict__ dw, int M, int E, int k,
+                                                              float* __restrict__ dlogits) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  for (int t = blockIdx.x * 4 + wave; t < M; t += gridDim.x * 4) {
+    const int64_t at = (int64_t)t * k + lane;
+    const int id = lane < k ? ids[at] : -1;
+    const bool ok = (unsigned)id < (unsigned)E;
+    const float wj = ok ? w[at] : 0.0f, dj = ok ? dw[at] : 0.0f;
+    const float mean = wave_sum(wj * dj);
+    const float g = wj * (dj - mean);
+    for (int e = lane; e < E; e += kWave) {
+      float s = 0.0f;
+      for (int j = 0; j < k; ++j) {
+        const int ij = __builtin_amdgcn_readlane(id, j);
+        const float gj = __uint_as_float((unsigned)__builtin_amdgcn_readlane((int)__float_as_uint(g), j));
+        s += ij == e ? gj : 0.0f;
+      }
+      dlogits[(int64_t)t * E + e] = s;
+    }
+  }
+}
+
+// ---------------------------------------------------------------- host side
+bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+moe_status_t launch_status() { return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_DEVICE; }
+
+constexpr int kMaxPairs = 1 << 26;
+constexpr int64_t kMaxRowBytes = (int64_t)1 << 22;
+constexpr int kMaxGrid = 1 << 22;
+
+int cdiv(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
+int grid_of(int64_t n) { return (int)(n < kMaxGrid ? n : kMaxGrid); }
+
+bool routed(int M, int k) { return (int64_t)M * k < kMaxPairs && k <= kMaxTopK; }
+
+// Rows of `width` elements of `esz` bytes, `stride` elements apart.
+moe_status_t check_matrix(const void* p, int64_t stride, int64_t width, int esz) {
+  if (!p || !aligned(p, 16) || stride < width || stride * esz % 16) return MOE_ERR_INVALID_ARG;
+  return stride * esz >= kMaxRowBytes ? MOE_ERR_UNSUPPORTED : MOE_OK;
+}
+
+bool known(moe_out_t t) { return t == MOE_OUT_BF16 || t == MOE_OUT_FP32; }
+int size_of(moe_out_t t) { return t == MOE_OUT_FP32 ? 4 : 2; }
+
+template <bool F32>
+void launch_combine(int grid_y, hipStream_t st, const CombineArgs& a) {
+  const dim3 grid(grid_of(cdiv(a.M, a.per_wg)), grid_y);
+  if (a.k <= 2)
+    combine_kernel<F32, 2><<<grid, kThreads, 0, st>>>(a);
+  else if (a.k <= 4)
+    combine_kernel<F32, 4><<<grid, kThreads, 0, st>>>(a);
+  else
+    combine_kernel<F32, 8><<<grid, kThreads, 0, st>>>(a);
+}
+
+template <bool F32, int KB>
+void launch_combine_grad(hipStream_t st, const CombineGradArgs& a) {
+  if (a.H <= 2048)
+    combine_grad_kernel<F32, KB, 1><<<grid_of(cdiv(a.M, 4)), kThreads, 0, st>>>(a);
+  else
+    combine_grad_kernel<F32, KB, 4><<<grid_of(a.M), kThreads, 0, st>>>(a);
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t moe_dispatch_workspace_size(int32_t M, int32_t top_k, int32_t E) {
+  if (M < 0 || top_k < 1 || E < 1 || E > kMaxExperts || !routed(M, top_k)) return 0;
+  const int P = M * top_k;
+  return P <= kCountAllPairs ? 0 : (size_t)(cdiv(P, kChunk) + 1) * E * 4;
+}
+
+moe_status_t moe_dispatch(const moe_dispatch_args_t* a, void* stream) {
+  if (!a || a->M < 0 || a->E < 1 || a->top_k < 1 || a->first_expert < 0 || a->row_bytes < 1) return MOE_ERR_INVALID_ARG;
+  if (!routed(a->M, a->top_k) || a->E > kMaxExperts || a->row_bytes % 16 || a->row_bytes >= kMaxRowBytes)
+    return MOE_ERR_UNSUPPORTED;
+  if (!a->offsets || !aligned(a->offsets, 4)) return MOE_ERR_INVALID_ARG;
+  const hipStream_t st = (hipStream_t)stream;
+  DispatchArgs d = {};
+  d.M = a->M;
+  d.k = a->top_k;
+  d.E = a->E;
+  d.first = a->first_expert;
+  d.row_bytes = a->row_bytes;
+  d.offsets = a->offsets;
+  d.group = 1;
+  const int P = a->M * a->top_k;
+  if (P > 0) {
+    if (!a->ids || !aligned(a->ids, 4) || !a->positions || !aligned(a->positions, 4) || !a->pairs ||
+        !aligned(a->pairs, 4))
+      return MOE_ERR_INVALID_ARG;
+    moe_status_t rc;
+    if ((rc = check_matrix(a->x, a->x_stride, a->row_bytes, 1)) != MOE_OK) return rc;
+    if ((rc = check_matrix(a->rows, a->rows_stride, a->row_bytes, 1)) != MOE_OK) return rc;
+    d.x = (const uint8_t*)a->x;
+    d.x_stride = a->x_stride;
+    d.ids = a->ids;
+    d.rows = (uint8_t*)a->rows;
+    d.rows_stride = a->rows_stride;
+    d.positions = a->positions;
+    d.pairs = a->pairs;
+    d.chunks = cdiv(P, kChunk);
+    if (P > kCountAllPairs) {
+      if (!a->workspace || !aligned(a->workspace, 16)) return MOE_ERR_INVALID_ARG;
+      if (a->workspace_bytes < moe_dispatch_workspace_size(a->M, a->top_k, a->E)) return MOE_ERR_WORKSPACE_TOO_SMALL;
+      d.counts = (int32_t*)a->workspace;
+    }
+    // tokens of a workgroup: as many as one wave ranks, fewer where that would leave CUs idle
+    const int most = kOwn / d.k, even = cdiv(d.M, 512);
+    d.group = even < most ? even : most;
+  }
+  const int groups = P ? cdiv(d.M, d.group) : 1;
+  // few workgroups share a token's row
+  const int steps = cdiv((int64_t)d.group * (d.row_bytes / 16), kThreads);
+  int split = 256 / groups;
+  split = split < 1 ? 1 : (split > steps ? steps : split);
+  const dim3 grid(groups, split);
+  if (P <= kCountAllPairs) {
+    dispatch_kernel<kCountAll><<<grid, kThreads, 0, st>>>(d);
+  } else {
+    count_chunks_kernel<<<d.chunks, kThreads, 0, st>>>(d.ids, P, d.E, d.first, d.counts);
+    if (d.chunks * (int64_t)d.E <= kSumChunksCounts) {
+      dispatch_kernel<kSumChunks><<<grid, kThreads, 0, st>>>(d);
+    } else {
+      scan_chunks_kernel<<<cdiv(d.E, kWave), 1024, 0, st>>>(d.counts, d.chunks, d.E);
+      dispatch_kernel<kScanned><<<grid, kThreads, 0, st>>>(d);
+    }
+  }
+  return launch_status();
+}
+
+moe_status_t moe_combine(const moe_combine_args_t* a, void* stream) {
+  if (!a || a->M < 0 || a->R < 0 || a->top_k < 1 || a->H < 1 || !known(a->rows_type) || !known(a->y_type))
+    return MOE_ERR_INVALID_ARG;
+  if (!routed(a->M, a->top_k) || a->R > kMaxPairs || a->H % 8) return MOE_ERR_UNSUPPORTED;
+  if (a->M == 0) return MOE_OK;
+  if (!a->positions || !aligned(a->positions, 4) || !aligned(a->weights, 4)) return MOE_ERR_INVALID_ARG;
+  moe_status_t rc;
+  if ((rc = check_matrix(a->rows, a->rows_stride, a->H, size_of(a->rows_type))) != MOE_OK) return rc;
+  if ((rc = check_matrix(a->y, a->y_stride, a->H, size_of(a->y_type))) != MOE_OK) return rc;
+  CombineArgs c = {};
+  const int cols = a->H / 8;
+  c.rows = (const uint8_t*)a->rows;
+  c.rows_stride = a->rows_stride * size_of(a->rows_type);
+  c.R = a->R;
+  c.positions = a->positions;
+  c.weights = a->weights;
+  c.M = a->M;
+  c.k = a->top_k;
+  c.H = a->H;
+  c.y = (uint8_t*)a->y;
+  c.y_stride = a->y_stride * size_of(a->y_type);
+  c.y_f32 = a->y_type == MOE_OUT_FP32;
+  c.per_wg = cols < kThreads ? kThreads / cols : 1;
+  const int grid_y = c.per_wg > 1 ? 1 : cdiv(cols, kThreads);
+  if (a->rows_type == MOE_OUT_FP32)
+    launch_combine<true>(grid_y, (hipStream_t)stream, c);
+  else
+    launch_combine<false>(grid_y, (hipStream_t)stream, c);
+  return launch_status();
+}
+
+moe_status_t moe_combine_grad(const moe_combine_grad_args_t* a, void* stream) {
+  if (!a || a->M < 0 || a->R < 0 || a->top_k < 1 || a->H < 1 || !known(a->dy_type) || !known(a->rows_type) ||
+      !known(a->drows_type))
+    return MOE_ERR_INVALID_ARG;
+  if (!routed(a->M, a->top_k) || a->R > kMaxPairs || a->H % 8) return MOE_ERR_UNSUPPORTED;
+  if (a->M == 0) return MOE_OK;
+  if (!a->positions || !aligned(a->positions, 4) || !aligned(a->weights, 4) || !aligned(a->dweights, 4))
+    return MOE_ERR_INVALID_ARG;
+  if ((!a->drows && !a->dweights) || (a->rows != nullptr) != (a->dweights != nullptr)) return MOE_ERR_INVALID_ARG;
+  moe_status_t rc;
+  if ((rc = check_matrix(a->dy, a->dy_stride, a->H, size_of(a->dy_type))) != MOE_OK) return rc;
+  if (a->rows && (rc = check_matrix(a->rows, a->rows_stride, a->H, size_of(a->rows_type))) != MOE_OK) return rc;
+  if (a->drows && (rc = check_matrix(a->drows, a->drows_stride, a->H, size_of(a->drows_type))) != MOE_OK) return rc;
+  CombineGradArgs c = {};
+  c.dy = (const uint8_t*)a->dy;
+  c.dy_stride = a->dy_stride * size_of(a->dy_type);
+  c.dy_f32 = a->dy_type == MOE_OUT_FP32;
+  c.rows = (const uint8_t*)a->rows;
+  c.rows_stride = a->rows_stride * size_of(a->rows_type);
+  c.R = a->R;
+  c.positions = a->positions;
+  c.weights = a->weights;
+  c.M = a->M;
+  c.k = a->top_k;
+  c.H = a->H;
+  c.drows = (uint8_t*)a->drows;
+  c.drows_stride = a->drows_stride * size_of(a->drows_type);
+  c.drows_f32 = a->drows_type == MOE_OUT_FP32;
+  c.dweights = a->dweights;
+  const hipStream_t st = (hipStream_t)stream;
+  const bool f32 = a->rows_type == MOE_OUT_FP32;
+  if (a->top_k <= 2)
+    f32 ? launch_combine_grad<true, 2>(st, c) : launch_combine_grad<false, 2>(st, c);
+  else
+    f32 ? launch_combine_grad<true, 8>(st, c) : launch_combine_grad<false, 8>(st, c);
+  return launch_status();
+}
+
+moe_status_t moe_route_topk_grad(const int32_t* topk_ids, const float* topk_weights, const float* dweights, int32_t M,
+                                 int32_t E, int32_t top_k, float* dlogits, void* stream) {
+  if (M < 0 || E < 1 || top_k < 1) return MOE_ERR_INVALID_ARG;
+  if (E > kMaxExperts || !routed(M, top_k)) return MOE_ERR_UNSUPPORTED;
+  if (M == 0) return MOE_OK;
+  if (!topk_ids || !topk_weights || !dweights || !dlogits || !aligned(topk_ids, 4) || !aligned(topk_weights, 4) ||
+      !aligned(dweights, 4) || !aligned(dlogits, 4))
+    return MOE_ERR_INVALID_ARG;
+  route_grad_kernel<<<grid_of(cdiv(M, 4)), kThreads, 0, (hipStream_t)stream>>>(topk_ids, topk_weights, dweights, M, E,
+                                                                               top_k, dlogits);
+  return launch_status();
+}
+
+}  // extern "C"
