@@ -9,6 +9,7 @@ is not built, every call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional, Sequence
 
@@ -469,6 +470,11 @@ def fused_forward(x: torch.Tensor, logits: Optional[torch.Tensor], w13: torch.Te
 
 
 # ------------------------------------------------------------------ grouped products and the checkpointed activation
+@functools.lru_cache(maxsize=None)
+def _device(index: int) -> torch.device:
+    return torch.device("cuda", index)
+
+
 class _Call:
     """The tensors of one call: all on one GPU, whose current stream (or
     `stream`) it runs on; outputs made here are from that stream's memory.  A
@@ -495,7 +501,11 @@ class _Call:
         raise ValueError("%s is on %s, the other operands on cuda:%d" % (name, t.device, self.index))
 
     def empty(self, shape, dtype):
-        return _empty(shape, dtype, self.index, self.given)
+        if self.given is not None:
+            return _empty(shape, dtype, self.index, self.given)
+        # 0.5 us less than torch.empty with a device made anew
+        steps = (1,) if len(shape) == 1 else (shape[1], 1) if len(shape) == 2 else (shape[1] * shape[2], shape[2], 1)
+        return torch.empty_strided(shape, steps, dtype=dtype, device=_device(self.index))
 
     def vector(self, t, name, dtype, n):
         return None if t is None else self.need(t, name, dtype, (n,))
@@ -758,7 +768,11 @@ def dispatch(x: torch.Tensor, ids: torch.Tensor, E: int, out: Optional[torch.Ten
     if out is None:
         out = call.empty((P, H), x.dtype)
     op, os_ = _matrix(call, out, "out", (x.dtype,), H, P)
-    offsets, positions, pairs = (call.empty(s, torch.int32) for s in ((max(E, 0) + 1,), (M, k), (P,)))
+    # one allocation for the three: 1.5 us less
+    n = max(E, 0) + 1
+    ints = call.empty((n + 2 * P,), torch.int32)
+    offsets, positions, pairs = (ints.as_strided((n,), (1,), 0), ints.as_strided((M, k), (k, 1), n),
+                                 ints.as_strided((P,), (1,), n + P))
     need = (_lib or load()).moe_dispatch_workspace_size(M, k, E)
     ws = _empty((need,), torch.uint8, call.index, stream, scratch=True) if need else None
     call.run("moe_dispatch", ctypes.byref(_DispatchArgs(
