@@ -692,9 +692,10 @@ moe_status_t moe_swiglu_int8(const void* gu, int64_t gu_stride, const float* row
  *   out[i,n] = s * w_scale[e,n] * sum over k of q[k] * w[e,n,k]
  * the sum in int32, exact.  in.data: codes int8 with in_scale fp32 [in.rows]
  * (one per row of the matrix that the ids choose from), or, with in_scale NULL,
- * bf16 rows, which the call turns to 8 bits itself (moe_quant_int8 of all
- * in.rows rows) in `workspace` (moe_grouped_int8_workspace_size bytes, 256-byte
- * aligned).  in.stride counts elements of their type.  The other conventions
+ * bf16 rows, which the call turns to 8 bits itself, to the bits of
+ * moe_quant_int8, in `workspace` (moe_grouped_int8_workspace_size bytes, 256-byte
+ * aligned; none for few rows and weights, whose codes are made on the way into
+ * the product).  in.stride counts elements of their type.  The other conventions
  * are the grouped products' (rows, offsets, ids, out, errors); K is a multiple
  * of 16 below 2^17 (bf16 rows: at most 2^16), N of 8, an expert's matrix below
  * 2^31 bytes, in.rows below 2^26.
@@ -712,9 +713,9 @@ typedef struct {
   size_t workspace_bytes;
 } moe_grouped_int8_args_t;
 
-/* Host-only: bytes that moe_grouped_gemm_int8 needs for bf16 rows; 0 for invalid
- * or unsupported sizes. */
-size_t moe_grouped_int8_workspace_size(int32_t rows, int32_t K);
+/* Host-only: bytes that moe_grouped_gemm_int8 needs for `rows` bf16 rows (in.rows);
+ * 0 for invalid or unsupported sizes too. */
+size_t moe_grouped_int8_workspace_size(int32_t R, int32_t E, int32_t N, int32_t K, int32_t rows);
 moe_status_t moe_grouped_gemm_int8(const moe_grouped_int8_args_t* args, void* stream);
 
 #ifdef __cplusplus

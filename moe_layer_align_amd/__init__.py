@@ -182,7 +182,7 @@ def load():
     lib.moe_swiglu_int8.restype = ctypes.c_int
     lib.moe_swiglu_int8.argtypes = [vp, i64, vp, i32, i32, vp, vp, vp, vp]
     lib.moe_grouped_int8_workspace_size.restype = sz
-    lib.moe_grouped_int8_workspace_size.argtypes = [i32, i32]
+    lib.moe_grouped_int8_workspace_size.argtypes = [i32] * 5
     lib.moe_grouped_gemm_int8.restype = ctypes.c_int
     lib.moe_grouped_gemm_int8.argtypes = [ctypes.POINTER(_GroupedInt8Args), vp]
     if lib.moe_abi_version() != _ABI:
@@ -941,7 +941,7 @@ def grouped_gemm_int8(a: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor, o
         raise ValueError("a_scale goes with int8 rows")
     src = call.rows(a, "input", torch.int8 if a.dtype is torch.int8 else torch.bfloat16, K, a_rows, a_div, R)
     if scale is None:
-        need = (_lib or load()).moe_grouped_int8_workspace_size(rows, K)
+        need = (_lib or load()).moe_grouped_int8_workspace_size(R, E, N, K, rows)
         ws = _empty((need,), torch.uint8, call.index, stream, scratch=True) if need else None
     call.run("moe_grouped_gemm_int8", ctypes.byref(_GroupedInt8Args(
         R, E, N, K, off, src, scale, call.need(w, "w", torch.int8, (E, N, K)),

@@ -42,7 +42,7 @@ struct GroupedInt8Args {
   int R, E, N, K;
   const int32_t* offsets;
   RowsArg in, out;
-  const float* in_scale;  // by matrix row
+  const float* in_scale;  // by matrix row; null: `in` is bf16
   const uint8_t* w;
   const float* w_scale;   // [E,N]
 };
@@ -59,6 +59,8 @@ __device__ __forceinline__ void group_range(const int32_t* offsets, int e, int R
 bool launch_grouped_tile(bool dgrad, bool f32, hipStream_t st, const GroupedArgs& a);
 bool launch_grouped_wgrad(bool f32, bool accumulate, hipStream_t st, const GroupedWgradArgs& a);
 bool launch_grouped_stream(int format, bool f32, hipStream_t st, const GroupedArgs& a);
+// Whether the product of these sizes takes bf16 rows as they are.
+bool int8_rows_in_stream(int R, int E, int64_t N, int64_t K);
 bool launch_grouped_int8(bool f32, hipStream_t st, const GroupedInt8Args& a);
 bool launch_grouped_tile_int8(bool f32, hipStream_t st, const GroupedInt8Args& a);
 

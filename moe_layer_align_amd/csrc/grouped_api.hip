@@ -175,9 +175,9 @@ moe_status_t moe_swiglu_int8(const void* gu, int64_t gu_stride, const float* row
   return launch_status();
 }
 
-size_t moe_grouped_int8_workspace_size(int32_t rows, int32_t K) {
-  if (rows < 0 || K < 1 || !int8_sizes(rows, K)) return 0;
-  return int8_scales_at(rows, K) + (size_t)rows * 4;
+size_t moe_grouped_int8_workspace_size(int32_t R, int32_t E, int32_t N, int32_t K, int32_t rows) {
+  if (R < 0 || E < 1 || N < 1 || K < 1 || rows < 0 || !int8_sizes(rows, K)) return 0;
+  return int8_rows_in_stream(R, E, N, K) ? 0 : int8_scales_at(rows, K) + (size_t)rows * 4;
 }
 
 moe_status_t moe_grouped_gemm_int8(const moe_grouped_int8_args_t* a, void* stream) {
@@ -198,13 +198,14 @@ moe_status_t moe_grouped_gemm_int8(const moe_grouped_int8_args_t* a, void* strea
   const hipStream_t st = (hipStream_t)stream;
   GroupedInt8Args g{a->R,          a->E, a->N, a->K, a->offsets, rows_arg(a->in), rows_arg(a->out), a->in_scale,
                     (const uint8_t*)a->w, a->w_scale};
-  if (!quantised) {
+  const size_t need =
+      quantised ? 0 : moe_grouped_int8_workspace_size(a->R, a->E, a->N, a->K, a->in.rows);
+  if (need) {
     if (!a->workspace || !aligned(a->workspace, 256)) return MOE_ERR_INVALID_ARG;
-    if (a->workspace_bytes < moe_grouped_int8_workspace_size(a->in.rows, a->K)) return MOE_ERR_WORKSPACE_TOO_SMALL;
+    if (a->workspace_bytes < need) return MOE_ERR_WORKSPACE_TOO_SMALL;
     uint8_t* const codes = (uint8_t*)a->workspace;
     float* const scales = (float*)(codes + int8_scales_at(a->in.rows, a->K));
-    if (a->in.rows > 0)
-      launch_int8_rows<false>(Int8Args{g.in.p, a->in.stride, a->in.rows, a->K, nullptr, nullptr, codes, scales}, st);
+    launch_int8_rows<false>(Int8Args{g.in.p, a->in.stride, a->in.rows, a->K, nullptr, nullptr, codes, scales}, st);
     g.in.p = codes;
     g.in.stride = a->K;
     g.in_scale = scales;

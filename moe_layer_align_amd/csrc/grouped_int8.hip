@@ -15,34 +15,75 @@
 #include <type_traits>
 
 #include "grouped_stream.h"
+#include "int8.h"
 
 namespace moe {
 namespace {
 
 constexpr int kStep = 128;  // K per step
+// bf16 rows become codes inside the product, which saves a launch and its codes'
+// way through memory, where the weights that may be read are fewer bytes than this
+// and the rows few: one token, top-2 of 8 experts of 4096 x 2048 12.0 us a call
+// against 16.5 in two launches; from 200 MB on there is nothing between the two
+// (one token, 28672 x 4096 49.0 and 48.8).
+constexpr int64_t kOneLaunchBytes = (int64_t)1 << 27;
+constexpr int kOneLaunchRows = 8;  // per expert, on average
 
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) int lds_i32;
+typedef __attribute__((address_space(3))) unsigned lds_u32;
 typedef __attribute__((address_space(3))) i32x4 lds_i32x4;
 
 __device__ __forceinline__ i32x4 mfma_i8(u32x4 a, u32x4 b, i32x4 c) {
   return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, a), __builtin_bit_cast(i32x4, b), c, 0, 0, 0);
 }
 
+// The largest magnitudes of grouped rows [i0, i0 + n) of bf16, as fp32 bits, to
+// top[0..n): wave w takes rows w, w + 4, ...; rows at or beyond hi and masked ones
+// have none.
+__device__ __forceinline__ void row_tops(const GroupedInt8Args& a, int i0, int n, int hi, lds_u32* top) {
+  typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+  constexpr int kBatch = 8;  // loads in flight
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int chunks = a.K / 8;
+  for (int r = wave; r < n; r += 4) {
+    u16x2 m = {0, 0};
+    const int row = i0 + r < hi ? row_of(a.in, i0 + r) : -1;
+    if (row >= 0) {
+      const u32x4* const p = (const u32x4*)(a.in.p + row * a.in.stride * 2);
+      for (int c = lane; c < chunks; c += kBatch * kWave) {
+        u32x4 v[kBatch];
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) v[u] = p[min(c + u * kWave, chunks - 1)];
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u)
+#pragma unroll
+          for (int w = 0; w < 4; ++w) m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2, v[u][w] & 0x7fff7fffu));
+      }
+    }
+    const unsigned t = wave_umax(m[0] > m[1] ? m[0] : m[1]);
+    if (lane == 0) top[r] = t << 16;
+  }
+}
+
 // Grouped rows [i0, i0 + 16 NT) of expert e, of which those below hi are
-// written.
-template <bool F32, int WK, int FT, int NT>
-__device__ __forceinline__ void pass(const GroupedInt8Args& a, int e, int n0, int i0, int hi, lds_u8* smem) {
+// written.  BF16: the rows are bf16 and become codes here, on their way from
+// memory to the MFMA, under the largest magnitude that a first look at them
+// finds while the first weights are on their way.
+template <bool BF16, bool F32, int WK, int FT, int NT>
+__device__ __forceinline__ void pass(const GroupedInt8Args& a, int e, int n0, int i0, int hi, lds_u8* smem,
+                                     lds_u32* top) {
   constexpr int kBand = 16 * FT * (4 / WK);  // weight rows of the workgroup
   constexpr int kLd = kBand + 4;              // row stride of the partial sums
   constexpr int kStage = stage_bytes(FT);
+  constexpr int kEsz = BF16 ? 2 : 1;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wk = wave % WK, wb = wave / WK;
   const int r16 = lane & 15, q = lane >> 4;
   const int nstep = (a.K + kStep - 1) / kStep;
   const unsigned wrow = (unsigned)a.K;
   const __amdgpu_buffer_rsrc_t rw = buffer(a.w + (int64_t)e * a.N * wrow, (unsigned)a.N * wrow);
-  const __amdgpu_buffer_rsrc_t rx = buffer(a.in.ids ? a.in.p : a.in.p + (int64_t)i0 * a.in.stride, kOob);
+  const __amdgpu_buffer_rsrc_t rx = buffer(a.in.ids ? a.in.p : a.in.p + (int64_t)i0 * a.in.stride * kEsz, kOob);
   lds_u8* const stage = smem + wave * (2 * kStage);
   const int nb = n0 + 16 * FT * wb;  // the wave's first weight row
 
@@ -63,14 +104,33 @@ __device__ __forceinline__ void pass(const GroupedInt8Args& a, int e, int n0, in
   };
   unsigned x0[NT];
   struct Step {
-    u32x4 x[NT][2];
+    u32x4 x[NT][2][kEsz];
   };
   auto load_x = [&](Step& g, int c) {
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
       for (int i = 0; i < 2; ++i)
-        g.x[t][i] = load16(rx, c * kStep + 64 * i + 16 * q < a.K ? x0[t] + c * kStep + 64 * i : kOob);
+#pragma unroll
+        for (int h = 0; h < kEsz; ++h)
+          g.x[t][i][h] = load16(
+              rx, c * kStep + 64 * i + 16 * q < a.K ? x0[t] + (unsigned)(c * kStep + 64 * i) * kEsz + 16 * h : kOob);
+  };
+  RowScale rs[NT];
+  auto codes = [&](const Step& g, int t, int i) {
+    if constexpr (BF16) {
+      float lo[8], hi8[8], v[16];
+      unpack8(g.x[t][i][0], lo);
+      unpack8(g.x[t][i][kEsz - 1], hi8);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        v[k] = lo[k];
+        v[8 + k] = hi8[k];
+      }
+      return int8_codes(v, rs[t]);
+    } else {
+      return g.x[t][i][0];
+    }
   };
   i32x4 acc[FT][NT] = {};
   // Fragments of a stage: tile f's row at f * 2048, chunk 4 i + q.
@@ -79,7 +139,7 @@ __device__ __forceinline__ void pass(const GroupedInt8Args& a, int e, int n0, in
 
   // One step: its loads have landed when at most those of the next step are
   // outstanding (they are issued in this order and kept in it by the fences).
-  constexpr int kLater = 2 * FT + 2 * NT;  // loads of a step
+  constexpr int kLater = 2 * FT + 2 * kEsz * NT;  // loads of a step
   static_assert(kLater < 64, "vmcnt range");
   auto fence = [] {
     asm volatile("" ::: "memory");
@@ -96,11 +156,15 @@ __device__ __forceinline__ void pass(const GroupedInt8Args& a, int e, int n0, in
     if constexpr (more()) load_w(c + 2 * WK, b);
     fence();
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < 2; ++i) {
+      u32x4 x[NT];
+#pragma unroll
+      for (int t = 0; t < NT; ++t) x[t] = codes(g, t, i);
 #pragma unroll
       for (int f = 0; f < FT; ++f)
 #pragma unroll
-        for (int t = 0; t < NT; ++t) acc[f][t] = mfma_i8(g.x[t][i], w[f][i], acc[f][t]);
+        for (int t = 0; t < NT; ++t) acc[f][t] = mfma_i8(x[t], w[f][i], acc[f][t]);
+    }
     fence();
     if constexpr (more()) load_x(g, c + 2 * WK);
     fence();
@@ -129,7 +193,7 @@ __device__ __forceinline__ void pass(const GroupedInt8Args& a, int e, int n0, in
   for (int t = 0; t < NT; ++t) {
     const int i = i0 + 16 * t + r16;
     const int m = i < hi ? (a.in.ids ? row_of(a.in, i, in_id[t]) : i - i0) : -1;
-    x0[t] = m >= 0 ? (unsigned)m * (unsigned)a.in.stride + 16 * q : kOob;
+    x0[t] = m >= 0 ? ((unsigned)m * (unsigned)a.in.stride + 16 * q) * kEsz : kOob;
   }
   load_x(g0, wk);
   fence();
@@ -139,8 +203,10 @@ __device__ __forceinline__ void pass(const GroupedInt8Args& a, int e, int n0, in
 #pragma unroll
   for (int u = 0; u < kStores; ++u) {
     const int at_u = u * 256 + tid, i = min(i0 + at_u / kCols, last), n = min(n0 + (at_u % kCols) * kPer, a.N - kPer);
-    const int m = row_of(a.in, i, from_id[u]);
-    sa[u] = m < 0 ? 0.0f : a.in_scale[m];
+    if constexpr (!BF16) {
+      const int m = row_of(a.in, i, from_id[u]);
+      sa[u] = m < 0 ? 0.0f : a.in_scale[m];
+    }
 #pragma unroll
     for (int h = 0; h < kPer / 4; ++h) sw[u][h] = *(const f32x4*)(a.w_scale + (int64_t)e * a.N + n + 4 * h);
   }
@@ -148,6 +214,15 @@ __device__ __forceinline__ void pass(const GroupedInt8Args& a, int e, int n0, in
   load_w(wk + WK, 1);
   fence();
   load_x(g1, wk + WK);
+  if constexpr (BF16) {
+    fence();
+    row_tops(a, i0, 16 * NT, hi, top);
+    __syncthreads();
+#pragma unroll
+    for (int t = 0; t < NT; ++t) rs[t] = row_scale(top[16 * t + r16]);
+#pragma unroll
+    for (int u = 0; u < kStores; ++u) sa[u] = row_scale(top[min((u * 256 + tid) / kCols, 16 * NT - 1)]).s;
+  }
   int c = wk;
   for (; c + 2 * WK < nstep; c += 2 * WK) {  // loads past the last step read nothing
     step(g0, c, 0, next_in_flight, std::true_type{});
@@ -193,44 +268,56 @@ __device__ __forceinline__ void pass(const GroupedInt8Args& a, int e, int n0, in
   __syncthreads();  // the next pass loads over the partial sums
 }
 
-template <bool F32, int WK, int FT, int NT>
+// An expert's rows in passes of 64, the last ones in one of 16 or 32 where that
+// holds them: the weights are streamed once per pass.  bf16 rows take passes of
+// at most 32 (their conversion costs as much per row as the stream of the weights).
+template <bool BF16, bool F32, int WK, int FT>
 __global__ __launch_bounds__(256, 2) void grouped_int8_kernel(GroupedInt8Args a) {
-  constexpr int kBand = 16 * FT * (4 / WK);
-  constexpr int kSums = WK * 16 * NT * (kBand + 4) * 4, kStages = 8 * stage_bytes(FT);
-  __shared__ __align__(16) uint8_t smem[kStages];
-  static_assert(kSums <= kStages, "the partial sums fit the stages");
+  constexpr int kBand = 16 * FT * (4 / WK), kMost = BF16 ? 2 : 4;
+  constexpr int kSums = WK * 16 * kMost * (kBand + 4) * 4, kStages = 8 * stage_bytes(FT);
+  __shared__ __align__(16) uint8_t smem[kStages > kSums ? kStages : kSums];
+  __shared__ unsigned top[16 * kMost];
   const Found f = find_expert(a.offsets, a.R, a.E);
   if (f.e >= a.E) return;
-  for (int i0 = f.lo; i0 < f.hi; i0 += 16 * NT)
-    pass<F32, WK, FT, NT>(a, f.e, blockIdx.x * kBand, i0, f.hi, (lds_u8*)smem);
+  const int n0 = blockIdx.x * kBand;
+  for (int i0 = f.lo; i0 < f.hi; i0 += 16 * kMost) {
+    const int n = f.hi - i0;
+    if (n <= 16)
+      pass<BF16, F32, WK, FT, 1>(a, f.e, n0, i0, f.hi, (lds_u8*)smem, (lds_u32*)top);
+    else if (n <= 32 || kMost == 2)
+      pass<BF16, F32, WK, FT, 2>(a, f.e, n0, i0, f.hi, (lds_u8*)smem, (lds_u32*)top);
+    else if constexpr (kMost == 4)
+      pass<BF16, F32, WK, FT, 4>(a, f.e, n0, i0, f.hi, (lds_u8*)smem, (lds_u32*)top);
+  }
 }
 
-template <bool F32, int WK, int FT, int NT>
+template <bool BF16, bool F32, int WK, int FT>
 void launch(hipStream_t st, const GroupedInt8Args& a) {
   constexpr int kBand = 16 * FT * (4 / WK);
-  grouped_int8_kernel<F32, WK, FT, NT><<<dim3((a.N + kBand - 1) / kBand, a.R < a.E ? a.R : a.E), 256, 0, st>>>(a);
+  grouped_int8_kernel<BF16, F32, WK, FT><<<dim3((a.N + kBand - 1) / kBand, a.R < a.E ? a.R : a.E), 256, 0, st>>>(a);
 }
 
-template <bool F32, int NT>
+template <bool BF16, bool F32>
 void pick(hipStream_t st, const GroupedInt8Args& a) {
-  const int steps = (a.K + kStep - 1) / kStep;
   const int64_t rows = (int64_t)(a.R < a.E ? a.R : a.E) * a.N;  // weight rows that may be read
   if (rows < 256 * 64)
-    launch<F32, 4, 2, NT>(st, a);
-  else if (steps >= 8)
-    launch<F32, 4, 4, NT>(st, a);
+    launch<BF16, F32, 4, 2>(st, a);
   else
-    launch<F32, 2, 4, NT>(st, a);
+    launch<BF16, F32, 4, 4>(st, a);
 }
 
 }  // namespace
 
+bool int8_rows_in_stream(int R, int E, int64_t N, int64_t K) {
+  return R <= kOneLaunchRows * (int64_t)E && (R < E ? R : E) * N * K < kOneLaunchBytes;
+}
+
 bool launch_grouped_int8(bool f32, hipStream_t st, const GroupedInt8Args& a) {
-  if (a.R > 16 * (int64_t)a.E) return launch_grouped_tile_int8(f32, st, a);
-  if (a.R <= 8 * (int64_t)a.E)
-    f32 ? pick<true, 1>(st, a) : pick<false, 1>(st, a);
+  if (a.R > 24 * (int64_t)a.E) return launch_grouped_tile_int8(f32, st, a);
+  if (a.in_scale)
+    f32 ? pick<false, true>(st, a) : pick<false, false>(st, a);
   else
-    f32 ? pick<true, 2>(st, a) : pick<false, 2>(st, a);
+    f32 ? pick<true, true>(st, a) : pick<true, false>(st, a);
   return true;
 }
 

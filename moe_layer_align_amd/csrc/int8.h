@@ -14,23 +14,53 @@ namespace moe {
 constexpr int kInt8Chunk = 16;
 constexpr int kInt8MaxRow = 1 << 16;
 
+// Largest value of a wave.  Magnitudes compare as their bits do, NaN above all.
+__device__ __forceinline__ unsigned wave_umax(unsigned v) {
+  v = umax(v, dpp_u32<kDppXor1>(v));
+  v = umax(v, dpp_u32<kDppXor2>(v));
+  v = umax(v, dpp_u32<kDppHalfMirror>(v));
+  v = umax(v, dpp_u32<kDppMirror>(v));
+  v = umax(v, dpp_u32<kDppBcast15, 0xA>(v));
+  v = umax(v, dpp_u32<kDppBcast31, 0xC>(v));
+  return (unsigned)__builtin_amdgcn_readlane((int)v, 63);
+}
+
+// A row's scale, and what its codes are formed with, from its largest magnitude
+// (fp32 bits, infinity or NaN where the row holds one).  f keeps 1/top and 127 v
+// inside fp32's normal range.
+struct RowScale {
+  float s, f127, top, r;  // scale; 127 f; f top; its reciprocal
+};
+__device__ __forceinline__ RowScale row_scale(unsigned bits) {
+  const float m = __uint_as_float(bits);
+  const float f = m < 0x1p-100f ? 0x1p100f : (m > 0x1p100f ? 0x1p-100f : 1.0f);
+  RowScale o;
+  o.s = bits == 0 ? 1.0f : (bits < 0x7f800000u ? m / 127.0f : __uint_as_float(0x7fc00000u));
+  o.top = bits == 0 ? 1.0f : m * f;
+  o.r = __builtin_amdgcn_rcpf(o.top);
+  o.f127 = 127.0f * f;
+  return o;
+}
+
 // Sixteen values at v -> codes.  127 v/top to the nearest integer, ties to even:
 // for bf16 values 127 v is exact, and one correction of the quotient by its
 // exact remainder makes a tie, which fp32 holds, come out as one; other
 // quotients lie further from a tie (2^-9 of their size) than fp32's error.
-__device__ __forceinline__ u32x4 int8_codes(const float (&v)[16], float top, float r) {
+// Adding 1.5 * 2^23 rounds to an integer and leaves its low byte in front.
+__device__ __forceinline__ u32x4 int8_codes(const float (&v)[16], const RowScale& s) {
   u32x4 o;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    unsigned w = 0;
+    unsigned b[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const float x = 127.0f * v[4 * i + j];
-      float q = x * r;
-      q = __builtin_fmaf(__builtin_fmaf(-q, top, x), r, q);
-      w |= ((unsigned)(int)__builtin_rintf(q) & 0xffu) << (8 * j);
+      const float x = s.f127 * v[4 * i + j];
+      const float q = x * s.r;
+      b[j] = __float_as_uint(__builtin_fmaf(__builtin_fmaf(-q, s.top, x), s.r, q) + 0x1.8p23f);
     }
-    o[i] = w;
+    // byte 0 of each
+    o[i] = __builtin_amdgcn_perm(__builtin_amdgcn_perm(b[3], b[2], 0x0c0c0400u),
+                                 __builtin_amdgcn_perm(b[1], b[0], 0x0c0c0400u), 0x05040100u);
   }
   return o;
 }
@@ -85,14 +115,7 @@ static __global__ __launch_bounds__(WPR < 4 ? 256 : 64 * WPR) void int8_rows_ker
       }
     }
   }
-  // magnitudes compare as their bits do; NaN above all
-  top = umax(top, dpp_u32<kDppXor1>(top));
-  top = umax(top, dpp_u32<kDppXor2>(top));
-  top = umax(top, dpp_u32<kDppHalfMirror>(top));
-  top = umax(top, dpp_u32<kDppMirror>(top));
-  top = umax(top, dpp_u32<kDppBcast15, 0xA>(top));
-  top = umax(top, dpp_u32<kDppBcast31, 0xC>(top));
-  top = (unsigned)__builtin_amdgcn_readlane((int)top, 63);
+  top = wave_umax(top);
   if constexpr (WPR > 1) {
     if (lane == 0) part[wave] = top;
     __syncthreads();
@@ -101,24 +124,13 @@ static __global__ __launch_bounds__(WPR < 4 ? 256 : 64 * WPR) void int8_rows_ker
     for (int w = 1; w < WPR; ++w) top = umax(top, part[w]);
   }
   if (!in) return;
-  const bool finite = top < 0x7f800000u, zero = top == 0;
-  const float m = __uint_as_float(top);
-  if (at == 0) {
-    float s = zero ? 1.0f : m / 127.0f;
-    if (a.weight) s *= a.weight[row];
-    a.scales[row] = finite ? s : __uint_as_float(0x7fc00000u);
-  }
-  // neither 1/top nor 127 v may leave fp32's normal range
-  const float f = m < 0x1p-100f ? 0x1p100f : (m > 0x1p100f ? 0x1p-100f : 1.0f);
-  const float scaled = zero ? 1.0f : m * f;
-  const float r = __builtin_amdgcn_rcpf(scaled);
+  const RowScale rs = row_scale(top);
+  if (at == 0) a.scales[row] = a.weight ? rs.s * a.weight[row] : rs.s;
+  const bool finite = top < 0x7f800000u;
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
     const int k = (c * 64 * WPR + at) * kInt8Chunk;
-    if (k >= a.K) continue;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) v[c][i] = finite ? v[c][i] * f : 0.0f;
-    *(u32x4*)(a.codes + (int64_t)row * a.K + k) = int8_codes(v[c], scaled, r);
+    if (k < a.K) *(u32x4*)(a.codes + (int64_t)row * a.K + k) = finite ? int8_codes(v[c], rs) : u32x4{0, 0, 0, 0};
   }
 }
 

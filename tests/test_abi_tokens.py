@@ -133,6 +133,9 @@ def int8(m, in_=None, out=None, **kw):  # noqa: F811
     return m.load().moe_grouped_gemm_int8(ctypes.byref(a), None)
 
 
+MANY = dict(R=1000, in_=dict(n=1000), out=dict(n=1000), in_scale=None, workspace=P, workspace_bytes=1 << 20)
+
+
 @pytest.mark.parametrize("kw,code", [
     (dict(R=-1), INVALID), (dict(E=0), INVALID), (dict(N=0), INVALID), (dict(K=-16), INVALID),
     (dict(out_type=2), INVALID), (dict(E=513), UNSUPPORTED), (dict(N=12), UNSUPPORTED), (dict(K=136), UNSUPPORTED),
@@ -146,8 +149,8 @@ def int8(m, in_=None, out=None, **kw):  # noqa: F811
     (dict(in_=dict(ids=P, n=(1 << 26) - 1)), UNSUPPORTED), (dict(out=dict(n=9)), INVALID),
     (dict(out=dict(data=P + 4)), INVALID), (dict(out=dict(ids=P, div=2)), INVALID),
     (dict(out=dict(stride=56)), INVALID),
-    (dict(in_scale=None), INVALID), (dict(in_scale=None, workspace=P + 128, workspace_bytes=1 << 20), INVALID),
-    (dict(in_scale=None, workspace=P, workspace_bytes=10 * 128 + 39), WORKSPACE),
+    (dict(MANY, workspace=None), INVALID), (dict(MANY, workspace=P + 128), INVALID),
+    (dict(MANY, workspace_bytes=1000 * 128 + 3999), WORKSPACE),
 ])
 def test_product_refusals(m, kw, code):  # noqa: F811
     assert int8(m, **kw) == code
@@ -156,8 +159,11 @@ def test_product_refusals(m, kw, code):  # noqa: F811
 
 def test_product_workspace(m):  # noqa: F811
     size = m.load().moe_grouped_int8_workspace_size
-    assert size(10, 128) == 1280 + 40 and size(3, 16) == 256 + 12 and size(0, 16) == 0
-    assert size(-1, 16) == size(1, 0) == size(1, 24) == size(1, 65552) == size(1 << 26, 16) == 0
+    assert size(1000, 4, 64, 128, 10) == 1280 + 40 and size(1000, 4, 64, 16, 3) == 256 + 12
+    assert size(1000, 4, 64, 16, 0) == size(10, 4, 64, 128, 10) == 0  # the latter in one launch
+    for bad in ((-1, 4, 64, 128, 9), (1000, 0, 64, 128, 9), (1000, 4, 0, 128, 9), (1000, 4, 64, 0, 9),
+                (1000, 4, 64, 24, 9), (1000, 4, 64, 65552, 9), (1000, 4, 64, 128, -1), (1000, 4, 64, 128, 1 << 26)):
+        assert size(*bad) == 0
     assert int8(m, R=0, offsets=None, w=None) == OK
 
 

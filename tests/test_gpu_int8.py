@@ -240,7 +240,10 @@ def test_product_of_bf16_rows(name, gather):
     counts, N, K, div = COUNTS[name], 136, 272, 3
     off, R = offsets_of(counts), int(sum(counts))
     n = R if not gather else R // div + 1
-    a = poisoned(bf16(rng, n, K), 8)
+    a = bf16(rng, n, K)
+    a[n - 1, 3] = float("nan")  # its scale, and with it its results
+    a[n // 2] = 0.0
+    a = poisoned(a, 8)
     ids = torch.from_numpy(rng.integers(-1, n * div + 2, R).astype(np.int32)).to(DEV) if gather else None
     w, ws = moe.quant_int8(bf16(rng, len(counts) * N, K).to(DEV))
     w, ws = w.view(-1, N, K), ws.view(-1, N)
@@ -249,7 +252,25 @@ def test_product_of_bf16_rows(name, gather):
     one = moe.grouped_gemm_int8(a, w, ws, g_off, **kw)
     codes, s = moe.quant_int8(a)
     two = moe.grouped_gemm_int8(codes, w, ws, g_off, a_scale=s, **kw)
-    assert torch.equal(one, two)
+    assert torch.equal(one.view(torch.int16), two.view(torch.int16))
+
+
+@pytest.mark.parametrize("counts", [[1] * 16, [2, 0, 0, 5, 1, 0, 0, 0], [0] * 9 + [17], [0] * 11 + [33, 1]])
+@pytest.mark.parametrize("N,K", [(8, 16), (200, 1168), (2056, 2064), (1032, 6160)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_codes_on_the_way(counts, N, K, dtype):
+    """Few bf16 rows, whose codes are made inside the product: the same bits as in two steps."""
+    say("codes on the way %s N=%d K=%d" % (counts, N, K))
+    rng = np.random.default_rng([len(counts), N, K])
+    off, R = offsets_of(counts), int(sum(counts))
+    a = poisoned(bf16(rng, R, K) * torch.from_numpy(np.exp(rng.standard_normal((R, 1)))).to(torch.bfloat16), 8)
+    w = torch.from_numpy(rng.integers(-128, 128, (len(counts), N, K), dtype=np.int8)).to(DEV)
+    ws = torch.rand(len(counts), N, device=DEV)
+    g_off = torch.from_numpy(off).to(DEV)
+    assert moe.load().moe_grouped_int8_workspace_size(R, len(counts), N, K, R) == 0
+    one = moe.grouped_gemm_int8(a, w, ws, g_off, out_dtype=dtype)
+    codes, s = moe.quant_int8(a)
+    assert torch.equal(one, moe.grouped_gemm_int8(codes, w, ws, g_off, a_scale=s, out_dtype=dtype))
 
 
 def test_no_rows():
