@@ -2,16 +2,21 @@
 // decoding: bound by the stream of the weights.
 //
 // As in the 4-bit products a workgroup multiplies a band of one expert's weight
-// rows by that expert's rows, 16 or 32 of them per pass, and each wave streams
+// rows by that expert's rows, 16, 32 or 64 of them per pass, and each wave streams
 // its own part of the band through a private pair of LDS stages by direct-to-LDS
-// loads of whole lines.  A step is 128 of K, 128 bytes of a weight row: lane l
-// holds bytes 64 i + 16 (l/16) .. + 15 (i = 0, 1) of weight row l%16, and the
-// same of the rows' codes, so that 16x16x64 MFMAs multiply them as they lie.
-// The weights are the B operand: a lane's four results are four rows' sums for
-// one weight row.  Sums are exact in int32; the scales join once, at the end.
+// loads of whole lines: 64 tokens over 256 experts of 4096 x 7168, of which 151
+// hold rows (4.4 GB), 657 to 682 us by machine, 6.5 to 6.7 TB/s; one token through
+// two of 28672 x 4096 (235 MB) 38 to 44 us.
 //
-// WK waves split K, step by step, and the others the band; partial sums meet in
-// LDS.
+// A step is 128 of K, 128 bytes of a weight row: lane l holds bytes 64 i + 16
+// (l/16) .. + 15 (i = 0, 1) of weight row l%16, and the same of the rows' codes,
+// so that 16x16x64 MFMAs multiply them as they lie.  The weights are the B
+// operand: a lane's four results are four rows' sums for one weight row.  Sums
+// are exact in int32; the scales join once, at the end.
+//
+// The four waves split K, step by step (wave w takes steps w, w + 4, ...); their
+// partial sums meet in LDS.  Few weight rows take bands of 32 instead of 64, so
+// that no CU is idle.
 #include <type_traits>
 
 #include "grouped_stream.h"
@@ -58,7 +63,8 @@ __device__ __forceinline__ void row_tops(const GroupedInt8Args& a, int i0, int n
 #pragma unroll
         for (int u = 0; u < kBatch; ++u)
 #pragma unroll
-          for (int w = 0; w < 4; ++w) m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2, v[u][w] & 0x7fff7fffu));
+          for (int w = 0; w < 4; ++w)
+            m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2, v[u][w] & 0x7fff7fffu));
       }
     }
     const unsigned t = wave_umax(m[0] > m[1] ? m[0] : m[1]);
@@ -70,29 +76,27 @@ __device__ __forceinline__ void row_tops(const GroupedInt8Args& a, int i0, int n
 // written.  BF16: the rows are bf16 and become codes here, on their way from
 // memory to the MFMA, under the largest magnitude that a first look at them
 // finds while the first weights are on their way.
-template <bool BF16, bool F32, int WK, int FT, int NT>
+template <bool BF16, bool F32, int FT, int NT>
 __device__ __forceinline__ void pass(const GroupedInt8Args& a, int e, int n0, int i0, int hi, lds_u8* smem,
                                      lds_u32* top) {
-  constexpr int kBand = 16 * FT * (4 / WK);  // weight rows of the workgroup
+  constexpr int kBand = 16 * FT;  // weight rows of the workgroup
   constexpr int kLd = kBand + 4;              // row stride of the partial sums
   constexpr int kStage = stage_bytes(FT);
   constexpr int kEsz = BF16 ? 2 : 1;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wk = wave % WK, wb = wave / WK;
   const int r16 = lane & 15, q = lane >> 4;
   const int nstep = (a.K + kStep - 1) / kStep;
   const unsigned wrow = (unsigned)a.K;
   const __amdgpu_buffer_rsrc_t rw = buffer(a.w + (int64_t)e * a.N * wrow, (unsigned)a.N * wrow);
   const __amdgpu_buffer_rsrc_t rx = buffer(a.in.ids ? a.in.p : a.in.p + (int64_t)i0 * a.in.stride * kEsz, kOob);
   lds_u8* const stage = smem + wave * (2 * kStage);
-  const int nb = n0 + 16 * FT * wb;  // the wave's first weight row
 
-  // weights: load d of a step takes rows nb + 8d + lane/8, lane l the 16-byte
+  // weights: load d of a step takes rows n0 + 8d + lane/8, lane l the 16-byte
   // chunk (l%8) ^ pf_mix(row) of their 128 bytes; rows at or past N lie past
   // the buffer, chunks past K take kOob
   const int wchunk = (lane & 7) ^ (lane >> 3);
-  const unsigned w0 = (unsigned)(nb + (lane >> 3)) * wrow + (wchunk << 4);
-  const unsigned w1 = (unsigned)(nb + (lane >> 3)) * wrow + ((wchunk ^ 1) << 4);
+  const unsigned w0 = (unsigned)(n0 + (lane >> 3)) * wrow + (wchunk << 4);
+  const unsigned w1 = (unsigned)(n0 + (lane >> 3)) * wrow + ((wchunk ^ 1) << 4);
   auto load_w = [&](int c, int b) {
     const int left = a.K - c * kStep;  // bytes of a row from this step on
     const bool ok0 = (wchunk << 4) < left, ok1 = ((wchunk ^ 1) << 4) < left;
@@ -153,7 +157,7 @@ __device__ __forceinline__ void pass(const GroupedInt8Args& a, int e, int n0, in
     u32x4 w[FT][2];
     read_stage<FT>(w, frag0 + b * kStage, frag1 + b * kStage);  // the stage is read: load it again
     fence();
-    if constexpr (more()) load_w(c + 2 * WK, b);
+    if constexpr (more()) load_w(c + 8, b);
     fence();
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -166,7 +170,7 @@ __device__ __forceinline__ void pass(const GroupedInt8Args& a, int e, int n0, in
         for (int t = 0; t < NT; ++t) acc[f][t] = mfma_i8(x[t], w[f][i], acc[f][t]);
     }
     fence();
-    if constexpr (more()) load_x(g, c + 2 * WK);
+    if constexpr (more()) load_x(g, c + 8);
     fence();
   };
   constexpr std::integral_constant<int, kLater> next_in_flight{};
@@ -187,7 +191,7 @@ __device__ __forceinline__ void pass(const GroupedInt8Args& a, int e, int n0, in
     out_id[u] = a.out.ids ? a.out.ids[i] : 0;
   }
   fence();
-  load_w(wk, 0);
+  load_w(wave, 0);
   fence();
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
@@ -195,7 +199,7 @@ __device__ __forceinline__ void pass(const GroupedInt8Args& a, int e, int n0, in
     const int m = i < hi ? (a.in.ids ? row_of(a.in, i, in_id[t]) : i - i0) : -1;
     x0[t] = m >= 0 ? ((unsigned)m * (unsigned)a.in.stride + 16 * q) * kEsz : kOob;
   }
-  load_x(g0, wk);
+  load_x(g0, wave);
   fence();
   // the scales of the thread's results
   float sa[kStores];
@@ -211,9 +215,9 @@ __device__ __forceinline__ void pass(const GroupedInt8Args& a, int e, int n0, in
     for (int h = 0; h < kPer / 4; ++h) sw[u][h] = *(const f32x4*)(a.w_scale + (int64_t)e * a.N + n + 4 * h);
   }
   fence();
-  load_w(wk + WK, 1);
+  load_w(wave + 4, 1);
   fence();
-  load_x(g1, wk + WK);
+  load_x(g1, wave + 4);
   if constexpr (BF16) {
     fence();
     row_tops(a, i0, 16 * NT, hi, top);
@@ -223,17 +227,17 @@ __device__ __forceinline__ void pass(const GroupedInt8Args& a, int e, int n0, in
 #pragma unroll
     for (int u = 0; u < kStores; ++u) sa[u] = row_scale(top[min((u * 256 + tid) / kCols, 16 * NT - 1)]).s;
   }
-  int c = wk;
-  for (; c + 2 * WK < nstep; c += 2 * WK) {  // loads past the last step read nothing
+  int c = wave;
+  for (; c + 8 < nstep; c += 8) {  // loads past the last step read nothing
     step(g0, c, 0, next_in_flight, std::true_type{});
-    step(g1, c + WK, 1, next_in_flight, std::true_type{});
+    step(g1, c + 4, 1, next_in_flight, std::true_type{});
   }
   if (c < nstep) step(g0, c, 0, next_in_flight, std::false_type{});
-  if (c + WK < nstep) step(g1, c + WK, 1, none_in_flight, std::false_type{});
+  if (c + 4 < nstep) step(g1, c + 4, 1, none_in_flight, std::false_type{});
   fence();
   wait_vm<0>();  // loads past the last step still write LDS
   lds_i32* const red = (lds_i32*)smem;
-  // partial sums: [wk][row][weight row], over the stages
+  // partial sums: [wave][row][weight row], over the stages
   __syncthreads();
 #pragma unroll
   for (int f = 0; f < FT; ++f)
@@ -241,7 +245,7 @@ __device__ __forceinline__ void pass(const GroupedInt8Args& a, int e, int n0, in
     for (int t = 0; t < NT; ++t)
 #pragma unroll
       for (int v = 0; v < 4; ++v)
-        red[(wk * 16 * NT + 16 * t + 4 * q + v) * kLd + 16 * (FT * wb + f) + r16] = acc[f][t][v];
+        red[(wave * 16 * NT + 16 * t + 4 * q + v) * kLd + 16 * f + r16] = acc[f][t][v];
   __syncthreads();
 #pragma unroll
   for (int u = 0; u < kStores; ++u) {
@@ -254,7 +258,7 @@ __device__ __forceinline__ void pass(const GroupedInt8Args& a, int e, int n0, in
     for (int h = 0; h < kPer / 4; ++h) {
       i32x4 s = *(const lds_i32x4*)(red + row * kLd + col + 4 * h);
 #pragma unroll
-      for (int k = 1; k < WK; ++k) s += *(const lds_i32x4*)(red + (k * 16 * NT + row) * kLd + col + 4 * h);
+      for (int k = 1; k < 4; ++k) s += *(const lds_i32x4*)(red + (k * 16 * NT + row) * kLd + col + 4 * h);
 #pragma unroll
       for (int j = 0; j < 4; ++j) v[h][j] = (float)s[j] * sa[u] * sw[u][h][j];
     }
@@ -271,10 +275,10 @@ __device__ __forceinline__ void pass(const GroupedInt8Args& a, int e, int n0, in
 // An expert's rows in passes of 64, the last ones in one of 16 or 32 where that
 // holds them: the weights are streamed once per pass.  bf16 rows take passes of
 // at most 32 (their conversion costs as much per row as the stream of the weights).
-template <bool BF16, bool F32, int WK, int FT>
+template <bool BF16, bool F32, int FT>
 __global__ __launch_bounds__(256, 2) void grouped_int8_kernel(GroupedInt8Args a) {
-  constexpr int kBand = 16 * FT * (4 / WK), kMost = BF16 ? 2 : 4;
-  constexpr int kSums = WK * 16 * kMost * (kBand + 4) * 4, kStages = 8 * stage_bytes(FT);
+  constexpr int kBand = 16 * FT, kMost = BF16 ? 2 : 4;
+  constexpr int kSums = 4 * 16 * kMost * (kBand + 4) * 4, kStages = 8 * stage_bytes(FT);
   __shared__ __align__(16) uint8_t smem[kStages > kSums ? kStages : kSums];
   __shared__ unsigned top[16 * kMost];
   const Found f = find_expert(a.offsets, a.R, a.E);
@@ -283,37 +287,50 @@ __global__ __launch_bounds__(256, 2) void grouped_int8_kernel(GroupedInt8Args a)
   for (int i0 = f.lo; i0 < f.hi; i0 += 16 * kMost) {
     const int n = f.hi - i0;
     if (n <= 16)
-      pass<BF16, F32, WK, FT, 1>(a, f.e, n0, i0, f.hi, (lds_u8*)smem, (lds_u32*)top);
+      pass<BF16, F32, FT, 1>(a, f.e, n0, i0, f.hi, (lds_u8*)smem, (lds_u32*)top);
     else if (n <= 32 || kMost == 2)
-      pass<BF16, F32, WK, FT, 2>(a, f.e, n0, i0, f.hi, (lds_u8*)smem, (lds_u32*)top);
+      pass<BF16, F32, FT, 2>(a, f.e, n0, i0, f.hi, (lds_u8*)smem, (lds_u32*)top);
     else if constexpr (kMost == 4)
-      pass<BF16, F32, WK, FT, 4>(a, f.e, n0, i0, f.hi, (lds_u8*)smem, (lds_u32*)top);
+      pass<BF16, F32, FT, 4>(a, f.e, n0, i0, f.hi, (lds_u8*)smem, (lds_u32*)top);
   }
 }
 
-template <bool BF16, bool F32, int WK, int FT>
+template <bool BF16, bool F32, int FT>
 void launch(hipStream_t st, const GroupedInt8Args& a) {
-  constexpr int kBand = 16 * FT * (4 / WK);
-  grouped_int8_kernel<BF16, F32, WK, FT><<<dim3((a.N + kBand - 1) / kBand, a.R < a.E ? a.R : a.E), 256, 0, st>>>(a);
+  constexpr int kBand = 16 * FT;
+  grouped_int8_kernel<BF16, F32, FT><<<dim3((a.N + kBand - 1) / kBand, a.R < a.E ? a.R : a.E), 256, 0, st>>>(a);
 }
 
 template <bool BF16, bool F32>
 void pick(hipStream_t st, const GroupedInt8Args& a) {
   const int64_t rows = (int64_t)(a.R < a.E ? a.R : a.E) * a.N;  // weight rows that may be read
   if (rows < 256 * 64)
-    launch<BF16, F32, 4, 2>(st, a);
+    launch<BF16, F32, 2>(st, a);
   else
-    launch<BF16, F32, 4, 4>(st, a);
+    launch<BF16, F32, 4>(st, a);
+}
+
+// Streamed or tiled, by the rows per expert on average (streamed and tiled, us).
+// The stream has less to start and end: 402 MB of 128 experts of 1536 x 2048 with 2
+// rows 60.6 and 74.6, 8 76.5 and 83.5, 16 78.7 and 87.3, 64 112.9 and 102.0; 268
+// MB of 16 experts with 16 55.6 and 68.1.  It streams an expert's weights once per
+// 64 rows, which costs where a few experts hold most rows, the more so the more
+// there is to stream: under a Zipf-like routing of 16 rows 71.1 and 69.5, 63.1 and
+// 77.3, but 505.7 and 367.2 for 3.8 GB (256 experts of 2048 x 7168), which even
+// rows take as long in either form (2 rows 523.4 and 525.7, 16 718.6 and 719.4).
+bool streamed(int R, int E, int64_t N, int64_t K) {
+  const int rows = (R < E ? R : E) * N * K < ((int64_t)1 << 30) ? 16 : 4;
+  return R <= rows * (int64_t)E;
 }
 
 }  // namespace
 
 bool int8_rows_in_stream(int R, int E, int64_t N, int64_t K) {
-  return R <= kOneLaunchRows * (int64_t)E && (R < E ? R : E) * N * K < kOneLaunchBytes;
+  return streamed(R, E, N, K) && R <= kOneLaunchRows * (int64_t)E && (R < E ? R : E) * N * K < kOneLaunchBytes;
 }
 
 bool launch_grouped_int8(bool f32, hipStream_t st, const GroupedInt8Args& a) {
-  if (a.R > 24 * (int64_t)a.E) return launch_grouped_tile_int8(f32, st, a);
+  if (!streamed(a.R, a.E, a.N, a.K)) return launch_grouped_tile_int8(f32, st, a);
   if (a.in_scale)
     f32 ? pick<false, true>(st, a) : pick<false, false>(st, a);
   else

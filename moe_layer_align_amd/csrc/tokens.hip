@@ -135,7 +135,7 @@ __global__ __launch_bounds__(kThreads) void dispatch_kernel(DispatchArgs a) {
     before[e] = COUNTS == kScanned ? a.counts[(int64_t)chunk * a.E + e] : 0;
   }
   __syncthreads();
-  if constexpr (COUNTS == kSumChunks) {  // thread i adds up expert i % width of the chunks i / width, i / width + step, ..
+  if constexpr (COUNTS == kSumChunks) {  // thread i: expert i % width of the chunks i / width, i / width + step, ...
     const int width = a.E < kThreads ? a.E : kThreads, step = kThreads / width;
     const int first = tid / width, of = tid - first * width;
     for (int e = of; e < a.E && first < step; e += width) {
