@@ -17,6 +17,12 @@ namespace {
 
 constexpr int kThreads = 256;
 
+// 16 bytes of what a call reads once.  Kept out of the caches' way, the rows leave
+// them to the results (fresh buffers each call): 4096 tokens, top-8, H 2048,
+// combine_grad with the router's gradient 77.8 -> 57.6 us, dispatch 32.9 -> 30.4;
+// 8192 tokens, top-2, H 4096, fp32 rows, combine 63.6 -> 60.4.
+__device__ __forceinline__ u32x4 load_once(const uint8_t* p) { return __builtin_nontemporal_load((const u32x4*)p); }
+
 // ---------------------------------------------------------------- dispatch
 // A counting sort of the pairs by expert, stable in the pair index, and the copy
 // of the tokens' rows to where it puts them, in one kernel: workgroup x owns
@@ -220,7 +226,7 @@ __global__ __launch_bounds__(kThreads) void dispatch_kernel(DispatchArgs a) {
       const uint8_t* src = a.x + (t0 + t) * a.x_stride;
       u32x4 v[4];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) v[u] = *(const u32x4*)(src + min(c + u * kWave, per_row - 1) * 16);
+      for (int u = 0; u < 4; ++u) v[u] = load_once(src + min(c + u * kWave, per_row - 1) * 16);
       for (; todo; todo &= todo - 1) {
         uint8_t* dst = a.rows + __builtin_amdgcn_readlane(p, __ffsll(todo) - 1) * a.rows_stride;
 #pragma unroll
@@ -237,7 +243,7 @@ __global__ __launch_bounds__(kThreads) void dispatch_kernel(DispatchArgs a) {
       for (int j = 0; j < a.k; ++j) {
         const int p = place[t * a.k + j];
         if (p < 0) continue;
-        if (!have) v = *(const u32x4*)(a.x + (t0 + t) * a.x_stride + c * 16);
+        if (!have) v = load_once(a.x + (t0 + t) * a.x_stride + c * 16);
         have = true;
         *(u32x4*)(a.rows + p * a.rows_stride + c * 16) = v;
       }
@@ -302,7 +308,7 @@ __global__ __launch_bounds__(kThreads) void combine_kernel(CombineArgs a) {
         if (ok[j])
 #pragma unroll
           for (int i = 0; i < (F32 ? 2 : 1); ++i)
-            raw[j][i] = *(const u32x4*)(a.rows + p * a.rows_stride + (int64_t)col * (F32 ? 32 : 16) + 16 * i);
+            raw[j][i] = load_once(a.rows + p * a.rows_stride + (int64_t)col * (F32 ? 32 : 16) + 16 * i);
       }
 #pragma unroll
       for (int j = 0; j < KB; ++j) {
@@ -337,7 +343,9 @@ struct CombineGradArgs {
 // fixed order), 512 columns per wave and step, whose dy is read once for up to
 // KB slots.  The loads of a step are issued before the step ahead of it is
 // multiplied and stored: without that a wave's reads and writes take turns (4096
-// tokens, top-8, H 2048, with the router's gradient: 73.2 -> 60.5 us).
+// tokens, top-8, H 2048, with the router's gradient, a wave per token and the
+// results in one buffer: 73.2 -> 60.5 us).  Of four waves per token and one, in
+// fresh buffers: 55.1 and 57.5.
 template <bool F32, int KB, int WPT>
 __global__ __launch_bounds__(kThreads) void combine_grad_kernel(CombineGradArgs a) {
   constexpr int kTokens = 4 / WPT;  // per workgroup
@@ -362,15 +370,15 @@ __global__ __launch_bounds__(kThreads) void combine_grad_kernel(CombineGradArgs 
       const uint8_t* const dy = a.dy + t * a.dy_stride;
       auto load = [&](int col) {
         if (col >= a.H || t >= a.M) return;
-        d[0] = *(const u32x4*)(dy + (int64_t)col * (a.dy_f32 ? 4 : 2));
-        if (a.dy_f32) d[1] = *(const u32x4*)(dy + (int64_t)col * 4 + 16);
+        d[0] = load_once(dy + (int64_t)col * (a.dy_f32 ? 4 : 2));
+        if (a.dy_f32) d[1] = load_once(dy + (int64_t)col * 4 + 16);
         if (!a.rows) return;
 #pragma unroll
         for (int j = 0; j < KB; ++j)
           if (p[j] >= 0)
 #pragma unroll
             for (int i = 0; i < kRaw; ++i)
-              next[j][i] = *(const u32x4*)(a.rows + p[j] * a.rows_stride + (int64_t)col * (F32 ? 4 : 2) + 16 * i);
+              next[j][i] = load_once(a.rows + p[j] * a.rows_stride + (int64_t)col * (F32 ? 4 : 2) + 16 * i);
       };
       const int col0 = (wt * 64 + lane) * 8;
       load(col0);
@@ -492,7 +500,7 @@ void launch_combine(int grid_y, hipStream_t st, const CombineArgs& a) {
 
 template <bool F32, int KB>
 void launch_combine_grad(hipStream_t st, const CombineGradArgs& a) {
-  if (a.H <= 2048)
+  if (a.H <= 1024)
     combine_grad_kernel<F32, KB, 1><<<grid_of(cdiv(a.M, 4)), kThreads, 0, st>>>(a);
   else
     combine_grad_kernel<F32, KB, 4><<<grid_of(a.M), kThreads, 0, st>>>(a);
