@@ -739,6 +739,12 @@ def _matrix(call, t, name, dtypes, width, rows=None):
     return t.data_ptr() or 16, step[0] if shape[0] > 1 else width
 
 
+def _made(call, rows, width, dtype):
+    """A [rows, width] result made here: (tensor, pointer, stride)."""
+    t = call.empty((rows, width), dtype)
+    return t, t.data_ptr() or 16, width
+
+
 _ROW_TYPES = (torch.bfloat16, torch.float32)
 
 
@@ -766,8 +772,9 @@ def dispatch(x: torch.Tensor, ids: torch.Tensor, E: int, out: Optional[torch.Ten
     xp, xs = _matrix(call, x, "x", (x.dtype,), H, M)
     ip = call.need(ids, "ids", torch.int32, (M, k))
     if out is None:
-        out = call.empty((P, H), x.dtype)
-    op, os_ = _matrix(call, out, "out", (x.dtype,), H, P)
+        out, op, os_ = _made(call, P, H, x.dtype)
+    else:
+        op, os_ = _matrix(call, out, "out", (x.dtype,), H, P)
     # one allocation for the three: 1.5 us less
     n = max(E, 0) + 1
     ints = call.empty((n + 2 * P,), torch.int32)
@@ -797,8 +804,9 @@ def combine(rows: torch.Tensor, positions: torch.Tensor, weights: Optional[torch
     if out is None:
         dtype = rows.dtype if out_dtype is None else out_dtype
         _out_type(dtype, "out_dtype")
-        out = call.empty((M, H), dtype)
-    yp, ys = _matrix(call, out, "out", _ROW_TYPES, H, M)
+        out, yp, ys = _made(call, M, H, dtype)
+    else:
+        yp, ys = _matrix(call, out, "out", _ROW_TYPES, H, M)
     call.run("moe_combine", ctypes.byref(_CombineArgs(
         M, k, H, R, rp, rs, _OUT_TYPE[rows.dtype], call.need(positions, "positions", torch.int32, (M, k)),
         None if weights is None else call.need(weights, "weights", torch.float32, (M, k)), yp, ys,
@@ -834,16 +842,20 @@ def combine_grad(dy: torch.Tensor, rows: Optional[torch.Tensor], positions: torc
     rp, rs = (None, H) if rows is None else _matrix(call, rows, "rows", _ROW_TYPES, H)
     if drows is None:
         _out_type(out_dtype, "out_dtype")
-        drows = call.empty((R, H), out_dtype)
-    op, os_ = _matrix(call, drows, "drows", _ROW_TYPES, H, R)
-    if dweights is None and rows is not None:
+        drows, op, os_ = _made(call, R, H, out_dtype)
+    else:
+        op, os_ = _matrix(call, drows, "drows", _ROW_TYPES, H, R)
+    wp = None
+    if dweights is not None:
+        wp = call.need(dweights, "dweights", torch.float32, (M, k))
+    elif rows is not None:
         dweights = call.empty((M, k), torch.float32)
+        wp = dweights.data_ptr()
     call.run("moe_combine_grad", ctypes.byref(_CombineGradArgs(
         M, k, H, R, dp, ds, _OUT_TYPE[dy.dtype], rp, rs, 0 if rows is None else _OUT_TYPE[rows.dtype],
         call.need(positions, "positions", torch.int32, (M, k)),
         None if weights is None else call.need(weights, "weights", torch.float32, (M, k)), op, os_,
-        _OUT_TYPE[drows.dtype],
-        None if dweights is None else call.need(dweights, "dweights", torch.float32, (M, k)))))
+        _OUT_TYPE[drows.dtype], wp)))
     return drows, dweights
 
 
@@ -857,15 +869,29 @@ def route_topk_grad(ids: torch.Tensor, weights: torch.Tensor, dweights: torch.Te
     M, k = ids.shape
     _sizes(M | k | E)
     if out is None:
-        out = call.empty((M, max(E, 0)), torch.float32)
+        out, op, _ = _made(call, M, max(E, 0), torch.float32)
+    else:
+        op = call.need(out, "out", torch.float32, (M, E))
     call.run("moe_route_topk_grad", call.need(ids, "ids", torch.int32, (M, k)),
              call.need(weights, "weights", torch.float32, (M, k)),
-             call.need(dweights, "dweights", torch.float32, (M, k)), M, E, k,
-             call.need(out, "out", torch.float32, (M, E)))
+             call.need(dweights, "dweights", torch.float32, (M, k)), M, E, k, op)
     return out
 
 
 # ------------------------------------------------------------------ 8-bit integers
+def _codes(call, codes, scales, rows, width):
+    """The codes and scales of [rows, width], given or made here, and their pointers."""
+    if codes is None:
+        codes = call.empty((rows, width), torch.int8)
+        cp = codes.data_ptr()
+    else:
+        cp = call.need(codes, "codes", torch.int8, (rows, width))
+    if scales is None:
+        scales = call.empty((rows,), torch.float32)
+        return codes, cp, scales, scales.data_ptr()
+    return codes, cp, scales, call.need(scales, "scales", torch.float32, (rows,))
+
+
 def quant_int8(x: torch.Tensor, codes: Optional[torch.Tensor] = None, scales: Optional[torch.Tensor] = None,
                stream=None):
     """Rows of x bf16 [M,K] (may be strided) as 8-bit integers (moe_quant_int8):
@@ -877,10 +903,8 @@ def quant_int8(x: torch.Tensor, codes: Optional[torch.Tensor] = None, scales: Op
     M, K = x.shape
     _sizes(M | K)
     xp, xs = _matrix(call, x, "x", (torch.bfloat16,), K)
-    codes = call.empty((M, K), torch.int8) if codes is None else codes
-    scales = call.empty((M,), torch.float32) if scales is None else scales
-    call.run("moe_quant_int8", xp, xs, M, K, call.need(codes, "codes", torch.int8, (M, K)),
-             call.need(scales, "scales", torch.float32, (M,)))
+    codes, cp, scales, sp = _codes(call, codes, scales, M, K)
+    call.run("moe_quant_int8", xp, xs, M, K, cp, sp)
     return codes, scales
 
 
@@ -897,11 +921,9 @@ def swiglu_int8(gu: torch.Tensor, row_weight: Optional[torch.Tensor] = None, *,
     R, I = gu.shape[0], gu.shape[1] // 2
     _sizes(R | I)
     gp, gs = _matrix(call, gu, "gu", (torch.bfloat16,), 2 * I)
-    codes = call.empty((R, I), torch.int8) if codes is None else codes
-    scales = call.empty((R,), torch.float32) if scales is None else scales
+    codes, cp, scales, sp = _codes(call, codes, scales, R, I)
     call.run("moe_swiglu_int8", gp, gs, call.vector(row_weight, "row_weight", torch.float32, R), R, I,
-             call.vector(num_rows, "num_rows", torch.int32, 1), call.need(codes, "codes", torch.int8, (R, I)),
-             call.need(scales, "scales", torch.float32, (R,)))
+             call.vector(num_rows, "num_rows", torch.int32, 1), cp, sp)
     return codes, scales
 
 
@@ -932,7 +954,8 @@ def grouped_gemm_int8(a: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor, o
         out_type = _out_type(out.dtype, "out")
     else:
         raise ValueError("out must be a GPU tensor")
-    ws, need, scale = None, 0, None
+    ws = ws_ptr = scale = None
+    need = 0
     if a.dtype is torch.int8:
         if a_scale is None:
             raise ValueError("int8 rows need a_scale")
@@ -942,9 +965,11 @@ def grouped_gemm_int8(a: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor, o
     src = call.rows(a, "input", torch.int8 if a.dtype is torch.int8 else torch.bfloat16, K, a_rows, a_div, R)
     if scale is None:
         need = (_lib or load()).moe_grouped_int8_workspace_size(R, E, N, K, rows)
-        ws = _empty((need,), torch.uint8, call.index, stream, scratch=True) if need else None
+        if need:
+            ws = _empty((need,), torch.uint8, call.index, stream, scratch=True)
+            ws_ptr = ws.data_ptr()
     call.run("moe_grouped_gemm_int8", ctypes.byref(_GroupedInt8Args(
         R, E, N, K, off, src, scale, call.need(w, "w", torch.int8, (E, N, K)),
         call.need(w_scale, "w_scale", torch.float32, (E, N)), call.rows(out, "out", out.dtype, N, out_rows, 1, R),
-        out_type, _ptr(ws), need)))
+        out_type, ws_ptr, need)))
     return out
