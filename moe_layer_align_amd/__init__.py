@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import importlib
 import os
 from typing import Optional, Sequence
 
@@ -89,36 +90,6 @@ class _GroupedWgradArgs(ctypes.Structure):  # moe_grouped_wgrad_args_t
                 ("out_type", ctypes.c_int32), ("accumulate", ctypes.c_int32)]
 
 
-class _DispatchArgs(ctypes.Structure):  # moe_dispatch_args_t
-    _fields_ = [("M", ctypes.c_int32), ("top_k", ctypes.c_int32), ("E", ctypes.c_int32),
-                ("first_expert", ctypes.c_int32), ("ids", ctypes.c_void_p), ("x", ctypes.c_void_p),
-                ("x_stride", ctypes.c_int64), ("row_bytes", ctypes.c_int32), ("rows", ctypes.c_void_p),
-                ("rows_stride", ctypes.c_int64), ("offsets", ctypes.c_void_p), ("positions", ctypes.c_void_p),
-                ("pairs", ctypes.c_void_p), ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t)]
-
-
-class _CombineArgs(ctypes.Structure):  # moe_combine_args_t
-    _fields_ = [("M", ctypes.c_int32), ("top_k", ctypes.c_int32), ("H", ctypes.c_int32), ("R", ctypes.c_int32),
-                ("rows", ctypes.c_void_p), ("rows_stride", ctypes.c_int64), ("rows_type", ctypes.c_int32),
-                ("positions", ctypes.c_void_p), ("weights", ctypes.c_void_p), ("y", ctypes.c_void_p),
-                ("y_stride", ctypes.c_int64), ("y_type", ctypes.c_int32)]
-
-
-class _CombineGradArgs(ctypes.Structure):  # moe_combine_grad_args_t
-    _fields_ = [("M", ctypes.c_int32), ("top_k", ctypes.c_int32), ("H", ctypes.c_int32), ("R", ctypes.c_int32),
-                ("dy", ctypes.c_void_p), ("dy_stride", ctypes.c_int64), ("dy_type", ctypes.c_int32),
-                ("rows", ctypes.c_void_p), ("rows_stride", ctypes.c_int64), ("rows_type", ctypes.c_int32),
-                ("positions", ctypes.c_void_p), ("weights", ctypes.c_void_p), ("drows", ctypes.c_void_p),
-                ("drows_stride", ctypes.c_int64), ("drows_type", ctypes.c_int32), ("dweights", ctypes.c_void_p)]
-
-
-class _GroupedInt8Args(ctypes.Structure):  # moe_grouped_int8_args_t
-    _fields_ = [("R", ctypes.c_int32), ("E", ctypes.c_int32), ("N", ctypes.c_int32), ("K", ctypes.c_int32),
-                ("offsets", ctypes.c_void_p), ("in_", _Rows), ("in_scale", ctypes.c_void_p), ("w", ctypes.c_void_p),
-                ("w_scale", ctypes.c_void_p), ("out", _Rows), ("out_type", ctypes.c_int32),
-                ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t)]
-
-
 _lib = None
 _ABI = 15  # moe_abi_version() of the library whose moe_fused_args_t _FusedArgs mirrors
 
@@ -169,22 +140,8 @@ def load():
     lib.moe_swiglu_checkpoint_grad.argtypes = [vp, vp, vp, vp, i32, i32, vp, vp, vp, vp, vp]
     lib.moe_dispatch_workspace_size.restype = sz
     lib.moe_dispatch_workspace_size.argtypes = [i32, i32, i32]
-    lib.moe_dispatch.restype = ctypes.c_int
-    lib.moe_dispatch.argtypes = [ctypes.POINTER(_DispatchArgs), vp]
-    lib.moe_combine.restype = ctypes.c_int
-    lib.moe_combine.argtypes = [ctypes.POINTER(_CombineArgs), vp]
-    lib.moe_combine_grad.restype = ctypes.c_int
-    lib.moe_combine_grad.argtypes = [ctypes.POINTER(_CombineGradArgs), vp]
-    lib.moe_route_topk_grad.restype = ctypes.c_int
-    lib.moe_route_topk_grad.argtypes = [vp, vp, vp, i32, i32, i32, vp, vp]
-    lib.moe_quant_int8.restype = ctypes.c_int
-    lib.moe_quant_int8.argtypes = [vp, i64, i32, i32, vp, vp, vp]
-    lib.moe_swiglu_int8.restype = ctypes.c_int
-    lib.moe_swiglu_int8.argtypes = [vp, i64, vp, i32, i32, vp, vp, vp, vp]
     lib.moe_grouped_int8_workspace_size.restype = sz
     lib.moe_grouped_int8_workspace_size.argtypes = [i32] * 5
-    lib.moe_grouped_gemm_int8.restype = ctypes.c_int
-    lib.moe_grouped_gemm_int8.argtypes = [ctypes.POINTER(_GroupedInt8Args), vp]
     if lib.moe_abi_version() != _ABI:
         raise RuntimeError("libmoe_mi355x.so has ABI version %d, this binding expects %d: rebuild it"
                            % (lib.moe_abi_version(), _ABI))
@@ -720,32 +677,23 @@ def swiglu_checkpoint_grad(codes: torch.Tensor, scales: torch.Tensor, dh: torch.
 
 
 # ------------------------------------------------------------------ the tokens' way to their experts and back
-def _matrix(call, t, name, dtypes, width, rows=None):
-    """(pointer, stride) of a [rows, width] operand whose rows may be strided;
-    rows None: any number."""
-    if not isinstance(t, torch.Tensor) or t.get_device() != call.index:
-        raise ValueError("%s must be a tensor on cuda:%d" % (name, call.index))
-    if t.dtype not in dtypes:
-        raise TypeError("%s must be %s, got %s" % (name, " or ".join(map(str, dtypes)), t.dtype))
-    shape, step = t.shape, t.stride()
-    if len(shape) != 2 or shape[1] != width or (rows is not None and shape[0] != rows):
-        raise ValueError("%s must have shape (%s, %d), got %s" % (name, "rows" if rows is None else rows, width,
-                                                                  tuple(shape)))
-    if step[1] != 1 and width > 1:
-        raise ValueError("%s's rows must be contiguous" % name)
-    if shape[0] >> 31 or width >> 31:
-        _sizes(shape[0] | width)
-    # one row has no stride of its own, no row at all no address
-    return t.data_ptr() or 16, step[0] if shape[0] > 1 else width
+_native = None
 
 
-def _made(call, rows, width, dtype):
-    """A [rows, width] result made here: (tensor, pointer, stride)."""
-    t = call.empty((rows, width), dtype)
-    return t, t.data_ptr() or 16, width
-
-
-_ROW_TYPES = (torch.bfloat16, torch.float32)
+def _compiled():
+    """The compiled part of the binding (csrc/calls.cpp), which checks and makes
+    the calls below: in Python their steps took longer than the GPU does."""
+    global _native
+    if _native is None:
+        load()
+        try:
+            native = importlib.import_module("._calls", __name__)
+        except ImportError as e:
+            raise RuntimeError("the binding's compiled part is not built (run `python -c 'import __graft_entry__ as g; "
+                               "g.build()'`)") from e
+        native.init(_stream, _empty, MoEError, torch._C._cuda_getCurrentRawStream)
+        _native = native
+    return _native
 
 
 def dispatch(x: torch.Tensor, ids: torch.Tensor, E: int, out: Optional[torch.Tensor] = None, *, first_expert: int = 0,
@@ -760,32 +708,7 @@ def dispatch(x: torch.Tensor, ids: torch.Tensor, E: int, out: Optional[torch.Ten
     the grouped products take them), pair (t,j) is row positions[t,j] (-1: left
     out), row i is pair pairs[i] = t*top_k + j (-1 behind the last expert's, where
     rows are not written)."""
-    call = _Call(x, stream)
-    if x.dim() != 2 or x.element_size() not in (1, 2, 4) or x.is_complex():
-        raise ValueError("x must be a [tokens, H] tensor of a type of 1, 2 or 4 bytes")
-    if not isinstance(ids, torch.Tensor) or ids.dim() != 2:
-        raise ValueError("ids must have shape (tokens, top_k)")
-    (M, H), k, size = x.shape, ids.shape[1], x.element_size()
-    P = M * k
-    _sizes(M | k | E | P | H * size)
-    _sizes(first_expert)
-    xp, xs = _matrix(call, x, "x", (x.dtype,), H, M)
-    ip = call.need(ids, "ids", torch.int32, (M, k))
-    if out is None:
-        out, op, os_ = _made(call, P, H, x.dtype)
-    else:
-        op, os_ = _matrix(call, out, "out", (x.dtype,), H, P)
-    # one allocation for the three: 1.5 us less
-    n = max(E, 0) + 1
-    ints = call.empty((n + 2 * P,), torch.int32)
-    offsets, positions, pairs = (ints.as_strided((n,), (1,), 0), ints.as_strided((M, k), (k, 1), n),
-                                 ints.as_strided((P,), (1,), n + P))
-    need = (_lib or load()).moe_dispatch_workspace_size(M, k, E)
-    ws = _empty((need,), torch.uint8, call.index, stream, scratch=True) if need else None
-    call.run("moe_dispatch", ctypes.byref(_DispatchArgs(
-        M, k, E, first_expert, ip, xp, xs * size, H * size, op, os_ * size, offsets.data_ptr(), positions.data_ptr(),
-        pairs.data_ptr(), _ptr(ws), need)))
-    return out, offsets, positions, pairs
+    return (_native or _compiled()).dispatch(x, ids, E, out, first_expert, stream)
 
 
 def combine(rows: torch.Tensor, positions: torch.Tensor, weights: Optional[torch.Tensor] = None,
@@ -795,23 +718,7 @@ def combine(rows: torch.Tensor, positions: torch.Tensor, weights: Optional[torch
     dispatch's, slots outside [0,R) left out; weights fp32 [M,top_k] or None
     (ones: the gradient of dispatch).  out bf16 or fp32 [M,H], made here as
     out_dtype (rows' type by default) when not given."""
-    call = _Call(rows, stream)
-    if rows.dim() != 2 or not isinstance(positions, torch.Tensor) or positions.dim() != 2:
-        raise ValueError("rows must be a [rows, H] tensor and positions [tokens, top_k]")
-    (R, H), (M, k) = rows.shape, positions.shape
-    _sizes(R | H | M | k | M * k)
-    rp, rs = _matrix(call, rows, "rows", _ROW_TYPES, H)
-    if out is None:
-        dtype = rows.dtype if out_dtype is None else out_dtype
-        _out_type(dtype, "out_dtype")
-        out, yp, ys = _made(call, M, H, dtype)
-    else:
-        yp, ys = _matrix(call, out, "out", _ROW_TYPES, H, M)
-    call.run("moe_combine", ctypes.byref(_CombineArgs(
-        M, k, H, R, rp, rs, _OUT_TYPE[rows.dtype], call.need(positions, "positions", torch.int32, (M, k)),
-        None if weights is None else call.need(weights, "weights", torch.float32, (M, k)), yp, ys,
-        _OUT_TYPE[out.dtype])))
-    return out
+    return (_native or _compiled()).combine(rows, positions, weights, out, out_dtype, stream)
 
 
 def combine_grad(dy: torch.Tensor, rows: Optional[torch.Tensor], positions: torch.Tensor,
@@ -823,89 +730,24 @@ def combine_grad(dy: torch.Tensor, rows: Optional[torch.Tensor], positions: torc
     (rows that no position names are not written; made here as out_dtype, bf16 or
     fp32, when not given) and dweights[t,j] = dy[t] . rows[positions[t,j]].  rows
     None: no dweights, num_rows (default M*top_k) rows of drows."""
-    call = _Call(dy, stream)
-    if dy.dim() != 2 or not isinstance(positions, torch.Tensor) or positions.dim() != 2:
-        raise ValueError("dy must be a [tokens, H] tensor and positions [tokens, top_k]")
-    (M, H), k = dy.shape, positions.shape[1]
-    if rows is not None:
-        if not isinstance(rows, torch.Tensor) or rows.dim() != 2:
-            raise ValueError("rows must be a [rows, H] tensor")
-        if num_rows is not None and num_rows != rows.shape[0]:
-            raise ValueError("num_rows is %d, rows has %d" % (num_rows, rows.shape[0]))
-        R = rows.shape[0]
-    else:
-        if dweights is not None:
-            raise ValueError("dweights needs rows")
-        R = M * k if num_rows is None else num_rows
-    _sizes(R | H | M | k | M * k)
-    dp, ds = _matrix(call, dy, "dy", _ROW_TYPES, H)
-    rp, rs = (None, H) if rows is None else _matrix(call, rows, "rows", _ROW_TYPES, H)
-    if drows is None:
-        _out_type(out_dtype, "out_dtype")
-        drows, op, os_ = _made(call, R, H, out_dtype)
-    else:
-        op, os_ = _matrix(call, drows, "drows", _ROW_TYPES, H, R)
-    wp = None
-    if dweights is not None:
-        wp = call.need(dweights, "dweights", torch.float32, (M, k))
-    elif rows is not None:
-        dweights = call.empty((M, k), torch.float32)
-        wp = dweights.data_ptr()
-    call.run("moe_combine_grad", ctypes.byref(_CombineGradArgs(
-        M, k, H, R, dp, ds, _OUT_TYPE[dy.dtype], rp, rs, 0 if rows is None else _OUT_TYPE[rows.dtype],
-        call.need(positions, "positions", torch.int32, (M, k)),
-        None if weights is None else call.need(weights, "weights", torch.float32, (M, k)), op, os_,
-        _OUT_TYPE[drows.dtype], wp)))
-    return drows, dweights
+    return (_native or _compiled()).combine_grad(dy, rows, positions, weights, drows, dweights, num_rows, out_dtype,
+                                                 stream)
 
 
 def route_topk_grad(ids: torch.Tensor, weights: torch.Tensor, dweights: torch.Tensor, E: int,
                     out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """Gradient of route_topk's weights to its logits, fp32 [M,E]
     (moe_route_topk_grad): ids int32, weights and dweights fp32 [M,top_k]."""
-    call = _Call(ids, stream)
-    if ids.dim() != 2:
-        raise ValueError("ids must have shape (tokens, top_k)")
-    M, k = ids.shape
-    _sizes(M | k | E)
-    if out is None:
-        out, op, _ = _made(call, M, max(E, 0), torch.float32)
-    else:
-        op = call.need(out, "out", torch.float32, (M, E))
-    call.run("moe_route_topk_grad", call.need(ids, "ids", torch.int32, (M, k)),
-             call.need(weights, "weights", torch.float32, (M, k)),
-             call.need(dweights, "dweights", torch.float32, (M, k)), M, E, k, op)
-    return out
+    return (_native or _compiled()).route_topk_grad(ids, weights, dweights, E, out, stream)
 
 
 # ------------------------------------------------------------------ 8-bit integers
-def _codes(call, codes, scales, rows, width):
-    """The codes and scales of [rows, width], given or made here, and their pointers."""
-    if codes is None:
-        codes = call.empty((rows, width), torch.int8)
-        cp = codes.data_ptr()
-    else:
-        cp = call.need(codes, "codes", torch.int8, (rows, width))
-    if scales is None:
-        scales = call.empty((rows,), torch.float32)
-        return codes, cp, scales, scales.data_ptr()
-    return codes, cp, scales, call.need(scales, "scales", torch.float32, (rows,))
-
-
 def quant_int8(x: torch.Tensor, codes: Optional[torch.Tensor] = None, scales: Optional[torch.Tensor] = None,
                stream=None):
     """Rows of x bf16 [M,K] (may be strided) as 8-bit integers (moe_quant_int8):
     returns (codes int8 [M,K], scales fp32 [M]), scales = max|row|/127, codes =
     row/scale to the nearest, ties to even.  Lays out weights too: w.view(E*N, K)."""
-    call = _Call(x, stream)
-    if x.dim() != 2:
-        raise ValueError("x must have shape (rows, K), got %s" % (tuple(x.shape),))
-    M, K = x.shape
-    _sizes(M | K)
-    xp, xs = _matrix(call, x, "x", (torch.bfloat16,), K)
-    codes, cp, scales, sp = _codes(call, codes, scales, M, K)
-    call.run("moe_quant_int8", xp, xs, M, K, cp, sp)
-    return codes, scales
+    return (_native or _compiled()).quant_int8(x, codes, scales, stream)
 
 
 def swiglu_int8(gu: torch.Tensor, row_weight: Optional[torch.Tensor] = None, *,
@@ -915,16 +757,7 @@ def swiglu_int8(gu: torch.Tensor, row_weight: Optional[torch.Tensor] = None, *,
     strided) as 8-bit integers (moe_swiglu_int8): returns (codes int8 [R,I],
     scales fp32 [R]), the scales multiplied by row_weight fp32 [R].  num_rows int32
     [1] on the GPU (offsets[E:]): rows at or beyond it are left alone."""
-    call = _Call(gu, stream)
-    if gu.dim() != 2 or gu.shape[1] % 2:
-        raise ValueError("gu must have shape (rows, 2*I), got %s" % (tuple(gu.shape),))
-    R, I = gu.shape[0], gu.shape[1] // 2
-    _sizes(R | I)
-    gp, gs = _matrix(call, gu, "gu", (torch.bfloat16,), 2 * I)
-    codes, cp, scales, sp = _codes(call, codes, scales, R, I)
-    call.run("moe_swiglu_int8", gp, gs, call.vector(row_weight, "row_weight", torch.float32, R), R, I,
-             call.vector(num_rows, "num_rows", torch.int32, 1), cp, sp)
-    return codes, scales
+    return (_native or _compiled()).swiglu_int8(gu, row_weight, num_rows, codes, scales, stream)
 
 
 def grouped_gemm_int8(a: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor, offsets: torch.Tensor,
@@ -937,39 +770,5 @@ def grouped_gemm_int8(a: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor, o
     a int8 [rows,K] with a_scale fp32 [rows], quant_int8's or swiglu_int8's; or
     bf16 [rows,K] without a_scale: the call quantises its rows itself.  w int8
     [E,N,K], w_scale fp32 [E,N]; the rest as in grouped_gemm."""
-    call = _Call(a, stream)
-    if not isinstance(w, torch.Tensor) or w.dim() != 3:
-        raise ValueError("the weights must be a tensor [E, N, K]")
-    if a.dim() != 2:
-        raise ValueError("input must be a [rows, K] tensor")
-    E, N, K = w.shape
-    rows = a.shape[0]
-    R = rows if a_rows is None else a_rows.numel()
-    _sizes(R | E | N | K | a_div)
-    off = call.need(offsets, "offsets", torch.int32, (E + 1,))
-    if out is None:
-        out_type = _out_type(out_dtype, "out_dtype")
-        out = call.empty((R, N), out_dtype)
-    elif isinstance(out, torch.Tensor):
-        out_type = _out_type(out.dtype, "out")
-    else:
-        raise ValueError("out must be a GPU tensor")
-    ws = ws_ptr = scale = None
-    need = 0
-    if a.dtype is torch.int8:
-        if a_scale is None:
-            raise ValueError("int8 rows need a_scale")
-        scale = call.need(a_scale, "a_scale", torch.float32, (rows,)) or 16
-    elif a_scale is not None:
-        raise ValueError("a_scale goes with int8 rows")
-    src = call.rows(a, "input", torch.int8 if a.dtype is torch.int8 else torch.bfloat16, K, a_rows, a_div, R)
-    if scale is None:
-        need = (_lib or load()).moe_grouped_int8_workspace_size(R, E, N, K, rows)
-        if need:
-            ws = _empty((need,), torch.uint8, call.index, stream, scratch=True)
-            ws_ptr = ws.data_ptr()
-    call.run("moe_grouped_gemm_int8", ctypes.byref(_GroupedInt8Args(
-        R, E, N, K, off, src, scale, call.need(w, "w", torch.int8, (E, N, K)),
-        call.need(w_scale, "w_scale", torch.float32, (E, N)), call.rows(out, "out", out.dtype, N, out_rows, 1, R),
-        out_type, ws_ptr, need)))
-    return out
+    return (_native or _compiled()).grouped_gemm_int8(a, w, w_scale, offsets, out, a_scale, a_rows, a_div, out_rows,
+                                                   out_dtype, stream)

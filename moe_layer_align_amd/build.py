@@ -1,5 +1,6 @@
-"""Ahead-of-time build of the gfx950 HIP libraries: the layer
-(libmoe_mi355x.so) and the measurement probes (libmoe_probes.so).
+"""Ahead-of-time build of the gfx950 HIP libraries, the layer
+(libmoe_mi355x.so) and the measurement probes (libmoe_probes.so), and of the
+compiled part of the Python binding (_calls.so).
 
 Compiles the translation units under moe_layer_align_amd/csrc with hipcc for
 gfx950, in parallel, and links them into the package directory.  Every unit
@@ -12,6 +13,7 @@ from __future__ import annotations
 import os
 import subprocess
 import sys
+import sysconfig
 import tempfile
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -23,7 +25,9 @@ UNITS = ["moe_api.hip", "launch_decode_bf16.hip", "launch_decode_fp8.hip", "laun
 LIB = os.path.join(PKG, "libmoe_mi355x.so")
 PROBE_UNITS = ["probes.hip"]
 PROBE_LIB = os.path.join(PKG, "libmoe_probes.so")
+CALLS = os.path.join(PKG, "_calls.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
+CXX = os.environ.get("CXX", "g++")
 
 FLAGS = [
     "--offload-arch=gfx950",
@@ -77,15 +81,50 @@ def _compile_link(units, lib, inc, verbose, extra, tmpdir, tag):
     return finish
 
 
+def _binding(verbose, tmpdir):
+    """Start the compile of csrc/calls.cpp; returns a function that waits for it
+    and links it to the layer library and torch."""
+    import torch
+    from torch.utils.cpp_extension import include_paths
+    obj = os.path.join(tmpdir, "calls.o")
+    cmd = [CXX, "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-Wall",
+           "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI, "-I", os.path.join(ROOT, "include")]
+    for path in include_paths() + [sysconfig.get_paths()["include"]]:
+        cmd += ["-isystem", path]
+    cmd += ["-c", os.path.join(CSRC, "calls.cpp"), "-o", obj]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    proc = subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
+
+    def finish():
+        out, _ = proc.communicate()
+        if proc.returncode == 0:
+            tmp = CALLS + ".tmp%d" % os.getpid()
+            # the layer library lies beside it; torch's are loaded before it is
+            link = [CXX, "-shared", obj, "-o", tmp, "-L", os.path.join(os.path.dirname(torch.__file__), "lib"),
+                    "-ltorch_python", "-ltorch_cpu", "-lc10", "-L", PKG, "-l:" + os.path.basename(LIB),
+                    "-Wl,-rpath,$ORIGIN"]
+            res = subprocess.run(link, capture_output=True, text=True)
+            if res.returncode == 0:
+                os.replace(tmp, CALLS)
+                return
+            out = res.stdout + res.stderr
+        sys.stderr.write(out + "\n")
+        raise RuntimeError("the build of the binding's compiled part failed")
+    return finish
+
+
 def build(verbose: bool = False, extra=()) -> str:
-    """Build both libraries (all units compile in parallel); returns the
-    layer library's path."""
+    """Build both libraries (all units compile in parallel) and the binding's
+    compiled part; returns the layer library's path."""
     inc = ["-I", os.path.join(ROOT, "include"), "-I", CSRC]
     with tempfile.TemporaryDirectory(prefix="moe_build_") as tmpdir:
         layer = _compile_link(UNITS, LIB, inc, verbose, extra, tmpdir, "layer")
         probes = _compile_link(PROBE_UNITS, PROBE_LIB, inc, verbose, extra, tmpdir, "probes")
+        calls = _binding(verbose, tmpdir)
         layer()
         probes()
+        calls()
     return LIB
 
 
