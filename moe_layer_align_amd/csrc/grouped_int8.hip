@@ -26,13 +26,15 @@ namespace moe {
 namespace {
 
 constexpr int kStep = 128;  // K per step
+constexpr int kFull = 1024;  // workgroups that fill the CUs, two on each, with some to spare
 // bf16 rows become codes inside the product, which saves a launch and its codes'
 // way through memory, where the weights that may be read are fewer bytes than this
-// and the rows few: one token, top-2 of 8 experts of 4096 x 2048 12.0 us a call
-// against 16.5 in two launches; from 200 MB on there is nothing between the two
-// (one token, 28672 x 4096 49.0 and 48.8).
+// and the rows few, a call of one launch and of two (us): one token, top-2 of 8
+// experts of 1024 x 1024 5.5 and 8.5, 14336 x 4096 24.2 and 26.3; 4 tokens, top-8
+// of 128 of 1536 x 2048 21.5 and 20.5; one token, 28672 x 4096 50.5 and 50.5.
+// Every band converts the rows anew: 125 rows per expert, 1024 x 1024, 35.6 and 12.9.
 constexpr int64_t kOneLaunchBytes = (int64_t)1 << 27;
-constexpr int kOneLaunchRows = 8;  // per expert, on average
+constexpr int kOneLaunchRows = 4;  // per expert, on average
 
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) int lds_i32;
@@ -273,7 +275,8 @@ __device__ __forceinline__ void pass(const GroupedInt8Args& a, int e, int n0, in
 }
 
 // An expert's rows in passes of 64, the last ones in one of 16 or 32 where that
-// holds them: the weights are streamed once per pass.  bf16 rows take passes of
+// holds them: the weights are streamed once per pass, and the workgroups of a
+// band (blockIdx.z) take its passes in turn.  bf16 rows take passes of
 // at most 32 (their conversion costs as much per row as the stream of the weights).
 template <bool BF16, bool F32, int FT>
 __global__ __launch_bounds__(256, 2) void grouped_int8_kernel(GroupedInt8Args a) {
@@ -284,7 +287,8 @@ __global__ __launch_bounds__(256, 2) void grouped_int8_kernel(GroupedInt8Args a)
   const Found f = find_expert(a.offsets, a.R, a.E);
   if (f.e >= a.E) return;
   const int n0 = blockIdx.x * kBand;
-  for (int i0 = f.lo; i0 < f.hi; i0 += 16 * kMost) {
+  const int step = gridDim.z * (16 * kMost);
+  for (int i0 = f.lo + blockIdx.z * (16 * kMost); i0 < f.hi; i0 += step) {
     const int n = f.hi - i0;
     if (n <= 16)
       pass<BF16, F32, FT, 1>(a, f.e, n0, i0, f.hi, (lds_u8*)smem, (lds_u32*)top);
@@ -297,8 +301,12 @@ __global__ __launch_bounds__(256, 2) void grouped_int8_kernel(GroupedInt8Args a)
 
 template <bool BF16, bool F32, int FT>
 void launch(hipStream_t st, const GroupedInt8Args& a) {
-  constexpr int kBand = 16 * FT;
-  grouped_int8_kernel<BF16, F32, FT><<<dim3((a.N + kBand - 1) / kBand, a.R < a.E ? a.R : a.E), 256, 0, st>>>(a);
+  constexpr int kBand = 16 * FT, kRows = BF16 ? 32 : 64;
+  const int bands = (a.N + kBand - 1) / kBand, experts = a.R < a.E ? a.R : a.E, passes = (a.R + kRows - 1) / kRows;
+  // few bands: passes side by side, until the CUs are full
+  const int64_t blocks = (int64_t)bands * experts;
+  const int side = blocks >= kFull ? 1 : (int)((kFull + blocks - 1) / blocks);
+  grouped_int8_kernel<BF16, F32, FT><<<dim3(bands, experts, side < passes ? side : passes), 256, 0, st>>>(a);
 }
 
 template <bool BF16, bool F32>
@@ -310,8 +318,15 @@ void pick(hipStream_t st, const GroupedInt8Args& a) {
     launch<BF16, F32, 4>(st, a);
 }
 
-// Streamed or tiled, by the rows per expert on average (streamed and tiled, us).
-// The stream has less to start and end: 402 MB of 128 experts of 1536 x 2048 with 2
+// Whether the passes over the bands are few: then each takes a workgroup of its
+// own, all at once, where few tiles of 256 x 256 would leave most CUs idle
+// (streamed and tiled, us): 66 passes over 5 experts of 184 x 7744 16.8 and 67.0;
+// 384 of 1024 x 4096 23.5 and 39.7, 640 39.9 and 41.1; 640 of 1024 x 1024 14.7 and
+// 19.3, 1136 25.4 and 20.3.
+bool few(int R, int E, int64_t N) { return (R / 64 + (int64_t)(R < E ? R : E)) * ((N + 63) / 64) <= 640; }
+
+// Streamed or tiled otherwise, by the rows per expert on average (the same).  The
+// stream has less to start and end: 402 MB of 128 experts of 1536 x 2048 with 2
 // rows 60.6 and 74.6, 8 76.5 and 83.5, 16 78.7 and 87.3, 64 112.9 and 102.0; 268
 // MB of 16 experts with 16 55.6 and 68.1.  It streams an expert's weights once per
 // 64 rows, which costs where a few experts hold most rows, the more so the more
@@ -320,7 +335,7 @@ void pick(hipStream_t st, const GroupedInt8Args& a) {
 // rows take as long in either form (2 rows 523.4 and 525.7, 16 718.6 and 719.4).
 bool streamed(int R, int E, int64_t N, int64_t K) {
   const int rows = (R < E ? R : E) * N * K < ((int64_t)1 << 30) ? 16 : 4;
-  return R <= rows * (int64_t)E;
+  return R <= rows * (int64_t)E || few(R, E, N);
 }
 
 }  // namespace

@@ -205,6 +205,23 @@ def test_product_steps(name, K):
     run_product(COUNTS[name], 2056, K, True, True, torch.float32)
 
 
+@pytest.mark.parametrize("name", ["edges_64", "edges_128", "edges_256", "skewed"])
+@pytest.mark.parametrize("K", [16, 80, 208])
+@pytest.mark.parametrize("gather,scatter,dtype", [(False, False, torch.bfloat16), (True, False, torch.float32),
+                                                  (True, True, torch.bfloat16), (False, True, torch.float32)])
+def test_tiles(name, K, gather, scatter, dtype):
+    # wide results, whose tiles fill the GPU: the tiled form at its tiles' borders
+    run_product(COUNTS[name], 8200, K, gather, scatter, dtype)
+
+
+@pytest.mark.parametrize("counts", [[300], [64, 65, 0, 129], [1000, 1]])
+@pytest.mark.parametrize("N,K", [(24, 144), (184, 3888), (520, 272)])
+def test_passes_side_by_side(counts, N, K):
+    # narrow results of many rows: the passes of a band on workgroups of their own
+    run_product(counts, N, K, True, True, torch.bfloat16)
+    run_product(counts, N, K, False, False, torch.float32)
+
+
 MANY = {  # several tiles of each kind for every workgroup
     "whole": [2100, 700, 0, 2900, 1500],
     "halves": [70 + i % 59 for i in range(40)],
