@@ -579,7 +579,8 @@ moe_status_t moe_swiglu_checkpoint_grad(const uint8_t* codes, const uint8_t* sca
  *   positions [M,top_k]  the pair's row, -1 for a pair left out
  *   pairs     [M*top_k]  the row's pair, -1 for rows at or beyond offsets[E]
  *   rows      row positions[t,j] = row t of x, byte for byte; rows at or beyond
- *             offsets[E] are not written
+ *             offsets[E] are not written.  x and rows both NULL: the layout
+ *             alone, for products that gather the tokens themselves
  * An expert's rows are in the order of their pairs.  The ids of a token may be
  * equal.  The gradient of x is moe_combine of the rows' gradients without
  * weights.
@@ -589,7 +590,7 @@ moe_status_t moe_swiglu_checkpoint_grad(const uint8_t* codes, const uint8_t* sca
 typedef struct {
   int32_t M, top_k, E, first_expert;
   const int32_t* ids;  /* [M,top_k] */
-  const void* x;       /* [M] rows of row_bytes */
+  const void* x;       /* [M] rows of row_bytes, or NULL */
   int64_t x_stride;    /* bytes */
   int32_t row_bytes;
   void* rows;          /* [M*top_k] rows of row_bytes */

@@ -1,6 +1,7 @@
 """MI355X (gfx950) fused Mixture-of-Experts layer.
 
-Thin ctypes binding over libmoe_mi355x.so, the C ABI in include/moe.h.  The
+Thin binding over libmoe_mi355x.so, the C ABI in include/moe.h, by ctypes and,
+for the calls whose time is the host's, in C++ (csrc/calls.cpp).  The
 functions here only check tensor shapes/dtypes/devices and marshal pointers;
 every step of the layer runs in the library's HIP kernels.  PyTorch provides
 device memory and the current stream.  There is no fallback: if the library
@@ -696,7 +697,7 @@ def _compiled():
     return _native
 
 
-def dispatch(x: torch.Tensor, ids: torch.Tensor, E: int, out: Optional[torch.Tensor] = None, *, first_expert: int = 0,
+def dispatch(x: Optional[torch.Tensor], ids: torch.Tensor, E: int, out: Optional[torch.Tensor] = None, *, first_expert: int = 0,
              stream=None):
     """The tokens' rows copied to rows grouped by expert (moe_dispatch).
 
@@ -707,7 +708,8 @@ def dispatch(x: torch.Tensor, ids: torch.Tensor, E: int, out: Optional[torch.Ten
     pairs int32 [M*top_k]): expert e's rows are offsets[e] <= i < offsets[e+1] (as
     the grouped products take them), pair (t,j) is row positions[t,j] (-1: left
     out), row i is pair pairs[i] = t*top_k + j (-1 behind the last expert's, where
-    rows are not written)."""
+    rows are not written).  x None: no rows (None in their place), for products
+    that gather the tokens themselves (a_rows=pairs, a_div=top_k)."""
     return (_native or _compiled()).dispatch(x, ids, E, out, first_expert, stream)
 
 

@@ -173,6 +173,11 @@ struct Call {
   }
 };
 
+PyObject* wrap(const Tensor& t) {
+  if (!t.defined()) Py_RETURN_NONE;
+  return THPVariable_Wrap(t);
+}
+
 PyObject* tuple(std::initializer_list<PyObject*> items) {  // takes the references
   PyObject* t = PyTuple_New((Py_ssize_t)items.size());
   Py_ssize_t i = 0;
@@ -193,33 +198,40 @@ const std::initializer_list<ScalarType> kRowTypes = {ScalarType::BFloat16, Scala
 PyObject* dispatch(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   want(n, 6);
-  const Tensor &x = tensor(a[0], "x"), &ids = tensor(a[1], "ids");
-  const int64_t esz = x.element_size();
-  TORCH_CHECK_VALUE(x.dim() == 2 && (esz == 1 || esz == 2 || esz == 4) && !x.is_complex(),
-                    "x must be a [tokens, H] tensor of a type of 1, 2 or 4 bytes");
+  const Tensor& ids = tensor(a[1], "ids");
   TORCH_CHECK_VALUE(ids.dim() == 2, "ids must have shape (tokens, top_k)");
   moe_dispatch_args_t d = {};
-  d.M = size32(x.size(0));
+  d.M = size32(ids.size(0));
   d.top_k = size32(ids.size(1));
   d.E = integer(a[2], "E");
   d.first_expert = integer(a[4], "first_expert");
-  d.row_bytes = size32(x.size(1) * esz);
-  const int64_t P = size32((int64_t)d.M * d.top_k), H = x.size(1);
-  Call call(x, a[5]);
-  const Matrix xm = call.matrix(x, "x", {x.scalar_type()}, H, d.M);
-  d.x = xm.p;
-  d.x_stride = xm.stride * esz;
+  const int64_t P = size32((int64_t)d.M * d.top_k);
+  Call call(ids, a[5]);
   d.ids = (const int32_t*)call.need(ids, "ids", ScalarType::Int, {d.M, d.top_k});
-  Tensor out;
-  if (a[3] != Py_None) {
-    out = tensor(a[3], "out");
-    call.matrix(out, "out", {x.scalar_type()}, H, P);
+  const bool copy = a[0] != Py_None;
+  TORCH_CHECK_VALUE(copy || a[3] == Py_None, "out needs x");
+  Tensor x, out;
+  if (copy) {
+    x = tensor(a[0], "x");
+    const int64_t esz = x.element_size();
+    TORCH_CHECK_VALUE(x.dim() == 2 && (esz == 1 || esz == 2 || esz == 4) && !x.is_complex(),
+                      "x must be a [tokens, H] tensor of a type of 1, 2 or 4 bytes");
+    d.row_bytes = size32(x.size(1) * esz);
+    const Matrix xm = call.matrix(x, "x", {x.scalar_type()}, x.size(1), d.M);
+    d.x = xm.p;
+    d.x_stride = xm.stride * esz;
+    if (a[3] != Py_None) {
+      out = tensor(a[3], "out");
+      call.matrix(out, "out", {x.scalar_type()}, x.size(1), P);
+    }
   }
   call.begin();
-  if (!out.defined()) out = call.empty({P, H}, x.scalar_type());
-  const Matrix om = Call::place(out);
-  d.rows = om.p;
-  d.rows_stride = om.stride * esz;
+  if (copy) {
+    if (!out.defined()) out = call.empty({P, x.size(1)}, x.scalar_type());
+    const Matrix om = Call::place(out);
+    d.rows = om.p;
+    d.rows_stride = om.stride * x.element_size();
+  }
   const Tensor offsets = call.empty({std::max(d.E, 0) + (int64_t)1}, ScalarType::Int);
   const Tensor positions = call.empty({d.M, d.top_k}, ScalarType::Int), pairs = call.empty({P}, ScalarType::Int);
   d.offsets = (int32_t*)offsets.data_ptr();
@@ -232,8 +244,7 @@ PyObject* dispatch(PyObject*, PyObject* const* a, Py_ssize_t n) {
     d.workspace = workspace.data_ptr();
   }
   call.run("moe_dispatch", [&](void* s) { return moe_dispatch(&d, s); });
-  return tuple({THPVariable_Wrap(out), THPVariable_Wrap(offsets), THPVariable_Wrap(positions),
-                THPVariable_Wrap(pairs)});
+  return tuple({wrap(out), wrap(offsets), wrap(positions), wrap(pairs)});
   END_HANDLE_TH_ERRORS
 }
 
@@ -273,7 +284,7 @@ PyObject* combine(PyObject*, PyObject* const* a, Py_ssize_t n) {
   c.y = om.p;
   c.y_stride = om.stride;
   call.run("moe_combine", [&](void* s) { return moe_combine(&c, s); });
-  return THPVariable_Wrap(out);
+  return wrap(out);
   END_HANDLE_TH_ERRORS
 }
 
@@ -336,8 +347,7 @@ PyObject* combine_grad(PyObject*, PyObject* const* a, Py_ssize_t n) {
     c.dweights = (float*)dweights.data_ptr();
   }
   call.run("moe_combine_grad", [&](void* s) { return moe_combine_grad(&c, s); });
-  if (!dweights.defined()) Py_INCREF(Py_None);
-  return tuple({THPVariable_Wrap(drows), dweights.defined() ? THPVariable_Wrap(dweights) : Py_None});
+  return tuple({wrap(drows), wrap(dweights)});
   END_HANDLE_TH_ERRORS
 }
 
@@ -361,7 +371,7 @@ PyObject* route_topk_grad(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (!out.defined()) out = call.empty({M, std::max(E, 0)}, ScalarType::Float);
   call.run("moe_route_topk_grad",
            [&](void* s) { return moe_route_topk_grad(ip, wp, dp, M, E, k, (float*)out.data_ptr(), s); });
-  return THPVariable_Wrap(out);
+  return wrap(out);
   END_HANDLE_TH_ERRORS
 }
 
@@ -395,7 +405,7 @@ PyObject* quant_int8(PyObject*, PyObject* const* a, Py_ssize_t n) {
   void *cp = codes.data_ptr(), *sp = scales.data_ptr();
   call.run("moe_quant_int8",
            [&](void* s) { return moe_quant_int8(xm.p, xm.stride, M, K, (int8_t*)cp, (float*)sp, s); });
-  return tuple({THPVariable_Wrap(codes), THPVariable_Wrap(scales)});
+  return tuple({wrap(codes), wrap(scales)});
   END_HANDLE_TH_ERRORS
 }
 
@@ -414,7 +424,7 @@ PyObject* swiglu_int8(PyObject*, PyObject* const* a, Py_ssize_t n) {
   void *cp = codes.data_ptr(), *sp = scales.data_ptr();
   call.run("moe_swiglu_int8",
            [&](void* s) { return moe_swiglu_int8(gm.p, gm.stride, wp, R, I, np, (int8_t*)cp, (float*)sp, s); });
-  return tuple({THPVariable_Wrap(codes), THPVariable_Wrap(scales)});
+  return tuple({wrap(codes), wrap(scales)});
   END_HANDLE_TH_ERRORS
 }
 
@@ -476,7 +486,7 @@ PyObject* grouped_gemm_int8(PyObject*, PyObject* const* a, Py_ssize_t n) {
     }
   }
   call.run("moe_grouped_gemm_int8", [&](void* s) { return moe_grouped_gemm_int8(&g, s); });
-  return THPVariable_Wrap(out);
+  return wrap(out);
   END_HANDLE_TH_ERRORS
 }
 

@@ -212,6 +212,7 @@ __global__ __launch_bounds__(kThreads) void dispatch_kernel(DispatchArgs a) {
       if (f >= held) a.pairs[f] = -1;  // the rows behind the last expert's
     }
   }
+  if (!a.rows) return;  // the layout alone
   __syncthreads();
   // the copy, only of tokens with a row here
   const int per_row = a.row_bytes / 16;
@@ -517,8 +518,11 @@ size_t moe_dispatch_workspace_size(int32_t M, int32_t top_k, int32_t E) {
 }
 
 moe_status_t moe_dispatch(const moe_dispatch_args_t* a, void* stream) {
-  if (!a || a->M < 0 || a->E < 1 || a->top_k < 1 || a->first_expert < 0 || a->row_bytes < 1) return MOE_ERR_INVALID_ARG;
-  if (!routed(a->M, a->top_k) || a->E > kMaxExperts || a->row_bytes % 16 || a->row_bytes >= kMaxRowBytes)
+  if (!a || a->M < 0 || a->E < 1 || a->top_k < 1 || a->first_expert < 0) return MOE_ERR_INVALID_ARG;
+  const bool copy = a->x || a->rows;
+  if (copy && a->row_bytes < 1) return MOE_ERR_INVALID_ARG;
+  if (!routed(a->M, a->top_k) || a->E > kMaxExperts ||
+      (copy && (a->row_bytes % 16 || a->row_bytes >= kMaxRowBytes)))
     return MOE_ERR_UNSUPPORTED;
   if (!a->offsets || !aligned(a->offsets, 4)) return MOE_ERR_INVALID_ARG;
   const hipStream_t st = (hipStream_t)stream;
@@ -527,7 +531,7 @@ moe_status_t moe_dispatch(const moe_dispatch_args_t* a, void* stream) {
   d.k = a->top_k;
   d.E = a->E;
   d.first = a->first_expert;
-  d.row_bytes = a->row_bytes;
+  d.row_bytes = copy ? a->row_bytes : 0;
   d.offsets = a->offsets;
   d.group = 1;
   const int P = a->M * a->top_k;
@@ -536,8 +540,8 @@ moe_status_t moe_dispatch(const moe_dispatch_args_t* a, void* stream) {
         !aligned(a->pairs, 4))
       return MOE_ERR_INVALID_ARG;
     moe_status_t rc;
-    if ((rc = check_matrix(a->x, a->x_stride, a->row_bytes, 1)) != MOE_OK) return rc;
-    if ((rc = check_matrix(a->rows, a->rows_stride, a->row_bytes, 1)) != MOE_OK) return rc;
+    if (copy && (rc = check_matrix(a->x, a->x_stride, a->row_bytes, 1)) != MOE_OK) return rc;
+    if (copy && (rc = check_matrix(a->rows, a->rows_stride, a->row_bytes, 1)) != MOE_OK) return rc;
     d.x = (const uint8_t*)a->x;
     d.x_stride = a->x_stride;
     d.ids = a->ids;

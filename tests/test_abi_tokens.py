@@ -61,7 +61,7 @@ DISPATCH = dict(M=10, top_k=2, E=4, first_expert=0, ids=P, x=P, x_stride=128, ro
 
 @pytest.mark.parametrize("kw,code", [
     (dict(M=-1), INVALID), (dict(E=0), INVALID), (dict(top_k=0), INVALID), (dict(first_expert=-1), INVALID),
-    (dict(row_bytes=0), INVALID), (dict(E=513), UNSUPPORTED), (dict(top_k=17), UNSUPPORTED),
+    (dict(row_bytes=0), INVALID), (dict(x=None, rows=None, ids=None), INVALID), (dict(E=513), UNSUPPORTED), (dict(top_k=17), UNSUPPORTED),
     (dict(M=1 << 25), UNSUPPORTED), (dict(row_bytes=24, x_stride=32, rows_stride=32), UNSUPPORTED),
     (dict(row_bytes=1 << 22, x_stride=1 << 22, rows_stride=1 << 22), UNSUPPORTED),
     (dict(x_stride=1 << 22), UNSUPPORTED), (dict(rows_stride=1 << 22), UNSUPPORTED),
@@ -226,8 +226,10 @@ ROWS, X = zeros(12, 32), zeros(6, 32)
     ("out must not be Float", lambda: moe.dispatch(X, IDS, 4, zeros(12, 32, dtype=F32))),
     ("ids must be Int", lambda: moe.dispatch(X, IDS.long(), 4)),
     ("ids must be contiguous", lambda: moe.dispatch(X, zeros(2, 6, dtype=I32).t(), 4)),
-    ("ids must have shape", lambda: moe.dispatch(X[:5], IDS, 4)),
+    ("x must have 32 columns and the rows", lambda: moe.dispatch(X[:5], IDS, 4)),
+    ("out needs x", lambda: moe.dispatch(None, IDS, 4, ROWS)),
     ("ids must be a tensor", lambda: moe.dispatch(X, None, 4)),
+    ("ids must have shape", lambda: moe.dispatch(X, IDS[0], 4)),
     ("1, 2 or 4 bytes", lambda: moe.dispatch(X.double(), IDS, 4)),
     ("1, 2 or 4 bytes", lambda: moe.dispatch(X[0], IDS, 4)),
     ("x's rows must be contiguous", lambda: moe.dispatch(zeros(32, 6).t(), IDS, 4)),

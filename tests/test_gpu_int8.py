@@ -326,12 +326,15 @@ def test_layer(M, k, E):
     w13, s13 = moe.quant_int8(bf16(rng, E * 2 * I, H, scale=H ** -0.5).to(DEV))
     w2, s2 = moe.quant_int8(bf16(rng, E * H, I, scale=I ** -0.5).to(DEV))
     ids, w = moe.route_topk(logits, k)
-    al = moe.align(ids, E, 1)
-    off, rows = al["offsets"], al["sorted_ids"]
-    gu = moe.grouped_gemm_int8(x.to(DEV), w13.view(E, 2 * I, H), s13.view(E, 2 * I), off, a_rows=rows, a_div=k)
-    codes, scales = moe.swiglu_int8(gu, w.view(-1)[rows.long()])
-    o = moe.grouped_gemm_int8(codes, w2.view(E, H, I), s2.view(E, H), off, a_scale=scales, out_rows=rows)
-    y = moe.combine(o, torch.arange(M * k, dtype=torch.int32, device=DEV).view(M, k))
+    _, off, pos, pairs = moe.dispatch(None, ids, E)
+    gu = moe.grouped_gemm_int8(x.to(DEV), w13.view(E, 2 * I, H), s13.view(E, 2 * I), off, a_rows=pairs, a_div=k)
+    codes, scales = moe.swiglu_int8(gu, num_rows=off[E:])
+    o = moe.grouped_gemm_int8(codes, w2.view(E, H, I), s2.view(E, H), off, a_scale=scales)
+    y = moe.combine(o, pos, w)
+    # weighted in the activation's scales, and back in pair order
+    codes, scales = moe.swiglu_int8(gu, w.view(-1)[pairs.long()])
+    o = moe.grouped_gemm_int8(codes, w2.view(E, H, I), s2.view(E, H), off, a_scale=scales, out_rows=pairs)
+    y2 = moe.combine(o, torch.arange(M * k, dtype=torch.int32, device=DEV).view(M, k))
     torch.cuda.synchronize()
     q, s = int8_of(f64(x))
     v13, v2 = (f64(c).reshape(E, -1, n) * f64(t).reshape(E, -1, 1) for c, t, n in ((w13, s13, H), (w2, s2, I)))
@@ -346,4 +349,5 @@ def test_layer(M, k, E):
             wt = float(w[t, j])
             ref[t] += wt * (v2[e] @ h)
             mag[t] += wt * (np.abs(v2[e]) @ slack + BF16_STEP * (np.abs(v2[e]) @ np.abs(h)))
-    assert (np.abs(f64(y) - ref) <= 1.02 * mag + BF16_STEP * np.abs(ref)).all()
+    for got in (y, y2):
+        assert (np.abs(f64(got) - ref) <= 1.02 * mag + BF16_STEP * np.abs(ref)).all()

@@ -63,6 +63,9 @@ def check_dispatch(x, ids, E, first, dtype=torch.bfloat16, pad=8):
     canvas.check_untouched(written)
     token = torch.from_numpy(r_pairs[:n] // k).to(DEV)
     assert torch.equal(out[:n], x[token])
+    # the layout alone
+    none, *alone = moe.dispatch(None, torch.from_numpy(ids).to(DEV), E, first_expert=first)
+    assert none is None and all(torch.equal(a, b) for a, b in zip(alone, (off, pos, pairs)))
 
 
 # the pairs counted by every workgroup (up to 4096), as sums of chunks, and scanned
