@@ -697,8 +697,8 @@ def _compiled():
     return _native
 
 
-def dispatch(x: Optional[torch.Tensor], ids: torch.Tensor, E: int, out: Optional[torch.Tensor] = None, *, first_expert: int = 0,
-             stream=None):
+def dispatch(x: Optional[torch.Tensor], ids: torch.Tensor, E: int, out: Optional[torch.Tensor] = None, *,
+             first_expert: int = 0, stream=None):
     """The tokens' rows copied to rows grouped by expert (moe_dispatch).
 
     x [M,H] of a type of 1, 2 or 4 bytes (rows may be strided, and hold a

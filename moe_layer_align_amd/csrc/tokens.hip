@@ -562,8 +562,8 @@ moe_status_t moe_dispatch(const moe_dispatch_args_t* a, void* stream) {
   const int groups = P ? cdiv(d.M, d.group) : 1;
   // few workgroups share a token's row
   const int steps = cdiv((int64_t)d.group * (d.row_bytes / 16), 4 * kThreads);
-  int split = 256 / groups;
-  split = split < 1 ? 1 : (split > steps ? steps : split);
+  int split = 256 / groups < steps ? 256 / groups : steps;
+  if (split < 1) split = 1;
   const dim3 grid(groups, split);
   if (P <= kCountAllPairs) {
     dispatch_kernel<kCountAll><<<grid, kThreads, 0, st>>>(d);

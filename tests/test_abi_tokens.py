@@ -61,7 +61,8 @@ DISPATCH = dict(M=10, top_k=2, E=4, first_expert=0, ids=P, x=P, x_stride=128, ro
 
 @pytest.mark.parametrize("kw,code", [
     (dict(M=-1), INVALID), (dict(E=0), INVALID), (dict(top_k=0), INVALID), (dict(first_expert=-1), INVALID),
-    (dict(row_bytes=0), INVALID), (dict(x=None, rows=None, ids=None), INVALID), (dict(E=513), UNSUPPORTED), (dict(top_k=17), UNSUPPORTED),
+    (dict(row_bytes=0), INVALID), (dict(x=None, rows=None, ids=None), INVALID),
+    (dict(E=513), UNSUPPORTED), (dict(top_k=17), UNSUPPORTED),
     (dict(M=1 << 25), UNSUPPORTED), (dict(row_bytes=24, x_stride=32, rows_stride=32), UNSUPPORTED),
     (dict(row_bytes=1 << 22, x_stride=1 << 22, rows_stride=1 << 22), UNSUPPORTED),
     (dict(x_stride=1 << 22), UNSUPPORTED), (dict(rows_stride=1 << 22), UNSUPPORTED),
@@ -315,8 +316,8 @@ OFFM = meta(4, dtype=I32)
                                                         meta(3, 32, dtype=F32), OFFM, meta(HUGE, 32),
                                                         a_scale=meta(HUGE, dtype=F32))),
     ("divisor", lambda: moe.grouped_gemm_int8(meta(8, 64, dtype=I8), meta(3, 32, 64, dtype=I8),
-                                                   meta(3, 32, dtype=F32), OFFM, meta(8, 32), a_scale=meta(8, dtype=F32),
-                                                   a_rows=meta(8, dtype=I32), a_div=HUGE)),
+                                              meta(3, 32, dtype=F32), OFFM, meta(8, 32),
+                                              a_scale=meta(8, dtype=F32), a_rows=meta(8, dtype=I32), a_div=HUGE)),
 ])
 def test_sizes_past_32_bits(name, call):
     # the library's sizes are int32: a larger one must not become another size
