@@ -14,9 +14,10 @@
 // operand: a lane's four results are four rows' sums for one weight row.  Sums
 // are exact in int32; the scales join once, at the end.
 //
-// The four waves split K, step by step (wave w takes steps w, w + 4, ...); their
-// partial sums meet in LDS.  Few weight rows take bands of 32 instead of 64, so
-// that no CU is idle.
+// The four waves split K, step by step (wave w takes steps w, w + 4, ...), and
+// their partial sums meet in LDS; where K has few steps each wave takes a band of
+// its own instead.  Few weight rows take bands of 32 instead of 64, so that no CU
+// is idle.
 #include <type_traits>
 
 #include "grouped_stream.h"
@@ -78,10 +79,10 @@ __device__ __forceinline__ void row_tops(const GroupedInt8Args& a, int i0, int n
 // written.  BF16: the rows are bf16 and become codes here, on their way from
 // memory to the MFMA, under the largest magnitude that a first look at them
 // finds while the first weights are on their way.
-template <bool BF16, bool F32, int FT, int NT>
+template <bool BF16, bool F32, int WK, int FT, int NT>
 __device__ __forceinline__ void pass(const GroupedInt8Args& a, int e, int n0, int i0, int hi, lds_u8* smem,
                                      lds_u32* top) {
-  constexpr int kBand = 16 * FT;  // weight rows of the workgroup
+  constexpr int kBand = 16 * FT * (4 / WK);  // weight rows of the workgroup
   constexpr int kLd = kBand + 4;              // row stride of the partial sums
   constexpr int kStage = stage_bytes(FT);
   constexpr int kEsz = BF16 ? 2 : 1;
@@ -92,13 +93,14 @@ __device__ __forceinline__ void pass(const GroupedInt8Args& a, int e, int n0, in
   const __amdgpu_buffer_rsrc_t rw = buffer(a.w + (int64_t)e * a.N * wrow, (unsigned)a.N * wrow);
   const __amdgpu_buffer_rsrc_t rx = buffer(a.in.ids ? a.in.p : a.in.p + (int64_t)i0 * a.in.stride * kEsz, kOob);
   lds_u8* const stage = smem + wave * (2 * kStage);
+  const int wk = wave % WK, wb = wave / WK, nb = n0 + 16 * FT * wb;  // the wave's first step and weight row
 
-  // weights: load d of a step takes rows n0 + 8d + lane/8, lane l the 16-byte
+  // weights: load d of a step takes rows nb + 8d + lane/8, lane l the 16-byte
   // chunk (l%8) ^ pf_mix(row) of their 128 bytes; rows at or past N lie past
   // the buffer, chunks past K take kOob
   const int wchunk = (lane & 7) ^ (lane >> 3);
-  const unsigned w0 = (unsigned)(n0 + (lane >> 3)) * wrow + (wchunk << 4);
-  const unsigned w1 = (unsigned)(n0 + (lane >> 3)) * wrow + ((wchunk ^ 1) << 4);
+  const unsigned w0 = (unsigned)(nb + (lane >> 3)) * wrow + (wchunk << 4);
+  const unsigned w1 = (unsigned)(nb + (lane >> 3)) * wrow + ((wchunk ^ 1) << 4);
   auto load_w = [&](int c, int b) {
     const int left = a.K - c * kStep;  // bytes of a row from this step on
     const bool ok0 = (wchunk << 4) < left, ok1 = ((wchunk ^ 1) << 4) < left;
@@ -159,7 +161,7 @@ __device__ __forceinline__ void pass(const GroupedInt8Args& a, int e, int n0, in
     u32x4 w[FT][2];
     read_stage<FT>(w, frag0 + b * kStage, frag1 + b * kStage);  // the stage is read: load it again
     fence();
-    if constexpr (more()) load_w(c + 8, b);
+    if constexpr (more()) load_w(c + 2 * WK, b);
     fence();
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -172,7 +174,7 @@ __device__ __forceinline__ void pass(const GroupedInt8Args& a, int e, int n0, in
         for (int t = 0; t < NT; ++t) acc[f][t] = mfma_i8(x[t], w[f][i], acc[f][t]);
     }
     fence();
-    if constexpr (more()) load_x(g, c + 8);
+    if constexpr (more()) load_x(g, c + 2 * WK);
     fence();
   };
   constexpr std::integral_constant<int, kLater> next_in_flight{};
@@ -193,7 +195,7 @@ __device__ __forceinline__ void pass(const GroupedInt8Args& a, int e, int n0, in
     out_id[u] = a.out.ids ? a.out.ids[i] : 0;
   }
   fence();
-  load_w(wave, 0);
+  load_w(wk, 0);
   fence();
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
@@ -201,7 +203,7 @@ __device__ __forceinline__ void pass(const GroupedInt8Args& a, int e, int n0, in
     const int m = i < hi ? (a.in.ids ? row_of(a.in, i, in_id[t]) : i - i0) : -1;
     x0[t] = m >= 0 ? ((unsigned)m * (unsigned)a.in.stride + 16 * q) * kEsz : kOob;
   }
-  load_x(g0, wave);
+  load_x(g0, wk);
   fence();
   // the scales of the thread's results
   float sa[kStores];
@@ -217,9 +219,9 @@ __device__ __forceinline__ void pass(const GroupedInt8Args& a, int e, int n0, in
     for (int h = 0; h < kPer / 4; ++h) sw[u][h] = *(const f32x4*)(a.w_scale + (int64_t)e * a.N + n + 4 * h);
   }
   fence();
-  load_w(wave + 4, 1);
+  load_w(wk + WK, 1);
   fence();
-  load_x(g1, wave + 4);
+  load_x(g1, wk + WK);
   if constexpr (BF16) {
     fence();
     row_tops(a, i0, 16 * NT, hi, top);
@@ -229,17 +231,17 @@ __device__ __forceinline__ void pass(const GroupedInt8Args& a, int e, int n0, in
 #pragma unroll
     for (int u = 0; u < kStores; ++u) sa[u] = row_scale(top[min((u * 256 + tid) / kCols, 16 * NT - 1)]).s;
   }
-  int c = wave;
-  for (; c + 8 < nstep; c += 8) {  // loads past the last step read nothing
+  int c = wk;
+  for (; c + 2 * WK < nstep; c += 2 * WK) {  // loads past the last step read nothing
     step(g0, c, 0, next_in_flight, std::true_type{});
-    step(g1, c + 4, 1, next_in_flight, std::true_type{});
+    step(g1, c + WK, 1, next_in_flight, std::true_type{});
   }
   if (c < nstep) step(g0, c, 0, next_in_flight, std::false_type{});
-  if (c + 4 < nstep) step(g1, c + 4, 1, none_in_flight, std::false_type{});
+  if (c + WK < nstep) step(g1, c + WK, 1, none_in_flight, std::false_type{});
   fence();
   wait_vm<0>();  // loads past the last step still write LDS
   lds_i32* const red = (lds_i32*)smem;
-  // partial sums: [wave][row][weight row], over the stages
+  // partial sums: [wk][row][weight row], over the stages
   __syncthreads();
 #pragma unroll
   for (int f = 0; f < FT; ++f)
@@ -247,7 +249,7 @@ __device__ __forceinline__ void pass(const GroupedInt8Args& a, int e, int n0, in
     for (int t = 0; t < NT; ++t)
 #pragma unroll
       for (int v = 0; v < 4; ++v)
-        red[(wave * 16 * NT + 16 * t + 4 * q + v) * kLd + 16 * f + r16] = acc[f][t][v];
+        red[(wk * 16 * NT + 16 * t + 4 * q + v) * kLd + 16 * (FT * wb + f) + r16] = acc[f][t][v];
   __syncthreads();
 #pragma unroll
   for (int u = 0; u < kStores; ++u) {
@@ -260,7 +262,7 @@ __device__ __forceinline__ void pass(const GroupedInt8Args& a, int e, int n0, in
     for (int h = 0; h < kPer / 4; ++h) {
       i32x4 s = *(const lds_i32x4*)(red + row * kLd + col + 4 * h);
 #pragma unroll
-      for (int k = 1; k < 4; ++k) s += *(const lds_i32x4*)(red + (k * 16 * NT + row) * kLd + col + 4 * h);
+      for (int k = 1; k < WK; ++k) s += *(const lds_i32x4*)(red + (k * 16 * NT + row) * kLd + col + 4 * h);
 #pragma unroll
       for (int j = 0; j < 4; ++j) v[h][j] = (float)s[j] * sa[u] * sw[u][h][j];
     }
@@ -274,56 +276,72 @@ __device__ __forceinline__ void pass(const GroupedInt8Args& a, int e, int n0, in
   __syncthreads();  // the next pass loads over the partial sums
 }
 
-// An expert's rows in passes of 64, the last ones in one of 16 or 32 where that
-// holds them: the weights are streamed once per pass, and the workgroups of a
-// band (blockIdx.z) take its passes in turn.  bf16 rows take passes of
-// at most 32 (their conversion costs as much per row as the stream of the weights).
-template <bool BF16, bool F32, int FT>
+// Most rows of a pass.  bf16 rows cost as much per row as the stream of the
+// weights; wide bands need their registers for the results.
+constexpr int pass_rows(bool bf16, int wk) { return bf16 || wk == 1 ? 32 : 64; }
+
+// An expert's rows in passes of 64 (32), the last ones in one of 16 or 32 where
+// that holds them: the weights are streamed once per pass, and the workgroups of
+// a band (blockIdx.z) take its passes in turn.
+template <bool BF16, bool F32, int WK, int FT>
 __global__ __launch_bounds__(256, 2) void grouped_int8_kernel(GroupedInt8Args a) {
-  constexpr int kBand = 16 * FT, kMost = BF16 ? 2 : 4;
-  constexpr int kSums = 4 * 16 * kMost * (kBand + 4) * 4, kStages = 8 * stage_bytes(FT);
+  constexpr int kBand = 16 * FT * (4 / WK), kRows = pass_rows(BF16, WK);
+  constexpr int kSums = WK * kRows * (kBand + 4) * 4, kStages = 8 * stage_bytes(FT);
   __shared__ __align__(16) uint8_t smem[kStages > kSums ? kStages : kSums];
-  __shared__ unsigned top[16 * kMost];
+  __shared__ unsigned top[kRows];
   const Found f = find_expert(a.offsets, a.R, a.E);
   if (f.e >= a.E) return;
-  const int n0 = blockIdx.x * kBand;
-  const int step = gridDim.z * (16 * kMost);
-  for (int i0 = f.lo + blockIdx.z * (16 * kMost); i0 < f.hi; i0 += step) {
+  const int n0 = blockIdx.x * kBand, step = gridDim.z * kRows;
+  for (int i0 = f.lo + blockIdx.z * kRows; i0 < f.hi; i0 += step) {
     const int n = f.hi - i0;
     if (n <= 16)
-      pass<BF16, F32, FT, 1>(a, f.e, n0, i0, f.hi, (lds_u8*)smem, (lds_u32*)top);
-    else if (n <= 32 || kMost == 2)
-      pass<BF16, F32, FT, 2>(a, f.e, n0, i0, f.hi, (lds_u8*)smem, (lds_u32*)top);
-    else if constexpr (kMost == 4)
-      pass<BF16, F32, FT, 4>(a, f.e, n0, i0, f.hi, (lds_u8*)smem, (lds_u32*)top);
+      pass<BF16, F32, WK, FT, 1>(a, f.e, n0, i0, f.hi, (lds_u8*)smem, (lds_u32*)top);
+    else if (n <= 32 || kRows == 32)
+      pass<BF16, F32, WK, FT, 2>(a, f.e, n0, i0, f.hi, (lds_u8*)smem, (lds_u32*)top);
+    else if constexpr (kRows == 64)
+      pass<BF16, F32, WK, FT, 4>(a, f.e, n0, i0, f.hi, (lds_u8*)smem, (lds_u32*)top);
   }
 }
 
-template <bool BF16, bool F32, int FT>
+template <bool BF16, bool F32, int WK, int FT>
 void launch(hipStream_t st, const GroupedInt8Args& a) {
-  constexpr int kBand = 16 * FT, kRows = BF16 ? 32 : 64;
+  constexpr int kBand = 16 * FT * (4 / WK), kRows = pass_rows(BF16, WK);
   const int bands = (a.N + kBand - 1) / kBand, experts = a.R < a.E ? a.R : a.E, passes = (a.R + kRows - 1) / kRows;
   // few bands: passes side by side, until the CUs are full
   const int64_t blocks = (int64_t)bands * experts;
   const int side = blocks >= kFull ? 1 : (int)((kFull + blocks - 1) / blocks);
-  grouped_int8_kernel<BF16, F32, FT><<<dim3(bands, experts, side < passes ? side : passes), 256, 0, st>>>(a);
+  grouped_int8_kernel<BF16, F32, WK, FT>
+      <<<dim3(bands, experts, side < passes ? side : passes), 256, 0, st>>>(a);
 }
+
+// K of few steps: four bands a workgroup against its four waves on one (us): 238
+// experts of 13216 x 144 102.3 and 249.2, 256 of 4096 x 512 55.3 and 69.1, 128 of
+// 1536 x 512 17.0 and 19.8, 105 of 5768 x 672 13.5 and 15.0, 128 of 1536 x 768 29.4
+// and 28.8, 8 of 32768 x 1024 46.5 and 44.3.
+constexpr int kShort = 640;
 
 template <bool BF16, bool F32>
 void pick(hipStream_t st, const GroupedInt8Args& a) {
   const int64_t rows = (int64_t)(a.R < a.E ? a.R : a.E) * a.N;  // weight rows that may be read
   if (rows < 256 * 64)
-    launch<BF16, F32, 2>(st, a);
+    launch<BF16, F32, 4, 2>(st, a);
+  else if (a.K <= kShort)
+    launch<BF16, F32, 1, 4>(st, a);
   else
-    launch<BF16, F32, 4>(st, a);
+    launch<BF16, F32, 4, 4>(st, a);
 }
 
 // Whether the passes over the bands are few: then each takes a workgroup of its
 // own, all at once, where few tiles of 256 x 256 would leave most CUs idle
 // (streamed and tiled, us): 66 passes over 5 experts of 184 x 7744 16.8 and 67.0;
 // 384 of 1024 x 4096 23.5 and 39.7, 640 39.9 and 41.1; 640 of 1024 x 1024 14.7 and
-// 19.3, 1136 25.4 and 20.3.
-bool few(int R, int E, int64_t N) { return (R / 64 + (int64_t)(R < E ? R : E)) * ((N + 63) / 64) <= 640; }
+// 19.3, 1136 25.4 and 20.3.  Of short K: 966 over 79 experts of 1736 x 256 12.4 and
+// 21.1 (20.4 and 22.8 under a Zipf-like routing), 680 over 17 of 4096 x 512 14.3
+// and 19.3, 1088 21.3 and 19.6.
+bool few(int R, int E, int64_t N, int64_t K) {
+  const int64_t experts = R < E ? R : E;
+  return K <= kShort ? (R / 32 + experts) * ((N + 255) / 256) <= 960 : (R / 64 + experts) * ((N + 63) / 64) <= 640;
+}
 
 // Streamed or tiled otherwise, by the rows per expert on average (the same).  The
 // stream has less to start and end: 402 MB of 128 experts of 1536 x 2048 with 2
@@ -335,7 +353,7 @@ bool few(int R, int E, int64_t N) { return (R / 64 + (int64_t)(R < E ? R : E)) *
 // rows take as long in either form (2 rows 523.4 and 525.7, 16 718.6 and 719.4).
 bool streamed(int R, int E, int64_t N, int64_t K) {
   const int rows = (R < E ? R : E) * N * K < ((int64_t)1 << 30) ? 16 : 4;
-  return R <= rows * (int64_t)E || few(R, E, N);
+  return R <= rows * (int64_t)E || few(R, E, N, K);
 }
 
 }  // namespace

@@ -199,19 +199,27 @@ def test_product_rows(gather, scatter, dtype, name):
 
 
 @pytest.mark.parametrize("name", ["one_row", "decode", "few", "edges_64"])
-@pytest.mark.parametrize("K", [16, 128, 144, 384, 512, 640, 1024, 1040, 1168, 2064, 4112])
-def test_product_steps(name, K):
-    # every number of steps that the waves share, and parts of one; wide bands
-    run_product(COUNTS[name], 2056, K, True, True, torch.float32)
+@pytest.mark.parametrize("K", [16, 128, 144, 384, 512, 640, 656, 1024, 1040, 1168, 2064, 4112])
+@pytest.mark.parametrize("N,dtype", [(2056, torch.float32), (8200, torch.bfloat16)])
+def test_product_steps(name, K, N, dtype):
+    # every number of steps that a wave or the four share, and parts of one; bands of each width
+    run_product(COUNTS[name], N, K if N < 8200 else min(K, 1040), True, True, dtype)
+
+
+@pytest.mark.parametrize("counts,N", [([700, 640, 0, 720, 1, 129, 900], 8200),
+                                      ([64 * (i % 3) + 33 for i in range(90)], 1544)])
+@pytest.mark.parametrize("K", [16, 80, 208, 656])
+@pytest.mark.parametrize("gather,scatter,dtype", [(False, False, torch.bfloat16), (True, False, torch.float32),
+                                                  (True, True, torch.bfloat16), (False, True, torch.float32)])
+def test_tiles(counts, N, K, gather, scatter, dtype):
+    # results whose tiles fill the GPU: the tiled form
+    run_product(counts, N, K, gather, scatter, dtype)
 
 
 @pytest.mark.parametrize("name", ["edges_64", "edges_128", "edges_256", "skewed"])
-@pytest.mark.parametrize("K", [16, 80, 208])
-@pytest.mark.parametrize("gather,scatter,dtype", [(False, False, torch.bfloat16), (True, False, torch.float32),
-                                                  (True, True, torch.bfloat16), (False, True, torch.float32)])
-def test_tiles(name, K, gather, scatter, dtype):
-    # wide results, whose tiles fill the GPU: the tiled form at its tiles' borders
-    run_product(COUNTS[name], 8200, K, gather, scatter, dtype)
+@pytest.mark.parametrize("K,dtype", [(656, torch.bfloat16), (784, torch.float32)])
+def test_tile_edges(name, K, dtype):
+    run_product(COUNTS[name], 8200, K, name == "skewed", name == "edges_128", dtype)
 
 
 @pytest.mark.parametrize("counts", [[300], [64, 65, 0, 129], [1000, 1]])
