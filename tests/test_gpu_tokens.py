@@ -145,7 +145,8 @@ def combine_case(M, k, E, H, rows_type, y_type, weighted, drop, seed=0):
 
 
 CASES = [(1, 1, 1, 8), (1, 2, 8, 4096), (5, 16, 16, 2064), (64, 8, 32, 2048), (77, 3, 7, 520), (300, 4, 9, 72),
-         (130, 6, 64, 1032), (9, 2, 4, 14336)]
+         (130, 6, 64, 1032), (9, 2, 4, 14336), (40, 5, 12, 200), (33, 16, 16, 64), (50, 3, 8, 256), (600, 8, 8, 128),
+         (21, 9, 30, 24)]
 
 
 @pytest.mark.parametrize("M,k,E,H", CASES)
