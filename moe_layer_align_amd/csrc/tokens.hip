@@ -368,6 +368,7 @@ struct CombineGradArgs {
   int64_t drows_stride;
   int drows_f32;
   float* dweights;
+  int run;  // tokens at a time, run * k <= 64
 };
 
 // WPT waves work on one token (so that each of its dweights is one sum in a
@@ -377,92 +378,115 @@ struct CombineGradArgs {
 // tokens, top-8, H 2048, with the router's gradient, a wave per token and the
 // results in one buffer: 73.2 -> 60.5 us).  Of four waves per token and one, in
 // fresh buffers: 55.1 and 57.5.
+//
+// The waves take runs of tokens: one load has a run's places and weights, a lane
+// each, and a ballot its tokens with rows.  The others, most of them where the
+// experts are spread over many processes, cost no more than their zero weights,
+// and their dy is not read (16384 tokens, top-8, H 2048, with the router's
+// gradient, 8 of 256 experts here, against a workgroup per token that reads its
+// dy: 88.4 -> 42.9 us; 32 here, uneven, 96.7 -> 68.6; all experts here, 4096
+// tokens, 54.9 -> 53.5).
 template <bool F32, int KB, int WPT>
 __global__ __launch_bounds__(kThreads) void combine_grad_kernel(CombineGradArgs a) {
-  constexpr int kTokens = 4 / WPT;  // per workgroup
+  constexpr int kRuns = 4 / WPT;  // per workgroup
   __shared__ float part[4][KB];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wt = wave % WPT;
-  for (int t0 = blockIdx.x * kTokens; t0 < a.M; t0 += gridDim.x * kTokens) {
-    const int t = t0 + wave / WPT;
-    for (int j0 = 0; j0 < a.k; j0 += KB) {
-      int p[KB];
-      float w[KB], dot[KB];
-#pragma unroll
-      for (int j = 0; j < KB; ++j) {
-        const bool in = t < a.M && j0 + j < a.k;
-        p[j] = in ? a.positions[(int64_t)t * a.k + j0 + j] : -1;
-        if ((unsigned)p[j] >= (unsigned)a.R) p[j] = -1;
-        w[j] = in && a.weights ? a.weights[(int64_t)t * a.k + j0 + j] : 1.0f;
-        dot[j] = 0.0f;
-      }
-      constexpr int kRaw = F32 ? 2 : 1;
-      u32x4 d[2], next[KB][kRaw];
-      const uint8_t* const dy = a.dy + t * a.dy_stride;
-      auto load = [&](int col) {
-        if (col >= a.H || t >= a.M) return;
-        d[0] = load_once(dy + (int64_t)col * (a.dy_f32 ? 4 : 2));
-        if (a.dy_f32) d[1] = load_once(dy + (int64_t)col * 4 + 16);
-        if (!a.rows) return;
-#pragma unroll
-        for (int j = 0; j < KB; ++j)
-          if (p[j] >= 0)
-#pragma unroll
-            for (int i = 0; i < kRaw; ++i)
-              next[j][i] = load_once(a.rows + p[j] * a.rows_stride + (int64_t)col * (F32 ? 4 : 2) + 16 * i);
-      };
-      const int col0 = (wt * 64 + lane) * 8;
-      load(col0);
-      if (t < a.M)
-        for (int col = col0; col < a.H; col += WPT * 512) {
-          float g[8];
-          if (a.dy_f32)
-            unpack8<true>(d, g);
-          else
-            unpack8<false>(d, g);
-          u32x4 row[KB][kRaw];
-#pragma unroll
-          for (int j = 0; j < KB; ++j)
-#pragma unroll
-            for (int i = 0; i < kRaw; ++i) row[j][i] = next[j][i];
-          load(col + WPT * 512);
-#pragma unroll
-          for (int j = 0; j < KB; ++j) {
-            if (p[j] < 0) continue;
-            if (a.rows) {
-              float r[8];
-              unpack8<F32>(row[j], r);
-#pragma unroll
-              for (int i = 0; i < 8; ++i) dot[j] += g[i] * r[i];
-            }
-            if (a.drows) {
-              float o[8];
-#pragma unroll
-              for (int i = 0; i < 8; ++i) o[i] = w[j] * g[i];
-              store8(a.drows + p[j] * a.drows_stride + (int64_t)col * (a.drows_f32 ? 4 : 2), a.drows_f32, o);
-            }
-          }
-        }
-      if (!a.dweights) continue;
-#pragma unroll
-      for (int j = 0; j < KB; ++j) dot[j] = wave_sum(dot[j]);
-      if constexpr (WPT > 1) {
-        if (lane == 0)
-#pragma unroll
-          for (int j = 0; j < KB; ++j) part[wave][j] = dot[j];
-        __syncthreads();
+  const unsigned long long slots = ~0ull >> (64 - a.k);
+  for (int64_t t0 = (int64_t)blockIdx.x * kRuns * a.run; t0 < a.M; t0 += (int64_t)gridDim.x * kRuns * a.run) {
+    const int first = (int)t0 + wave / WPT * a.run;
+    const int64_t pair = (int64_t)first * a.k + lane;
+    const bool mine = lane < a.run * a.k && pair < (int64_t)a.M * a.k;
+    int place = mine ? a.positions[pair] : -1;
+    const float weight = mine && a.weights ? a.weights[pair] : 1.0f;
+    if ((unsigned)place >= (unsigned)a.R) place = -1;
+    unsigned long long left = __ballot(place >= 0);
+    if (a.dweights && wt == 0 && mine && !(left >> (lane / a.k * a.k) & slots)) a.dweights[pair] = 0.0f;
+    while (left) {
+      const int at = (int)__builtin_ctzll(left) / a.k * a.k;
+      left &= ~(slots << at);
+      const int t = first + at / a.k;
+      for (int j0 = 0; j0 < a.k; j0 += KB) {
+        int p[KB];
+        float w[KB], dot[KB];
 #pragma unroll
         for (int j = 0; j < KB; ++j) {
-          dot[j] = part[wave - wt][j];
-#pragma unroll
-          for (int i = 1; i < WPT; ++i) dot[j] += part[wave - wt + i][j];
+          const int from = at + j0 + j;
+          p[j] = j0 + j < a.k ? __builtin_amdgcn_readlane(place, from & 63) : -1;
+          w[j] = __uint_as_float((unsigned)__builtin_amdgcn_readlane((int)__float_as_uint(weight), from & 63));
+          dot[j] = 0.0f;
         }
-        __syncthreads();
-      }
-      if (wt == 0 && lane == 0 && t < a.M)
+        bool any = false;
 #pragma unroll
-        for (int j = 0; j < KB; ++j)
-          if (j0 + j < a.k) a.dweights[(int64_t)t * a.k + j0 + j] = dot[j];
+        for (int j = 0; j < KB; ++j) any |= p[j] >= 0;
+        constexpr int kRaw = F32 ? 2 : 1;
+        u32x4 d[2], next[KB][kRaw];
+        const uint8_t* const dy = a.dy + (int64_t)t * a.dy_stride;
+        auto load = [&](int col) {
+          if (col >= a.H) return;
+          d[0] = load_once(dy + (int64_t)col * (a.dy_f32 ? 4 : 2));
+          if (a.dy_f32) d[1] = load_once(dy + (int64_t)col * 4 + 16);
+          if (!a.rows) return;
+#pragma unroll
+          for (int j = 0; j < KB; ++j)
+            if (p[j] >= 0)
+#pragma unroll
+              for (int i = 0; i < kRaw; ++i)
+                next[j][i] = load_once(a.rows + p[j] * a.rows_stride + (int64_t)col * (F32 ? 4 : 2) + 16 * i);
+        };
+        const int col0 = (wt * 64 + lane) * 8;
+        if (any) load(col0);
+        if (any)
+          for (int col = col0; col < a.H; col += WPT * 512) {
+            float g[8];
+            if (a.dy_f32)
+              unpack8<true>(d, g);
+            else
+              unpack8<false>(d, g);
+            u32x4 row[KB][kRaw];
+#pragma unroll
+            for (int j = 0; j < KB; ++j)
+#pragma unroll
+              for (int i = 0; i < kRaw; ++i) row[j][i] = next[j][i];
+            load(col + WPT * 512);
+#pragma unroll
+            for (int j = 0; j < KB; ++j) {
+              if (p[j] < 0) continue;
+              if (a.rows) {
+                float r[8];
+                unpack8<F32>(row[j], r);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) dot[j] += g[i] * r[i];
+              }
+              if (a.drows) {
+                float o[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) o[i] = w[j] * g[i];
+                store8(a.drows + p[j] * a.drows_stride + (int64_t)col * (a.drows_f32 ? 4 : 2), a.drows_f32, o);
+              }
+            }
+          }
+        if (!a.dweights) continue;
+#pragma unroll
+        for (int j = 0; j < KB; ++j) dot[j] = wave_sum(dot[j]);
+        if constexpr (WPT > 1) {
+          if (lane == 0)
+#pragma unroll
+            for (int j = 0; j < KB; ++j) part[wave][j] = dot[j];
+          __syncthreads();
+#pragma unroll
+          for (int j = 0; j < KB; ++j) {
+            dot[j] = part[wave - wt][j];
+#pragma unroll
+            for (int i = 1; i < WPT; ++i) dot[j] += part[wave - wt + i][j];
+          }
+          __syncthreads();
+        }
+        if (wt == 0 && lane == 0)
+#pragma unroll
+          for (int j = 0; j < KB; ++j)
+            if (j0 + j < a.k) a.dweights[(int64_t)t * a.k + j0 + j] = dot[j];
+      }
     }
   }
 }
@@ -592,8 +616,17 @@ void launch_combine(int grid_y, hipStream_t st, const CombineArgs& a) {
     combine_kernel<F32, 8><<<grid, kThreads, 0, st>>>(a);
 }
 
+// Runs of tokens of combine_grad.  More runs balance better where every token has
+// rows, fewer cost less where most have none.  8192, 4096 and 2048 (us, with the
+// router's gradient): 16384 tokens, top-8, H 2048, 8 of 256 experts here 44.3, 42.9
+// and 43.0, 128 here 133.3, 139.3 and 144.0; 8192, top-2, H 4096, 1 of 8 here 18.9,
+// 17.8 and 20.9.
+constexpr int kGradRuns = 4096;
+
 template <bool F32, int KB>
-void launch_combine_grad(hipStream_t st, const CombineGradArgs& a) {
+void launch_combine_grad(hipStream_t st, CombineGradArgs a) {
+  const int runs = a.H <= 1024 ? 4 * kGradRuns : kGradRuns;
+  a.run = a.M / runs < 1 ? 1 : a.M / runs < kWave / a.k ? a.M / runs : kWave / a.k;
   if (a.H <= 64)
     combine_grad_narrow_kernel<F32, KB, 8><<<grid_of(cdiv(a.M, kThreads / 8)), kThreads, 0, st>>>(a);
   else if (a.H <= 128)
@@ -601,9 +634,9 @@ void launch_combine_grad(hipStream_t st, const CombineGradArgs& a) {
   else if (a.H <= 256)
     combine_grad_narrow_kernel<F32, KB, 32><<<grid_of(cdiv(a.M, kThreads / 32)), kThreads, 0, st>>>(a);
   else if (a.H <= 1024)
-    combine_grad_kernel<F32, KB, 1><<<grid_of(cdiv(a.M, 4)), kThreads, 0, st>>>(a);
+    combine_grad_kernel<F32, KB, 1><<<grid_of(cdiv(a.M, 4 * a.run)), kThreads, 0, st>>>(a);
   else
-    combine_grad_kernel<F32, KB, 4><<<grid_of(a.M), kThreads, 0, st>>>(a);
+    combine_grad_kernel<F32, KB, 4><<<grid_of(cdiv(a.M, a.run)), kThreads, 0, st>>>(a);
 }
 
 }  // namespace

@@ -198,6 +198,41 @@ def test_combine_grad(M, k, E, H, dy_type, rows_type, out, weighted, drop):
     assert none is None and torch.equal(only[torch.from_numpy(written)], canvas.t[torch.from_numpy(written)])
 
 
+@pytest.mark.parametrize("M,k,H,drop", [(13001, 3, 1032, 0.8), (12289, 16, 1032, 0.97), (40007, 2, 264, 0.9),
+                                        (20001, 8, 1040, 0.0), (70001, 1, 520, 0.5), (50000, 3, 264, 1.0)])
+def test_combine_grad_of_many_tokens(M, k, H, drop):
+    """Many tokens with few rows or none: the same bits as in calls on a few of them, whatever the others hold."""
+    say("combine_grad of many %s" % ((M, k, H, drop),))
+    rng = np.random.default_rng([M, k, H])
+    valid = rng.random((M, k)) >= drop
+    R = max(int(valid.sum()), 1)
+    pos = np.where(valid, 0, rng.choice([-1, R, R + 7, -2 ** 31], size=(M, k))).astype(np.int32)
+    pos[valid] = rng.permutation(int(valid.sum()))
+    torch.manual_seed(M)
+    dy = torch.randn(M, H, device=DEV).to(torch.bfloat16)
+    tv = torch.from_numpy(valid).to(DEV)
+    dy[~tv.any(1)] = float("nan")
+    rows = torch.randn(R, H, device=DEV).to(torch.bfloat16)
+    tp, w = torch.from_numpy(pos).to(DEV), torch.randn(M, k, device=DEV)
+    canvas = Canvas(R, H, torch.bfloat16)
+    drows, dw = moe.combine_grad(dy, rows, tp, w, canvas.t)
+    canvas.check_untouched(np.full(R, bool(valid.any())))
+    assert not bool(dw[~tv].any())
+    ref = torch.zeros(M, k, dtype=torch.float64, device=DEV)
+    mag = torch.zeros_like(ref)
+    for j in range(k):
+        at = tv[:, j]
+        terms = dy[at].double() * rows[tp[at, j].long()].double()
+        ref[at, j], mag[at, j] = terms.sum(1), terms.abs().sum(1)
+    check(dw, f64(ref), f64(mag), H, "dweights")
+    for t0 in list(range(0, M, M // 3 + 1)) + [M - 1]:
+        part = slice(t0, min(t0 + 999, M))
+        few = torch.full_like(rows, 7)
+        few, dwf = moe.combine_grad(dy[part], rows, tp[part], w[part], few)
+        here = tp[part][tv[part]].long()
+        assert torch.equal(dwf, dw[part]) and torch.equal(few[here], drows[here])
+
+
 @pytest.mark.parametrize("M,k,E", [(1, 1, 1), (1, 8, 64), (7, 16, 512), (333, 3, 7), (5000, 8, 128), (64, 2, 65)])
 def test_route_grad(M, k, E):
     rng = np.random.default_rng([M, k, E])
