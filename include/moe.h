@@ -562,6 +562,8 @@ moe_status_t moe_swiglu_checkpoint_grad(const uint8_t* codes, const uint8_t* sca
  *    grouped row, or a negative number (or one >= R) where it has none.
  *  - Sums are in fp32 in an order fixed by the sizes, rounded once to the
  *    output's type: the same bits on every call.  No floating-point atomics.
+ *  - top_k may be larger than E, unlike in routing: ids may lie outside the
+ *    experts of a call, or be equal.
  *  - MOE_ERR_UNSUPPORTED: M*top_k >= 2^26, top_k > 16, E > 512, H not a
  *    multiple of 8 (dispatch: row_bytes not one of 16), a row stride of 2^22
  *    bytes or more.  MOE_ERR_INVALID_ARG: NULL or misaligned pointers (16
@@ -655,7 +657,7 @@ moe_status_t moe_combine_grad(const moe_combine_grad_args_t* args, void* stream)
  * Gradient of moe_route_topk's weights: with w = topk_weights[t], d =
  * dweights[t], dlogits[t, topk_ids[t,j]] = w_j (d_j - sum_i w_i d_i) and zero
  * for the other experts; dlogits fp32 [M,E].  Slots whose id is outside [0,E)
- * take no part.
+ * take no part; those of equal ids add up.
  */
 moe_status_t moe_route_topk_grad(const int32_t* topk_ids, const float* topk_weights, const float* dweights, int32_t M,
                                  int32_t E, int32_t top_k, float* dlogits, void* stream);

@@ -557,12 +557,15 @@ __global__ __launch_bounds__(kThreads) void combine_grad_narrow_kernel(CombineGr
 // ---------------------------------------------------------------- router
 // dlogits of a token: w_j (dw_j - sum_i w_i dw_i) at its selected experts, zero
 // at the others.  A wave per token: lane j holds slot j, every lane adds up the
-// slots that name its experts (equal ids add up).
+// slots that name its experts (equal ids add up).  All lanes go through the
+// experts together, and only the store is left out past the last one: a loop that
+// lanes leave would let the compiler form g for the lanes in it alone, where the
+// slots of the others are read too.
 __global__ __launch_bounds__(kThreads) void route_grad_kernel(const int32_t* __restrict__ ids,
                                                               const float* __restrict__ w,
                                                               const float* __restrict__ dw, int M, int E, int k,
                                                               float* __restrict__ dlogits) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   for (int t = blockIdx.x * 4 + wave; t < M; t += gridDim.x * 4) {
     const int64_t at = (int64_t)t * k + lane;
     const int id = lane < k ? ids[at] : -1;
@@ -570,14 +573,15 @@ __global__ __launch_bounds__(kThreads) void route_grad_kernel(const int32_t* __r
     const float wj = ok ? w[at] : 0.0f, dj = ok ? dw[at] : 0.0f;
     const float mean = wave_sum(wj * dj);
     const float g = wj * (dj - mean);
-    for (int e = lane; e < E; e += kWave) {
+    for (int e0 = 0; e0 < E; e0 += kWave) {
+      const int e = e0 + lane;
       float s = 0.0f;
       for (int j = 0; j < k; ++j) {
         const int ij = __builtin_amdgcn_readlane(id, j);
         const float gj = __uint_as_float((unsigned)__builtin_amdgcn_readlane((int)__float_as_uint(g), j));
         s += ij == e ? gj : 0.0f;
       }
-      dlogits[(int64_t)t * E + e] = s;
+      if (e < E) dlogits[(int64_t)t * E + e] = s;
     }
   }
 }

@@ -1,0 +1,31 @@
+"""Corners of the tokens' way to their experts and back: more slots than experts."""
+import numpy as np
+import pytest
+import torch
+
+import moe_layer_align_amd as moe
+from gpu_common import say
+from grouped_common import DEV
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("M,k,E", [(1, 2, 1), (5, 16, 1), (70, 16, 3), (9, 12, 7), (1000, 5, 4), (33, 16, 15),
+                                   (17, 16, 66), (12, 3, 130)])
+def test_route_grad_of_equal_ids(M, k, E):
+    """Slots that name the same expert, outnumber the experts or name none: their gradients add up."""
+    say("route_grad of equal ids M=%d k=%d E=%d" % (M, k, E))
+    rng = np.random.default_rng([M, k, E])
+    ids = rng.integers(-1, E + 1, (M, k)).astype(np.int32)
+    # multiples of 1/16 and whole numbers: w (d - mean) is a multiple of 1/256 below 2^6, exact in fp32 as are its sums
+    w = rng.integers(1, 9, (M, k)) / 16.0
+    d = rng.integers(-8, 9, (M, k)).astype(np.float64)
+    held = (ids >= 0) & (ids < E)
+    g = np.where(held, w * (d - (w * d * held).sum(1, keepdims=True)), 0.0)
+    want = np.zeros((M, E))
+    for t, j in zip(*np.nonzero(held)):
+        want[t, ids[t, j]] += g[t, j]
+    w[~held], d[~held] = np.nan, np.nan
+    got = moe.route_topk_grad(*(torch.from_numpy(v).to(t).to(DEV) for v, t in
+                                ((ids, torch.int32), (w, torch.float32), (d, torch.float32))), E)
+    assert np.array_equal(got.double().cpu().numpy(), want)
