@@ -576,7 +576,8 @@ moe_status_t moe_swiglu_checkpoint_grad(const uint8_t* codes, const uint8_t* sca
  * Dispatch: the tokens' rows copied to rows grouped by expert.  The experts
  * are first_expert .. first_expert+E-1 of those that the ids name; a pair whose
  * id is outside is left out (an expert of another process, a token of the
- * padding with id -1).
+ * padding with id -1); negative ids are nobody's, also where the range would go
+ * on behind 2^31.
  *   offsets   [E+1]      rows of expert first_expert+e: offsets[e] <= i < offsets[e+1]
  *   positions [M,top_k]  the pair's row, -1 for a pair left out
  *   pairs     [M*top_k]  the row's pair, -1 for rows at or beyond offsets[E]

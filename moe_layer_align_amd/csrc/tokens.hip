@@ -63,7 +63,7 @@ struct DispatchArgs {
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
 __device__ __forceinline__ bool local_expert(int id, int first, int E, int* e) {
-  *e = (int)((unsigned)id - (unsigned)first);  // ids below `first` wrap past E
+  *e = __builtin_elementwise_sub_sat(id, first);  // negative for every id below `first` (first >= 0)
   return (unsigned)*e < (unsigned)E;
 }
 

@@ -1,4 +1,4 @@
-"""Corners of the tokens' way to their experts and back: more slots than experts."""
+"""Corners of the tokens' way to their experts and back: more slots than experts, expert numbers at the end of int32."""
 import numpy as np
 import pytest
 import torch
@@ -6,6 +6,7 @@ import torch
 import moe_layer_align_amd as moe
 from gpu_common import say
 from grouped_common import DEV
+from test_gpu_tokens import layout
 
 pytestmark = pytest.mark.gpu
 
@@ -29,3 +30,18 @@ def test_route_grad_of_equal_ids(M, k, E):
     got = moe.route_topk_grad(*(torch.from_numpy(v).to(t).to(DEV) for v, t in
                                 ((ids, torch.int32), (w, torch.float32), (d, torch.float32))), E)
     assert np.array_equal(got.double().cpu().numpy(), want)
+
+
+@pytest.mark.parametrize("M", [40, 3000, 40000])  # the three ways of counting pairs
+@pytest.mark.parametrize("E,back", [(8, 4), (512, 1), (512, 511), (300, 300)])
+def test_dispatch_at_the_end_of_int32(M, E, back):
+    """No id is an expert's of a range that would go on behind 2^31, the lowest int32s among them."""
+    say("dispatch M=%d of E=%d experts from 2^31 - %d" % (M, E, back))
+    rng = np.random.default_rng([M, E, back])
+    first, lowest, highest = 2 ** 31 - back, -2 ** 31, 2 ** 31 - 1
+    near = [highest - rng.integers(0, 600, (M, 2)), lowest + rng.integers(0, 600, (M, 2)),
+            np.tile([highest, lowest], (M, 1)), rng.integers(-2, 600, (M, 2))]
+    ids = np.choose(rng.integers(0, 4, (M, 2)), near).astype(np.int32)
+    got = moe.dispatch(None, torch.from_numpy(ids).to(DEV), E, first_expert=first)[1:]
+    for t, want in zip(got, layout(ids, E, first)):
+        assert np.array_equal(t.cpu().numpy(), want)
