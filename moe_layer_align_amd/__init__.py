@@ -95,18 +95,11 @@ _lib = None
 _ABI = 15  # moe_abi_version() of the library whose moe_fused_args_t _FusedArgs mirrors
 
 
-def load():
-    """Load the built library (raises if it has not been built)."""
-    global _lib
-    if _lib is not None:
-        return _lib
-    if not os.path.exists(LIB_PATH):
-        raise RuntimeError("libmoe_mi355x.so is not built (run `python -c 'import __graft_entry__ as g; g.build()'`)")
-    lib = ctypes.CDLL(LIB_PATH)
+def _declare(lib):
+    """The functions' types; AttributeError for one that the library lacks."""
     vp, i32, i64, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
     lib.moe_status_string.restype = ctypes.c_char_p
     lib.moe_status_string.argtypes = [ctypes.c_int]
-    lib.moe_abi_version.restype = i32
     lib.moe_route_topk.restype = ctypes.c_int
     lib.moe_route_topk.argtypes = [vp, i32, i32, i32, vp, vp, vp]
     lib.moe_align_capacity.restype = sz
@@ -143,9 +136,24 @@ def load():
     lib.moe_dispatch_workspace_size.argtypes = [i32, i32, i32]
     lib.moe_grouped_int8_workspace_size.restype = sz
     lib.moe_grouped_int8_workspace_size.argtypes = [i32] * 5
-    if lib.moe_abi_version() != _ABI:
-        raise RuntimeError("libmoe_mi355x.so has ABI version %d, this binding expects %d: rebuild it"
-                           % (lib.moe_abi_version(), _ABI))
+
+
+def load():
+    """Load the built library (raises if it has not been built)."""
+    global _lib
+    if _lib is not None:
+        return _lib
+    if not os.path.exists(LIB_PATH):
+        raise RuntimeError("libmoe_mi355x.so is not built (run `python -c 'import __graft_entry__ as g; g.build()'`)")
+    lib = ctypes.CDLL(LIB_PATH)
+    try:
+        lib.moe_abi_version.restype = ctypes.c_int32
+        if lib.moe_abi_version() != _ABI:
+            raise RuntimeError("libmoe_mi355x.so has ABI version %d, this binding expects %d: rebuild it"
+                               % (lib.moe_abi_version(), _ABI))
+        _declare(lib)
+    except AttributeError as e:  # entry points are added without a new version
+        raise RuntimeError("libmoe_mi355x.so is older than this binding (%s): rebuild it" % e) from e
     _lib = lib
     return lib
 
