@@ -67,7 +67,9 @@ typedef enum {
 /* Human-readable name of a status code (static string, never NULL). */
 const char* moe_status_string(moe_status_t status);
 
-/* ABI version of this header; bumped on any incompatible change. */
+/* ABI version of this header, and of the library that is loaded; bumped on any
+ * incompatible change. */
+#define MOE_ABI_VERSION 15
 int32_t moe_abi_version(void);
 
 /*

@@ -698,8 +698,8 @@ def _compiled():
         try:
             native = importlib.import_module("._calls", __name__)
         except ImportError as e:
-            raise RuntimeError("the binding's compiled part is not built (run `python -c 'import __graft_entry__ as g; "
-                               "g.build()'`)") from e
+            raise RuntimeError("the binding's compiled part is not built, or not for this library (%s): run `python -c "
+                               "'import __graft_entry__ as g; g.build()'`" % e) from e
         native.init(_stream, _empty, MoEError, torch._C._cuda_getCurrentRawStream)
         _native = native
     return _native

@@ -490,10 +490,13 @@ PyObject* grouped_gemm_int8(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
-// _stream, _empty, MoEError, the current stream of a device index
+// _stream, _empty, MoEError, the current stream of a device index.  The argument
+// structs here are those of this version's header.
 PyObject* init(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   want(n, 4);
+  TORCH_CHECK(moe_abi_version() == MOE_ABI_VERSION, "libmoe_mi355x.so has ABI version ", moe_abi_version(),
+              ", the binding's compiled part is of version ", MOE_ABI_VERSION, ": rebuild them");
   PyObject** const at[4] = {&py_stream, &py_empty, &py_error, &py_current};
   for (int i = 0; i < 4; ++i) {
     Py_INCREF(a[i]);

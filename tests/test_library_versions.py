@@ -1,7 +1,10 @@
 """What the binding says of a library of another version (CPU only: stand-ins
 built with the host compiler in place of the library)."""
+import os
+import re
 import shutil
 import subprocess
+import sys
 
 import pytest
 
@@ -37,3 +40,31 @@ def test_load_names_a_library_of_another_version(monkeypatch, tmp_path, said, ve
     with pytest.raises(RuntimeError, match=said):
         moe.load()
     assert moe._lib is None
+
+
+CALLS = """
+import importlib.util, sys
+import torch
+spec = importlib.util.spec_from_file_location("_calls", sys.argv[1])
+try:
+    calls = importlib.util.module_from_spec(spec)
+    calls.init(None, None, None, None)
+    print("fits")
+except (ImportError, RuntimeError) as e:
+    print(type(e).__name__, e)
+"""
+
+
+@pytest.mark.parametrize("said,version,without", [
+    ("fits", 15, ()),
+    ("RuntimeError libmoe_mi355x.so has ABI version 14, the binding's compiled part is of version 15: rebuild", 14, ()),
+    ("ImportError.*undefined symbol: moe_", 15, NEW),
+])
+def test_the_compiled_part_compares_versions(tmp_path, said, version, without):
+    # beside another library than its own, in a process that holds neither
+    part = os.path.join(os.path.dirname(moe.LIB_PATH), "_calls.so")
+    shutil.copy(part, tmp_path / "_calls.so")
+    stand_in(tmp_path / os.path.basename(moe.LIB_PATH), version, without)
+    res = subprocess.run([sys.executable, "-c", CALLS, str(tmp_path / "_calls.so")], capture_output=True, text=True)
+    assert res.returncode == 0, res.stderr
+    assert re.search(said, res.stdout), res.stdout
