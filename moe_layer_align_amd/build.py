@@ -110,20 +110,31 @@ def _binding(verbose, tmpdir):
                 return
             out = res.stdout + res.stderr
         sys.stderr.write(out + "\n")
-        raise RuntimeError("the build of the binding's compiled part failed")
+        raise RuntimeError(_BINDING_FAILED)
     return finish
+
+
+_BINDING_FAILED = "the build of the binding's compiled part failed; the libraries are built"
 
 
 def build(verbose: bool = False, extra=()) -> str:
     """Build both libraries (all units compile in parallel) and the binding's
-    compiled part; returns the layer library's path."""
+    compiled part; returns the layer library's path.  The libraries are the C ABI
+    and need hipcc alone: where the compiled part cannot be built (no host
+    compiler, no torch), they are there when that is raised."""
     inc = ["-I", os.path.join(ROOT, "include"), "-I", CSRC]
     with tempfile.TemporaryDirectory(prefix="moe_build_") as tmpdir:
         layer = _compile_link(UNITS, LIB, inc, verbose, extra, tmpdir, "layer")
         probes = _compile_link(PROBE_UNITS, PROBE_LIB, inc, verbose, extra, tmpdir, "probes")
-        calls = _binding(verbose, tmpdir)
+        calls = missing = None
+        try:
+            calls = _binding(verbose, tmpdir)
+        except (ImportError, OSError) as e:
+            missing = e
         layer()
         probes()
+        if missing:
+            raise RuntimeError("%s (%s)" % (_BINDING_FAILED, missing)) from missing
         calls()
     return LIB
 
