@@ -733,13 +733,14 @@ def combine(rows: torch.Tensor, positions: torch.Tensor, weights: Optional[torch
 
 def combine_grad(dy: torch.Tensor, rows: Optional[torch.Tensor], positions: torch.Tensor,
                  weights: Optional[torch.Tensor] = None, drows: Optional[torch.Tensor] = None,
-                 dweights: Optional[torch.Tensor] = None, *, num_rows: Optional[int] = None, out_dtype=torch.bfloat16,
-                 stream=None):
+                 dweights: Optional[torch.Tensor] = None, *, num_rows: Optional[int] = None,
+                 out_dtype: Optional[torch.dtype] = torch.bfloat16, stream=None):
     """Gradient of combine from dy bf16 or fp32 [M,H] (moe_combine_grad): returns
     (drows, dweights fp32 [M,top_k]), drows[positions[t,j]] = weights[t,j] * dy[t]
     (rows that no position names are not written; made here as out_dtype, bf16 or
     fp32, when not given) and dweights[t,j] = dy[t] . rows[positions[t,j]].  rows
-    None: no dweights, num_rows (default M*top_k) rows of drows."""
+    None: no dweights, num_rows (default M*top_k) rows of drows.  drows and
+    out_dtype None: no drows, for a router that is trained alone (None in its place)."""
     return (_native or _compiled()).combine_grad(dy, rows, positions, weights, drows, dweights, num_rows, out_dtype,
                                                  stream)
 

@@ -324,12 +324,14 @@ PyObject* combine_grad(PyObject*, PyObject* const* a, Py_ssize_t n) {
     TORCH_CHECK_VALUE(c.R >= 0, "num_rows is negative");
   }
   Tensor drows, dweights;
-  ScalarType type;
+  const bool give = a[4] != Py_None || a[7] != Py_None;  // no drows given and none to be made: not wanted
+  TORCH_CHECK_VALUE(give || c.rows, "neither drows nor dweights: rows and out_dtype are both None");
+  ScalarType type = ScalarType::BFloat16;
   if (a[4] != Py_None) {
     drows = tensor(a[4], "drows");
     call.matrix(drows, "drows", kRowTypes, c.H, c.R);
     type = drows.scalar_type();
-  } else {
+  } else if (give) {
     type = dtype(a[7], "out_dtype");
   }
   c.drows_type = out_type(type, "out_dtype");
@@ -338,10 +340,12 @@ PyObject* combine_grad(PyObject*, PyObject* const* a, Py_ssize_t n) {
     call.need(dweights, "dweights", ScalarType::Float, {c.M, c.top_k});
   }
   call.begin();
-  if (!drows.defined()) drows = call.empty({c.R, c.H}, type);
-  const Matrix om = Call::place(drows);
-  c.drows = om.p;
-  c.drows_stride = om.stride;
+  if (give) {
+    if (!drows.defined()) drows = call.empty({c.R, c.H}, type);
+    const Matrix om = Call::place(drows);
+    c.drows = om.p;
+    c.drows_stride = om.stride;
+  }
   if (c.rows) {
     if (!dweights.defined()) dweights = call.empty({c.M, c.top_k}, ScalarType::Float);
     c.dweights = (float*)dweights.data_ptr();

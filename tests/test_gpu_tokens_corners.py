@@ -1,4 +1,5 @@
-"""Corners of the tokens' way to their experts and back: more slots than experts, expert numbers at the end of int32."""
+"""Corners of the tokens' way to their experts and back: more slots than experts, expert numbers at the end of int32,
+the weights' gradient alone."""
 import numpy as np
 import pytest
 import torch
@@ -6,7 +7,7 @@ import torch
 import moe_layer_align_amd as moe
 from gpu_common import say
 from grouped_common import DEV
-from test_gpu_tokens import layout
+from test_gpu_tokens import TYPES, combine_case, layout
 
 pytestmark = pytest.mark.gpu
 
@@ -45,3 +46,29 @@ def test_dispatch_at_the_end_of_int32(M, E, back):
     got = moe.dispatch(None, torch.from_numpy(ids).to(DEV), E, first_expert=first)[1:]
     for t, want in zip(got, layout(ids, E, first)):
         assert np.array_equal(t.cpu().numpy(), want)
+
+
+@pytest.mark.parametrize("M,k,E,H", [(1, 1, 1, 8), (600, 8, 8, 64), (50, 3, 8, 128), (33, 16, 16, 256), (77, 3, 7, 520),
+                                     (130, 6, 64, 1024), (130, 6, 64, 1032), (9, 2, 4, 14336), (20001, 2, 9, 1040)])
+@pytest.mark.parametrize("dy_type,rows_type", [("bf16", "bf16"), ("fp32", "bf16"), ("bf16", "fp32"), ("fp32", "fp32")])
+@pytest.mark.parametrize("weighted", [True, False])
+def test_gradient_of_the_weights_alone(M, k, E, H, dy_type, rows_type, weighted):
+    """What a router that is trained alone takes: the bits of the call that makes both gradients."""
+    say("dweights alone %s" % ((M, k, E, H, dy_type, rows_type, weighted),))
+    rng, rows, pos, valid, w = combine_case(M, k, E, H, rows_type, "bf16", weighted, 0.3, 2)
+    dy = torch.from_numpy(rng.standard_normal((M, H)).astype(np.float32)).to(TYPES[dy_type]).to(DEV)
+    rows, pos = rows.to(DEV), torch.from_numpy(pos).to(DEV)
+    w = None if w is None else torch.from_numpy(w).to(DEV)
+    _, want = moe.combine_grad(dy, rows, pos, w)
+    canvas = torch.full((M, k), 7.0, device=DEV)
+    none, dw = moe.combine_grad(dy, rows, pos, w, dweights=canvas, out_dtype=None)
+    assert none is None and dw.data_ptr() == canvas.data_ptr() and torch.equal(dw, want)
+    none, made = moe.combine_grad(dy, rows, pos, w, out_dtype=None)
+    assert none is None and torch.equal(made, want)
+
+
+def test_given_rows_take_the_gradient_whatever_out_dtype_is():
+    dy = torch.ones(3, 64, device=DEV)
+    pos = torch.arange(6, dtype=torch.int32, device=DEV).view(3, 2)
+    drows, _ = moe.combine_grad(dy, None, pos, None, torch.zeros(6, 64, device=DEV), out_dtype=None)
+    assert bool((drows == 1).all())
