@@ -634,7 +634,9 @@ moe_status_t moe_combine(const moe_combine_args_t* args, void* stream);
 /*
  * Gradient of moe_combine, from dy, the gradient of y:
  *   drows[positions[t,j]] = weights[t,j] * dy[t]; rows that no position names
- *   are not written (two equal positions leave either's result); NULL = not wanted
+ *   are not written (two equal positions leave either's result, 16 bytes of a
+ *   row at a time); NULL = not wanted.  Where no two positions are equal, drows
+ *   may be rows itself, with its type and stride
  *   dweights[t,j] = sum over the columns of dy[t] * rows[positions[t,j]], 0 for
  *   a slot without a row; NULL, with rows NULL, = not wanted
  */

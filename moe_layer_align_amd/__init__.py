@@ -739,8 +739,8 @@ def combine_grad(dy: torch.Tensor, rows: Optional[torch.Tensor], positions: torc
     (drows, dweights fp32 [M,top_k]), drows[positions[t,j]] = weights[t,j] * dy[t]
     (rows that no position names are not written; made here as out_dtype, bf16 or
     fp32, when not given) and dweights[t,j] = dy[t] . rows[positions[t,j]].  rows
-    None: no dweights, num_rows (default M*top_k) rows of drows.  drows and
-    out_dtype None: no drows, for a router that is trained alone (None in its place)."""
+    None: no dweights, num_rows (default M*top_k) rows of drows.  drows may be rows
+    itself where no two positions are equal.  drows and out_dtype None: no drows, for a router that is trained alone (None in its place)."""
     return (_native or _compiled()).combine_grad(dy, rows, positions, weights, drows, dweights, num_rows, out_dtype,
                                                  stream)
 

@@ -1,5 +1,5 @@
 """Corners of the tokens' way to their experts and back: more slots than experts, expert numbers at the end of int32,
-the weights' gradient alone."""
+the weights' gradient alone, gradients in the rows' place and past 32 bits."""
 import numpy as np
 import pytest
 import torch
@@ -72,3 +72,48 @@ def test_given_rows_take_the_gradient_whatever_out_dtype_is():
     pos = torch.arange(6, dtype=torch.int32, device=DEV).view(3, 2)
     drows, _ = moe.combine_grad(dy, None, pos, None, torch.zeros(6, 64, device=DEV), out_dtype=None)
     assert bool((drows == 1).all())
+
+
+@pytest.mark.parametrize("M,k,E,H", [(600, 8, 8, 64), (33, 16, 16, 256), (77, 3, 7, 520), (130, 6, 64, 1032),
+                                     (9, 2, 4, 14336), (20001, 2, 9, 1040)])
+@pytest.mark.parametrize("kind", ["bf16", "fp32"])
+def test_gradient_in_the_rows_place(M, k, E, H, kind):
+    say("drows in place of rows %s" % ((M, k, E, H, kind),))
+    rng, rows, pos, valid, w = combine_case(M, k, E, H, kind, kind, True, 0.3, 3)
+    dy = torch.from_numpy(rng.standard_normal((M, H)).astype(np.float32)).to(TYPES[kind]).to(DEV)
+    pos, w = torch.from_numpy(pos).to(DEV), torch.from_numpy(w).to(DEV)
+    wide = torch.full((M * k, H + 16), 7.0, dtype=TYPES[kind], device=DEV)
+    place = wide[:, 8:H + 8]
+    place.copy_(rows)
+    apart = place.clone()
+    want, want_dw = moe.combine_grad(dy, place, pos, w, apart)
+    drows, dw = moe.combine_grad(dy, place, pos, w, place)
+    assert drows.data_ptr() == place.data_ptr()
+    as_bytes = [t.contiguous().view(torch.uint8) for t in (place, want)]  # rows without a place hold NaN
+    assert torch.equal(*as_bytes) and torch.equal(dw, want_dw)
+    assert bool((wide[:, :8] == 7).all()) and bool((wide[:, H + 8:] == 7).all())
+
+
+@pytest.mark.parametrize("alone", [False, True])
+def test_weights_gradient_past_32_bits(alone):
+    """Rows of 5 GB and their gradient of 5 GB beside them: places past 2^31 and 2^32 bytes, in both."""
+    M, k, E, H = 40000, 8, 32, 8192
+    g = torch.Generator(device=DEV).manual_seed(6)
+    # whole numbers, each row's sum of products below 2^24: exact in fp32 in any order
+    dy = torch.randint(-4, 5, (M, H), generator=g, device=DEV, dtype=torch.int32).to(torch.bfloat16)
+    ids = torch.topk(torch.rand(M, E, generator=g, device=DEV), k, 1).indices.to(torch.int32)
+    rows, off, pos, pairs = moe.dispatch(dy, ids, E)
+    # each row times a factor of its own place, so that another row's would show
+    factor = (torch.arange(M * k, device=DEV) % 13 - 6).to(torch.bfloat16)
+    rows *= factor[:, None]
+    w = torch.rand(M, k, generator=g, device=DEV)
+    drows, dw = moe.combine_grad(dy, rows, pos, w, out_dtype=None if alone else torch.bfloat16)
+    square = dy.float().square().sum(1, keepdim=True)
+    assert float(square.max()) * 6 < 2 ** 24
+    assert torch.equal(dw, square * factor.float()[pos.long()])
+    if alone:
+        assert drows is None
+        return
+    for i in range(0, M * k, 40000):
+        f = pairs[i:i + 40000].long()
+        assert torch.equal(drows[i:i + 40000], (w.view(-1)[f, None] * dy[f // k].float()).to(torch.bfloat16))
