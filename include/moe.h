@@ -702,8 +702,9 @@ moe_status_t moe_swiglu_int8(const void* gu, int64_t gu_stride, const float* row
  * (one per row of the matrix that the ids choose from), or, with in_scale NULL,
  * bf16 rows, which the call turns to 8 bits itself, to the bits of
  * moe_quant_int8, in `workspace` (moe_grouped_int8_workspace_size bytes, 256-byte
- * aligned, for all in.rows rows; none for few rows and weights, whose codes are
- * made on the way into the product).  in.stride counts elements of their type.
+ * aligned, with room for in.rows rows; none for few rows and weights, whose codes
+ * are made on the way into the product): all in.rows rows where ids choose from
+ * them, otherwise those below offsets[E].  in.stride counts elements of their type.
  * The other conventions are the grouped products' (rows, offsets, ids, out,
  * errors); K is a multiple of 16 below 2^17 (bf16 rows: at most 2^16), N of 8, an
  * expert's matrix below 2^31 bytes, in.rows below 2^26.

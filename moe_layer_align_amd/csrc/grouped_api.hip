@@ -205,7 +205,11 @@ moe_status_t moe_grouped_gemm_int8(const moe_grouped_int8_args_t* a, void* strea
     if (a->workspace_bytes < need) return MOE_ERR_WORKSPACE_TOO_SMALL;
     uint8_t* const codes = (uint8_t*)a->workspace;
     float* const scales = (float*)(codes + int8_scales_at(a->in.rows, a->K));
-    launch_int8_rows<false>(Int8Args{g.in.p, a->in.stride, a->in.rows, a->K, nullptr, nullptr, codes, scales}, st);
+    // without ids the rows that experts hold alone: those behind them are not read
+    const bool whole = a->in.ids != nullptr;
+    launch_int8_rows<false>(Int8Args{g.in.p, a->in.stride, whole ? a->in.rows : a->R, a->K, nullptr,
+                                     whole ? nullptr : a->offsets + a->E, codes, scales},
+                            st);
     g.in.p = codes;
     g.in.stride = a->K;
     g.in_scale = scales;
