@@ -61,10 +61,12 @@ int32_t size32(int64_t v) {
   return (int32_t)v;
 }
 
+// numpy's integers and integer tensors of one element too
 int32_t integer(PyObject* o, const char* name) {
-  TORCH_CHECK_TYPE(PyLong_Check(o), name, " must be an integer");
+  TORCH_CHECK_TYPE(PyIndex_Check(o), name, " must be an integer");
+  const Ref i(PyNumber_Index(o));
   int over = 0;
-  const long long v = PyLong_AsLongLongAndOverflow(o, &over);
+  const long long v = PyLong_AsLongLongAndOverflow(i.p, &over);
   TORCH_CHECK_VALUE(!over, "a size, or a divisor, does not fit 32 bits");
   return size32(v);
 }
