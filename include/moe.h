@@ -673,8 +673,8 @@ moe_status_t moe_route_topk_grad(const int32_t* topk_ids, const float* topk_weig
  *
  * Rows to 8 bits, x [M,K] bf16 with a row stride in elements:
  *   top = max |x[i]|, scales[i] = top/127, codes[i,k] = 127*x[i,k]/top rounded
- *   to the nearest integer, ties to even (exactly: the quotient is not rounded
- *   before).  A row of zeros: scale 1.  A row that holds an infinity or a NaN:
+ *   to the nearest integer, ties to even (of bf16 rows exactly: the quotient is
+ *   not rounded before).  A row of zeros: scale 1.  A row that holds an infinity or a NaN:
  *   scale NaN, codes 0.
  * The same call lays out weights: a row of W is an output channel.
  * codes int8 [M,K], scales fp32 [M].  K a multiple of 16 and at most 2^16, M
@@ -685,8 +685,10 @@ moe_status_t moe_quant_int8(const void* x, int64_t x_stride, int32_t M, int32_t 
 
 /*
  * Gated activation to 8 bits: h = SiLU(g)*u of gu [R,2I] bf16 (columns [0,I)
- * gate, [I,2I) up; row stride gu_stride) in fp32, then rows to 8 bits as above;
- * scales[i] is multiplied by row_weight[i] (fp32 [R], NULL: ones), so that the
+ * gate, [I,2I) up; row stride gu_stride) in fp32, then rows to 8 bits as above,
+ * but from values that are rounded already: where the exact quotient lies as near
+ * to a tie as fp32 is exact, either of the two codes comes out (some 70 of 117
+ * million values), the same on every call.  scales[i] is multiplied by row_weight[i] (fp32 [R], NULL: ones), so that the
  * down product comes out weighted.  num_rows: device int32 or NULL; rows at or
  * beyond *num_rows are neither read nor written.  I a multiple of 16 and at
  * most 2^16, R below 2^26, gu_stride below 2^20.

@@ -44,8 +44,11 @@ __device__ __forceinline__ RowScale row_scale(unsigned bits) {
 
 // Sixteen values at v -> codes.  127 v/top to the nearest integer, ties to even:
 // for bf16 values 127 v is exact, and one correction of the quotient by its
-// exact remainder makes a tie, which fp32 holds, come out as one; other
-// quotients lie further from a tie (2^-9 of their size) than fp32's error.
+// exact remainder makes a tie, which fp32 holds, come out as one; the quotient of
+// mantissas b and a (128 to 255), 127 b/(a 2^e), lies otherwise at least 1/(254 b)
+// of its size from a tie, 2^-16, further than fp32's error of 2^-23.  The gated
+// activation's values are fp32: their 127 v is rounded, and a value within that
+// rounding of a tie may take either code.
 // Adding 1.5 * 2^23 rounds to an integer and leaves its low byte in front.
 __device__ __forceinline__ u32x4 int8_codes(const float (&v)[16], const RowScale& s) {
   u32x4 o;
