@@ -56,6 +56,15 @@ bool activation_sizes(int R, int I) {
 // Rows to 8-bit integers: M rows of K codes.
 bool int8_sizes(int M, int K) { return M < kMaxRows && K % kInt8Chunk == 0 && K <= kInt8MaxRow; }
 
+// Products of 8-bit integers, of codes or of bf16 rows.
+moe_status_t int8_product_sizes(int R, int E, int N, int K) {
+  if (R < 0 || E < 1 || N < 1 || K < 1) return MOE_ERR_INVALID_ARG;
+  if (R >= kMaxRows || E > kMaxExperts || N % 8 || K % kInt8Chunk || K >= kMaxInt8Sum ||
+      (int64_t)N * K >= kMaxExpertBytes)
+    return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
 size_t int8_scales_at(int rows, int K) { return ((size_t)rows * K + 255) / 256 * 256; }  // in the workspace
 
 RowsArg rows_arg(const moe_rows_t& r) { return RowsArg{(uint8_t*)r.data, r.stride, r.rows, r.div, r.ids}; }
@@ -176,23 +185,21 @@ moe_status_t moe_swiglu_int8(const void* gu, int64_t gu_stride, const float* row
 }
 
 size_t moe_grouped_int8_workspace_size(int32_t R, int32_t E, int32_t N, int32_t K, int32_t rows) {
-  if (R < 0 || E < 1 || N < 1 || K < 1 || rows < 0 || !int8_sizes(rows, K)) return 0;
+  if (int8_product_sizes(R, E, N, K) != MOE_OK || rows < 0 || !int8_sizes(rows, K)) return 0;
   return int8_rows_in_stream(R, E, N, K) ? 0 : int8_scales_at(rows, K) + (size_t)rows * 4;
 }
 
 moe_status_t moe_grouped_gemm_int8(const moe_grouped_int8_args_t* a, void* stream) {
   if (!a) return MOE_ERR_INVALID_ARG;
   const bool quantised = a->in_scale != nullptr;
-  if (a->R < 0 || a->E < 1 || a->N < 1 || a->K < 1 || !known_out(a->out_type)) return MOE_ERR_INVALID_ARG;
-  if (a->R >= kMaxRows || a->E > kMaxExperts || a->N % 8 || a->K % kInt8Chunk || a->K >= kMaxInt8Sum ||
-      (int64_t)a->N * a->K >= kMaxExpertBytes || a->in.rows >= kMaxRows || (!quantised && a->K > kInt8MaxRow))
-    return MOE_ERR_UNSUPPORTED;
+  moe_status_t rc = int8_product_sizes(a->R, a->E, a->N, a->K);
+  if (rc == MOE_ERR_INVALID_ARG || !known_out(a->out_type)) return MOE_ERR_INVALID_ARG;
+  if (rc != MOE_OK || a->in.rows >= kMaxRows || (!quantised && a->K > kInt8MaxRow)) return MOE_ERR_UNSUPPORTED;
   if (a->R == 0) return MOE_OK;
   if (!a->offsets || !aligned(a->offsets, 4) || !a->w || !aligned(a->w, 16) || !a->w_scale ||
       !aligned(a->w_scale, 16) || !aligned(a->in_scale, 4))
     return MOE_ERR_INVALID_ARG;
   const bool f32 = a->out_type == MOE_OUT_FP32;
-  moe_status_t rc;
   if ((rc = check_rows(a->in, a->R, a->K, quantised ? 1 : 2, true)) != MOE_OK) return rc;
   if ((rc = check_rows(a->out, a->R, a->N, f32 ? 4 : 2, false)) != MOE_OK) return rc;
   const hipStream_t st = (hipStream_t)stream;
