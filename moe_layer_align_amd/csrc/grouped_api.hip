@@ -35,7 +35,7 @@ moe_status_t check_rows(const moe_rows_t& r, int R, int width, int esz, bool inp
   if (!r.data || !aligned(r.data, 16) || !aligned(r.ids, 4) || r.rows < 0 || r.div < 1) return MOE_ERR_INVALID_ARG;
   if (!r.ids && (r.rows < R || r.div != 1)) return MOE_ERR_INVALID_ARG;
   if (!input && r.div != 1) return MOE_ERR_INVALID_ARG;
-  if (r.stride < width || r.stride * esz % 16) return MOE_ERR_INVALID_ARG;
+  if (r.stride < width || r.stride % 16 * esz % 16) return MOE_ERR_INVALID_ARG;
   if (r.stride >= kMaxStride) return MOE_ERR_UNSUPPORTED;
   if (input && r.ids && (int64_t)r.rows * r.stride * esz > kMaxGatherBytes) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;

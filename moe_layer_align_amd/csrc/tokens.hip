@@ -602,8 +602,8 @@ bool routed(int M, int k) { return (int64_t)M * k < kMaxPairs && k <= kMaxTopK; 
 
 // Rows of `width` elements of `esz` bytes, `stride` elements apart.
 moe_status_t check_matrix(const void* p, int64_t stride, int64_t width, int esz) {
-  if (!p || !aligned(p, 16) || stride < width || stride * esz % 16) return MOE_ERR_INVALID_ARG;
-  return stride * esz >= kMaxRowBytes ? MOE_ERR_UNSUPPORTED : MOE_OK;
+  if (!p || !aligned(p, 16) || stride < width || stride % 16 * esz % 16) return MOE_ERR_INVALID_ARG;
+  return stride >= kMaxRowBytes / esz ? MOE_ERR_UNSUPPORTED : MOE_OK;
 }
 
 bool known(moe_out_t t) { return t == MOE_OUT_BF16 || t == MOE_OUT_FP32; }
@@ -764,7 +764,7 @@ moe_status_t moe_combine_grad(const moe_combine_grad_args_t* a, void* stream) {
   c.dy_stride = a->dy_stride * size_of(a->dy_type);
   c.dy_f32 = a->dy_type == MOE_OUT_FP32;
   c.rows = (const uint8_t*)a->rows;
-  c.rows_stride = a->rows_stride * size_of(a->rows_type);
+  c.rows_stride = a->rows ? a->rows_stride * size_of(a->rows_type) : 0;
   c.R = a->R;
   c.positions = a->positions;
   c.weights = a->weights;
@@ -772,7 +772,7 @@ moe_status_t moe_combine_grad(const moe_combine_grad_args_t* a, void* stream) {
   c.k = a->top_k;
   c.H = a->H;
   c.drows = (uint8_t*)a->drows;
-  c.drows_stride = a->drows_stride * size_of(a->drows_type);
+  c.drows_stride = a->drows ? a->drows_stride * size_of(a->drows_type) : 0;
   c.drows_f32 = a->drows_type == MOE_OUT_FP32;
   c.dweights = a->dweights;
   const hipStream_t st = (hipStream_t)stream;
