@@ -1,6 +1,6 @@
 /*
- * Sanitizer driver for the host side of dispatch, combine, their gradients and
- * the products in 8-bit integers (include/moe.h): linked by
+ * Sanitizer driver for the host side of dispatch, combine, their gradients, the
+ * grouped products and their activations (include/moe.h): linked by
  * tests/test_sanitizers_tokens.py against a host-only build of their
  * translation units under AddressSanitizer and UndefinedBehaviorSanitizer.
  * It calls the size helpers over a sweep that holds the ends of int32, and
@@ -208,6 +208,48 @@ static void product(void) {
   CHECK(moe_grouped_gemm_int8(NULL, NULL) == MOE_ERR_INVALID_ARG);
 }
 
+static void bf16_base(moe_grouped_args_t* a) {
+  const moe_rows_t in = {FAKE, 128, 10, 1, NULL}, out = {FAKE, 64, 10, 1, NULL};
+  memset(a, 0, sizeof *a);
+  a->R = 10, a->E = 4, a->N = 64, a->K = 128;
+  a->offsets = FAKE, a->in = in, a->w = FAKE, a->out = out;
+}
+
+static void wgrad_base(moe_grouped_wgrad_args_t* a) {
+  const moe_rows_t dy = {FAKE, 64, 10, 1, NULL}, in = {FAKE, 128, 10, 1, NULL};
+  memset(a, 0, sizeof *a);
+  a->R = 10, a->E = 4, a->N = 64, a->K = 128;
+  a->offsets = FAKE, a->dy = dy, a->in = in, a->dw = FAKE;
+}
+
+static void bf16_products(void) {
+  {
+    moe_grouped_args_t a;
+    for (size_t i = 0; i < COUNT(kSizes); ++i)
+      if (kSizes[i] != 0) /* no rows: nothing to do */
+        CASE(bf16_base, moe_grouped_gemm, (a.out.data = NULL, a.R = kSizes[i]),
+             kSizes[i] >= 1 << 26 ? MOE_ERR_UNSUPPORTED : MOE_ERR_INVALID_ARG);
+    EACH(bf16_base, moe_grouped_gemm, a.out.data = NULL, E, kSizes)
+    EACH(bf16_base, moe_grouped_gemm, a.out.data = NULL, N, kSizes)
+    EACH(bf16_base, moe_grouped_gemm_dgrad, a.out.data = NULL, K, kSizes)
+    EACH(bf16_base, moe_grouped_gemm, (a.out.data = NULL, a.in.ids = FAKE), in.rows, kSizes)
+    EACH(bf16_base, moe_grouped_gemm, (a.out.data = NULL, a.in.ids = FAKE), in.div, kSizes)
+    EACH(bf16_base, moe_grouped_gemm, a.out.data = NULL, in.stride, kStrides)
+    for (size_t i = 0; i < COUNT(kStrides); ++i)
+      if (kStrides[i] < 64 || kStrides[i] % 4 || kStrides[i] >= 1 << 20)
+        CASE(bf16_base, moe_grouped_gemm, (a.out_type = MOE_OUT_FP32, a.out.stride = kStrides[i]),
+             kStrides[i] < 64 || kStrides[i] % 4 ? MOE_ERR_INVALID_ARG : MOE_ERR_UNSUPPORTED);
+  }
+  moe_grouped_wgrad_args_t a;
+#define LAST a.in.data = NULL
+  EACH(wgrad_base, moe_grouped_gemm_wgrad, LAST, R, kSizes)
+  EACH(wgrad_base, moe_grouped_gemm_wgrad, LAST, E, kSizes)
+  EACH(wgrad_base, moe_grouped_gemm_wgrad, LAST, N, kSizes)
+  EACH(wgrad_base, moe_grouped_gemm_wgrad, LAST, K, kSizes)
+  EACH(wgrad_base, moe_grouped_gemm_wgrad, LAST, dy.stride, kStrides)
+#undef LAST
+}
+
 static void vectors(void) {
   for (size_t i = 0; i < COUNT(kSizes); ++i) {
     const int32_t n = kSizes[i];
@@ -215,7 +257,11 @@ static void vectors(void) {
       CHECK(moe_route_topk_grad(FAKE, FAKE, FAKE, n, 8, 2, NULL, NULL) != MOE_OK);
       CHECK(moe_quant_int8(FAKE, 64, n, 64, FAKE, NULL, NULL) != MOE_OK);
       CHECK(moe_swiglu_int8(FAKE, 128, NULL, n, 64, NULL, FAKE, NULL, NULL) != MOE_OK);
+      CHECK(moe_swiglu_checkpoint(FAKE, 128, NULL, n, 64, NULL, NULL, NULL, NULL, NULL) != MOE_OK);
+      CHECK(moe_swiglu_checkpoint_grad(FAKE, FAKE, FAKE, NULL, n, 64, NULL, NULL, NULL, NULL, NULL) != MOE_OK);
     }
+    CHECK(moe_swiglu_checkpoint(FAKE, INT64_MAX, NULL, 4, n, NULL, NULL, NULL, NULL, NULL) != MOE_OK);
+    CHECK(moe_swiglu_checkpoint_grad(FAKE, FAKE, FAKE, NULL, 4, n, NULL, NULL, NULL, NULL, NULL) != MOE_OK);
     CHECK(moe_route_topk_grad(FAKE, FAKE, FAKE, 4, n, 2, NULL, NULL) != MOE_OK);
     CHECK(moe_route_topk_grad(FAKE, FAKE, FAKE, 4, 8, n, NULL, NULL) != MOE_OK);
     CHECK(moe_quant_int8(FAKE, INT64_MAX, 4, n, FAKE, NULL, NULL) != MOE_OK);
@@ -233,6 +279,7 @@ int main(void) {
   combine();
   grad();
   product();
+  bf16_products();
   vectors();
   if (failures) {
     fprintf(stderr, "%d checks failed\n", failures);

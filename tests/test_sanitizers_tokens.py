@@ -1,5 +1,5 @@
-"""CPU sanitizer job of dispatch, combine, their gradients and the products in
-8-bit integers (no GPU needed): the host side of their translation units, built
+"""CPU sanitizer job of dispatch, combine, their gradients, the grouped products and
+their activations (no GPU needed): the host side of their translation units, built
 as in test_sanitizers.py, driven by tests/sanitize/abi_tokens_driver.c through
 the size helpers and the refusals, with every size and stride at its ends."""
 import os
